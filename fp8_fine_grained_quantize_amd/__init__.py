@@ -23,6 +23,10 @@ __all__ = [
     "quantize_128x1_grouped", "token_group_slots", "grouped_wgrad_fp8_blockscaled", "gemm_fp8_blockscaled_q1x128",
     "workspace_bytes", "status_string", "abi_version", "EXPORTED_SYMBOLS", "empty_pitched", "as_pitched",
     "mfma_probe", "gemm_fp8_blockscaled_noalloc",
+    # the operators around the GEMMs (layer.py)
+    "layer_abi_version", "LAYER_SYMBOLS", "moe_sort", "moe_dispatch", "moe_dispatch_fp8", "moe_combine",
+    "moe_combine_backward", "ResidualNorm", "ResidualNormGrad", "residual_norm", "residual_norm_backward",
+    "GradTable", "grad_table", "grad_norm", "grad_clip", "clip_grad_norm",
 ]
 
 OP_N, OP_T = 0, 1
@@ -78,7 +82,7 @@ def lib() -> ctypes.CDLL:
             raise Fp8BlkError(f"{library_path} is missing: build it with "
                               "`python -m fp8_fine_grained_quantize_amd.build`")
         L = ctypes.CDLL(library_path)
-        for name, (res, args) in _SIGNATURES.items():
+        for name, (res, args) in (*_SIGNATURES.items(), *layer.SIGNATURES.items()):
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
@@ -371,3 +375,10 @@ def grouped_wgrad_fp8_blockscaled(offsets: torch.Tensor, T: int, AT, sA, BT, sB,
         (GEMM_POW2_SCALES if pow2_scales else 0) | ob, _ptr(C), C.stride(1), C.stride(0), _stream()),
         "grouped_wgrad_fp8_blockscaled")
     return C
+
+
+from . import layer  # noqa: E402  (it uses the helpers above)
+from .layer import (  # noqa: E402
+    LAYER_SYMBOLS, GradTable, ResidualNorm, ResidualNormGrad, clip_grad_norm, grad_clip, grad_norm, grad_table,
+    layer_abi_version, moe_combine, moe_combine_backward, moe_dispatch, moe_dispatch_fp8, moe_sort, residual_norm,
+    residual_norm_backward)

@@ -1,0 +1,247 @@
+// Global gradient norm over many tensors, and clipping by it (gfx950).
+//
+//   N = (sum over all elements g^2)^(1/2),   out = g min(1, max_norm / (N + eps)).
+//
+// Two passes over the gradients, both bound by HBM: no element can be scaled
+// before the last one is read.  All tensors are cut into chunks of kChunk
+// elements; a workgroup takes a contiguous run of chunks, finds the first
+// one's tensor in the table once and walks on from there.  Squares are summed
+// in FP64 (one conversion and one FMA per element, hidden behind the loads):
+// an FP32 sum of squares would overflow from gradients of 2^64 on and lose
+// those below 2^-63.  The partial sums are added in a fixed order, by every
+// workgroup of the second pass for itself, which saves a launch between.
+#include "../../include/libfp8blk_layer.h"
+#include "host_common.h"
+#include "layer_device.h"
+
+namespace fp8blk {
+
+constexpr int64_t kChunk = 8192;
+constexpr int kGradBlocks = 2048;  // most workgroups, one partial sum each
+static_assert(kGradBlocks * sizeof(double) <= FP8BLK_GRAD_WORKSPACE_BYTES, "partial sums fit the workspace");
+
+// One entry of the table; its chunks are [chunk0, the next entry's chunk0).
+struct GradEntry {
+  const void* src;
+  void* dst;
+  int64_t n, cols, ld, ldo;  // n = rows * cols elements
+  int64_t chunk0;
+  uint32_t flags;
+  uint32_t pitched;
+};
+static_assert(sizeof(GradEntry) == 64, "table entry");
+
+// The tensor that owns chunk c, found by the wave: 64 candidates at a time.
+// Every entry has at least one chunk, so chunk0 ascends strictly.
+__device__ __forceinline__ int64_t find_entry(const GradEntry* __restrict__ tab, int64_t n, int64_t c) {
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, len = n;  // the owner is in [lo, lo + len), tab[lo].chunk0 <= c
+  while (len > 1) {
+    const int64_t step = (len + 63) / 64;
+    const int64_t i = lo + lane * step;
+    const uint64_t le = __ballot(lane * step < len && tab[i].chunk0 <= c);
+    const int64_t last = 63 - __builtin_clzll(le);
+    lo += last * step;
+    len = min(step, len - last * step);
+  }
+  return lo;
+}
+
+// Element offset of a flat index: rows lie ld elements apart.
+__device__ __forceinline__ int64_t at(int64_t i, int64_t cols, int64_t ld) { return i / cols * ld + i % cols; }
+
+// Calls body(v, i, count) for the chunk's elements [lo, hi), `count` (at most
+// 8) of them in v from flat index i.
+template <typename T, typename F>
+__device__ __forceinline__ void each8(const GradEntry& e, int64_t lo, int64_t hi, F body) {
+  const T* src = reinterpret_cast<const T*>(e.src);
+  if (!e.pitched) {
+    for (int64_t i = lo + threadIdx.x * 8; i < hi; i += 256 * 8) {
+      Raw8<T> r;
+      load8(r, src + i, hi - i);
+      float v[8];
+      unpack8(r, v);
+      body(v, i, hi - i < 8 ? (int)(hi - i) : 8);
+    }
+  } else {
+    for (int64_t i = lo + threadIdx.x; i < hi; i += 256) {
+      float v[8] = {to_f32(src[at(i, e.cols, e.ld)])};
+      body(v, i, 1);
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void k_grad_squares(const GradEntry* __restrict__ tab, int64_t n, int64_t chunks,
+                                                       double* __restrict__ partial) {
+  __shared__ double red[4];
+  const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
+  int64_t t = find_entry(tab, n, c0);
+  double sum = 0.0;
+  for (int64_t c = c0; c < c1; ++c) {
+    while (t + 1 < n && tab[t + 1].chunk0 <= c) ++t;
+    const GradEntry e = tab[t];
+    const int64_t lo = (c - e.chunk0) * kChunk, hi = min(lo + kChunk, e.n);
+    auto add = [&](const float (&v)[8], int64_t, int) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = __builtin_fma((double)v[j], (double)v[j], sum);
+    };
+    if (e.flags & FP8BLK_GRAD_F32) each8<float>(e, lo, hi, add);
+    else each8<uint16_t>(e, lo, hi, add);
+  }
+  sum = wave_sum(sum);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) partial[blockIdx.x] = red[0] + red[1] + red[2] + red[3];
+}
+
+// The norm from the partial sums, the same bits in every workgroup of 256.
+__device__ __forceinline__ float norm_of(const double* __restrict__ partial, int np, double* red) {
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < np; i += 256) sum += partial[i];
+  sum = wave_sum(sum);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  return (float)sqrt(red[0] + red[1] + red[2] + red[3]);
+}
+
+__global__ __launch_bounds__(256) void k_grad_norm(const double* __restrict__ partial, int np,
+                                                    float* __restrict__ norm) {
+  __shared__ double red[4];
+  const float v = norm_of(partial, np, red);
+  if (threadIdx.x == 0) *norm = v;
+}
+
+template <typename TO>
+__device__ __forceinline__ void put8(const GradEntry& e, const float (&v)[8], float c, int64_t i, int count) {
+  TO* dst = reinterpret_cast<TO*>(e.dst);
+  if (!e.pitched) {
+    float o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = v[j] * c;
+    store8(dst + i, count, o);
+  } else {
+    dst[at(i, e.cols, e.ldo)] = from_f32<TO>(v[0] * c);
+  }
+}
+
+// given != NULL: the norm to clip by; otherwise it comes from the partial
+// sums and workgroup 0 writes it to *norm.
+__global__ __launch_bounds__(256) void k_grad_scale(const GradEntry* __restrict__ tab, int64_t n, int64_t chunks,
+                                                     const float* given, const double* __restrict__ partial, int np,
+                                                     float max_norm, float eps, float* norm) {
+  __shared__ double red[4];
+  float total;
+  if (given != nullptr) {
+    total = *given;
+  } else {
+    total = norm_of(partial, np, red);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+  }
+  float coef = max_norm / (total + eps);
+  coef = coef >= 1.0f ? 1.0f : coef;  // a NaN stays
+  const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
+  if (c0 >= c1) return;
+  int64_t t = find_entry(tab, n, c0);
+  for (int64_t c = c0; c < c1; ++c) {
+    while (t + 1 < n && tab[t + 1].chunk0 <= c) ++t;
+    const GradEntry e = tab[t];
+    if (coef == 1.0f && e.dst == e.src) continue;
+    const int64_t lo = (c - e.chunk0) * kChunk, hi = min(lo + kChunk, e.n);
+    auto scale = [&](const float (&v)[8], int64_t i, int count) {
+      if (e.flags & FP8BLK_GRAD_OUT_F32) put8<float>(e, v, coef, i, count);
+      else put8<uint16_t>(e, v, coef, i, count);
+    };
+    if (e.flags & FP8BLK_GRAD_F32) each8<float>(e, lo, hi, scale);
+    else each8<uint16_t>(e, lo, hi, scale);
+  }
+}
+
+inline unsigned grad_blocks(int64_t chunks) { return (unsigned)(chunks < kGradBlocks ? chunks : kGradBlocks); }
+
+inline bool table_ok(const void* table, int64_t n, int64_t chunks) {
+  if (n < 0 || chunks < n) return false;
+  return n == 0 ? chunks == 0 : table != nullptr && aligned(table, 8);
+}
+
+}  // namespace fp8blk
+
+using namespace fp8blk;
+
+extern "C" size_t fp8blk_grad_table_bytes(int64_t n) { return n > 0 ? (size_t)n * sizeof(GradEntry) : 0; }
+
+extern "C" fp8blk_status_t fp8blk_grad_table_build(const fp8blk_grad_t* list, int64_t n, void* table,
+                                                   size_t table_bytes, int64_t* chunks) {
+  if (n < 0 || chunks == nullptr) return FP8BLK_ERR_INVALID_ARG;
+  if (n > 0 && (list == nullptr || table == nullptr || !aligned(table, 8) || table_bytes < fp8blk_grad_table_bytes(n)))
+    return FP8BLK_ERR_INVALID_ARG;
+  int64_t next = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const fp8blk_grad_t& g = list[i];
+    const uintptr_t se = g.flags & FP8BLK_GRAD_F32 ? 4 : 2, de = g.flags & FP8BLK_GRAD_OUT_F32 ? 4 : 2;
+    if ((g.flags & ~(FP8BLK_GRAD_F32 | FP8BLK_GRAD_OUT_F32)) || g.reserved != 0) return FP8BLK_ERR_INVALID_ARG;
+    if (g.rows <= 0 || g.cols <= 0 || g.ld < g.cols || g.ldo < g.cols || g.rows > INT64_MAX / 16 / g.ld ||
+        g.rows > INT64_MAX / 16 / g.ldo)
+      return FP8BLK_ERR_INVALID_ARG;  // empty gradients have no place in the table
+    if (g.grad == nullptr || g.out == nullptr || !aligned(g.grad, se) || !aligned(g.out, de))
+      return FP8BLK_ERR_INVALID_ARG;
+    if (g.grad == g.out && (se != de || g.ld != g.ldo)) return FP8BLK_ERR_INVALID_ARG;
+    GradEntry e{};
+    e.src = g.grad;
+    e.dst = g.out;
+    e.n = g.rows * g.cols;
+    e.cols = g.cols;
+    e.ld = g.ld;
+    e.ldo = g.ldo;
+    e.chunk0 = next;
+    e.flags = g.flags;
+    e.pitched = g.rows > 1 && (g.ld != g.cols || g.ldo != g.cols);
+    next += ceil_div(e.n, kChunk);
+    reinterpret_cast<GradEntry*>(table)[i] = e;
+  }
+  *chunks = next;
+  return FP8BLK_OK;
+}
+
+extern "C" fp8blk_status_t fp8blk_grad_norm(const void* table, int64_t n, int64_t chunks, float* norm, void* workspace,
+                                            size_t workspace_bytes, void* stream) {
+  if (!table_ok(table, n, chunks) || norm == nullptr || !aligned(norm, 4)) return FP8BLK_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 8) || workspace_bytes < FP8BLK_GRAD_WORKSPACE_BYTES)
+    return FP8BLK_ERR_INVALID_ARG;
+  const unsigned nb = grad_blocks(chunks);
+  double* partial = reinterpret_cast<double*>(workspace);
+  if (nb > 0)
+    hipLaunchKernelGGL(k_grad_squares, dim3(nb), dim3(256), 0, as_stream(stream),
+                       reinterpret_cast<const GradEntry*>(table), n, chunks, partial);
+  hipLaunchKernelGGL(k_grad_norm, dim3(1), dim3(256), 0, as_stream(stream), partial, (int)nb, norm);
+  return launch_status();
+}
+
+extern "C" fp8blk_status_t fp8blk_grad_clip(const void* table, int64_t n, int64_t chunks, const float* norm,
+                                            float max_norm, float eps, void* stream) {
+  if (!table_ok(table, n, chunks) || norm == nullptr || !aligned(norm, 4) || !(max_norm >= 0.0f) || !(eps >= 0.0f))
+    return FP8BLK_ERR_INVALID_ARG;
+  if (n == 0) return FP8BLK_OK;
+  hipLaunchKernelGGL(k_grad_scale, dim3(grad_blocks(chunks)), dim3(256), 0, as_stream(stream),
+                     reinterpret_cast<const GradEntry*>(table), n, chunks, norm, nullptr, 0, max_norm, eps, nullptr);
+  return launch_status();
+}
+
+extern "C" fp8blk_status_t fp8blk_grad_clip_norm(const void* table, int64_t n, int64_t chunks, float max_norm,
+                                                 float eps, float* norm, void* workspace, size_t workspace_bytes,
+                                                 void* stream) {
+  if (!table_ok(table, n, chunks) || norm == nullptr || !aligned(norm, 4) || !(max_norm >= 0.0f) || !(eps >= 0.0f))
+    return FP8BLK_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 8) || workspace_bytes < FP8BLK_GRAD_WORKSPACE_BYTES)
+    return FP8BLK_ERR_INVALID_ARG;
+  if (n == 0) return fp8blk_grad_norm(table, n, chunks, norm, workspace, workspace_bytes, stream);
+  const unsigned nb = grad_blocks(chunks);
+  double* partial = reinterpret_cast<double*>(workspace);
+  hipLaunchKernelGGL(k_grad_squares, dim3(nb), dim3(256), 0, as_stream(stream),
+                     reinterpret_cast<const GradEntry*>(table), n, chunks, partial);
+  const fp8blk_status_t st = launch_status();
+  if (st != FP8BLK_OK) return st;
+  hipLaunchKernelGGL(k_grad_scale, dim3(nb), dim3(256), 0, as_stream(stream),
+                     reinterpret_cast<const GradEntry*>(table), n, chunks, nullptr, partial, (int)nb, max_norm, eps,
+                     norm);
+  return launch_status();
+}

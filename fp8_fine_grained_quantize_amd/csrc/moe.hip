@@ -1,0 +1,513 @@
+// Tokens into expert order and back, and the gradients (gfx950).
+//
+// The grouped GEMMs take rows ordered by expert with device-resident offsets;
+// each token goes to K experts [p5¶3] and MoE activations are quantized before
+// they are dispatched [p2¶4].  Citations [pN¶k]: N-th page of the source
+// collection, k-th paragraph (p2 = inprokorea.com wr_id 735329, p5 =
+// inprokorea.com wr_id 890463).
+//
+// With the rows of a permutation r(t, k) of the pairs:
+//   dispatch  out[r(t, k)] = x[t]
+//   combine   y[t] = sum_k w(t, k) rows[r(t, k)]
+// and, as the two are each other's transpose, the gradient of dispatch is the
+// combine with w = 1, that of the combine the dispatch of w dy, and
+// dw(t, k) = <dy[t], rows[r(t, k)]>.  All of them move memory and compute next
+// to nothing: HBM bounds them.
+#include "../../include/libfp8blk_layer.h"
+#include "host_common.h"
+#include "layer_device.h"
+#include "token_groups.h"
+
+namespace fp8blk {
+
+// ---------------------------------------------------------------------------
+// Sort by expert: a stable counting sort.  The rank of a pair is
+//   off[e] + (pairs of e before its workgroup) + (before its wave) + (before it
+//   in its wave),
+// the last from a wave-wide match of equal keys by ballots over the key's
+// bits, so the order is the pairs' own and nothing depends on timing.  Up to
+// kSortOne pairs one workgroup does it all; above, k_moe_count first counts
+// each workgroup's segment and every workgroup of k_moe_sort then sums the
+// counts before it.  Dropped pairs form the last bucket, key E.
+// ---------------------------------------------------------------------------
+constexpr int kMaxExperts = 960;       // 16 waves' counts stay within 64 KB of LDS
+constexpr int64_t kSortOne = 4096;     // pairs that one workgroup sorts
+constexpr int64_t kSortBlocks = 256;   // most workgroups of the two-launch sort
+constexpr int kSortWaves = 16;
+
+template <typename ID>
+__device__ __forceinline__ int sort_key(const ID* __restrict__ ids, int64_t ld, uint32_t K, uint32_t p, int E) {
+  const int64_t i = ld == (int64_t)K ? (int64_t)p : (int64_t)(p / K) * ld + p % K;
+  const ID v = ids[i];
+  return v >= 0 && v < (ID)E ? (int)v : E;
+}
+
+template <typename ID>
+__global__ __launch_bounds__(1024) void k_moe_count(const ID* __restrict__ ids, int64_t ld, uint32_t K, uint32_t P,
+                                                     int E, uint32_t per_block, int32_t* __restrict__ hist) {
+  extern __shared__ int32_t lds[];
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) lds[e] = 0;
+  __syncthreads();
+  const uint32_t p0 = blockIdx.x * per_block;
+  const uint32_t p1 = min(p0 + per_block, P);
+  for (uint32_t p = p0 + threadIdx.x; p < p1; p += blockDim.x) atomicAdd(&lds[sort_key(ids, ld, K, p, E)], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) hist[(int64_t)blockIdx.x * E + e] = lds[e];
+}
+
+// nb workgroups of nw waves; each wave takes per_wave (a multiple of 64)
+// consecutive pairs.  LDS: cnt[nw][E+1] and scan[2][nw].  blockDim >= E.
+template <typename ID>
+__global__ __launch_bounds__(1024) void k_moe_sort(const ID* __restrict__ ids, int64_t ld, uint32_t K, uint32_t P,
+                                                    int E, int nbits, uint32_t per_wave,
+                                                    const int32_t* __restrict__ hist, int32_t* __restrict__ offsets,
+                                                    int32_t* __restrict__ row_of, int32_t* __restrict__ slot_of) {
+  extern __shared__ int32_t lds[];
+  const int nw = blockDim.x >> 6;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int EB = E + 1;
+  int32_t* cnt = lds;                    // [nw][E+1]
+  int32_t* scan = lds + nw * EB;         // [2][nw]
+  const uint32_t b0 = blockIdx.x * per_wave * nw;
+  const uint32_t w0 = min(b0 + wave * per_wave, P);
+  const uint32_t w1 = min(w0 + per_wave, P);
+
+  for (int i = threadIdx.x; i < nw * EB; i += blockDim.x) cnt[i] = 0;
+  __syncthreads();
+  for (uint32_t p = w0 + lane; p < w1; p += 64) atomicAdd(&cnt[wave * EB + sort_key(ids, ld, K, p, E)], 1);
+  __syncthreads();
+
+  // Thread e: expert e's pairs in all workgroups, and in those before this one.
+  const int e = threadIdx.x;
+  int32_t total = 0, before = 0;
+  if (e < E) {
+    if (hist == nullptr) {
+      for (int w = 0; w < nw; ++w) total += cnt[w * EB + e];
+    } else {
+      for (uint32_t b = 0; b < gridDim.x; ++b) {
+        const int32_t h = hist[(int64_t)b * E + e];
+        total += h;
+        before += b < blockIdx.x ? h : 0;
+      }
+    }
+  }
+  const int32_t incl = wave_inclusive_sum(total), incl_before = wave_inclusive_sum(before);
+  if (lane == 63) {
+    scan[wave] = incl;
+    scan[nw + wave] = incl_before;
+  }
+  __syncthreads();
+  int32_t off = incl - total, kept = 0, kept_before = 0;
+  for (int w = 0; w < nw; ++w) {
+    off += w < wave ? scan[w] : 0;
+    kept += scan[w];
+    kept_before += scan[nw + w];
+  }
+  if (blockIdx.x == 0) {
+    if (e < E) offsets[e] = off;
+    if (threadIdx.x == 0) offsets[E] = kept;
+  }
+  // The row at which each wave's pairs of each key start.
+  if (e < E) {
+    int32_t run = off + before;
+    for (int w = 0; w < nw; ++w) {
+      const int32_t c = cnt[w * EB + e];
+      cnt[w * EB + e] = run;
+      run += c;
+    }
+  }
+  if (threadIdx.x == 0) {
+    int32_t run = kept + (int32_t)min(b0, P) - kept_before;
+    for (int w = 0; w < nw; ++w) {
+      const int32_t c = cnt[w * EB + E];
+      cnt[w * EB + E] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+
+  for (uint32_t p0 = w0; p0 < w1; p0 += 64) {
+    const uint32_t p = p0 + lane;
+    const bool valid = p < w1;
+    const int key = valid ? sort_key(ids, ld, K, p, E) : E;
+    uint64_t same = __ballot(valid);
+    for (int b = 0; b < nbits; ++b) {
+      const bool bit = (key >> b) & 1;
+      const uint64_t set = __ballot(bit);
+      same &= bit ? set : ~set;
+    }
+    const int lower = __popcll(same & ((1ull << lane) - 1));
+    const int32_t row = cnt[wave * EB + key] + lower;
+    __builtin_amdgcn_wave_barrier();  // every lane has read before the leaders advance
+    if (valid && lower == 0) cnt[wave * EB + key] += __popcll(same);
+    __builtin_amdgcn_wave_barrier();
+    if (valid) {
+      row_of[p] = key < E ? row : -1 - row;
+      slot_of[row] = key < E ? (int32_t)p : -1 - (int32_t)p;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Dispatch: a workgroup takes one token and a segment of its row, reads each
+// 16-byte chunk once and writes it to the K rows of the token's experts.  The
+// 1x128 scales lie [group][row], so they are gathered instead, by workgroups
+// of their own at the end of the grid: 256 consecutive rows x kScaleGroups
+// groups, written coalesced (the scales of all tokens stay in L2).
+// UNIT: bytes of an element, the granularity of a row's end.
+// ---------------------------------------------------------------------------
+constexpr int kScaleGroups = 8;
+
+template <int UNIT>
+__device__ __forceinline__ uint4 load_part(const uint8_t* p, int64_t avail) {
+  if (avail >= 16) return *reinterpret_cast<const uint4*>(p);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 16; j += UNIT)
+    if (j < avail) {
+      const uint32_t v = UNIT == 2 ? *reinterpret_cast<const uint16_t*>(p + j) : p[j];
+      w[j >> 2] |= v << ((j & 3) * 8);
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int UNIT>
+__device__ __forceinline__ void store_part(uint8_t* p, int64_t avail, const uint4& v) {
+  if (avail >= 16) {
+    *reinterpret_cast<uint4*>(p) = v;
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 16; j += UNIT)
+    if (j < avail) {
+      if (UNIT == 2)
+        *reinterpret_cast<uint16_t*>(p + j) = (uint16_t)(w[j >> 2] >> ((j & 3) * 8));
+      else
+        p[j] = (uint8_t)(w[j >> 2] >> ((j & 3) * 8));
+    }
+}
+
+template <int UNIT, bool SCALES>
+__global__ __launch_bounds__(256) void k_moe_dispatch(const uint8_t* __restrict__ x, int64_t ldx, int64_t row_bytes,
+                                                       int64_t T, uint32_t K, const int32_t* __restrict__ row_of,
+                                                       uint8_t* __restrict__ out, int64_t ldo, uint32_t segs,
+                                                       const float* __restrict__ s, int64_t G,
+                                                       const int32_t* __restrict__ slot_of, float* __restrict__ sr) {
+  const int64_t P = T * K;
+  const int64_t copies = T * segs;
+  if (!SCALES || (int64_t)blockIdx.x < copies) {
+    const int64_t t = blockIdx.x / segs;
+    const int64_t col = ((int64_t)(blockIdx.x % segs) * blockDim.x + threadIdx.x) * 16;
+    const int64_t avail = row_bytes - col;
+    if (avail <= 0) return;
+    const uint4 v = load_part<UNIT>(x + t * ldx + col, avail);
+    for (uint32_t k = 0; k < K; ++k) {
+      const int32_t r = row_of[t * K + k];
+      const int64_t row = r < 0 ? -1 - (int64_t)r : (int64_t)r;
+      if (row < P) store_part<UNIT>(out + row * ldo + col, avail, r < 0 ? make_uint4(0u, 0u, 0u, 0u) : v);
+    }
+    return;
+  }
+  const int64_t b = (int64_t)blockIdx.x - copies;
+  const int64_t row_blocks = (P + 255) / 256;
+  const int64_t r = (b % row_blocks) * 256 + threadIdx.x;
+  const int64_t g0 = b / row_blocks * kScaleGroups;
+  if (r >= P) return;
+  const int32_t p = slot_of[r];
+  const int64_t t = p < 0 ? -1 : (int64_t)((uint32_t)p / K);
+#pragma unroll
+  for (int i = 0; i < kScaleGroups; ++i) {
+    if (g0 + i < G) sr[(g0 + i) * P + r] = t < 0 || t >= T ? 1.0f : s[(g0 + i) * T + t];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Combine: a workgroup takes one token and a segment of the row; a lane sums
+// eight channels over the token's rows in FP32, k ascending, loads of eight
+// rows in flight.
+// ---------------------------------------------------------------------------
+template <typename TR, typename TY, bool WEIGHTED>
+__global__ __launch_bounds__(256) void k_moe_combine(const TR* __restrict__ rows, int64_t ldr, int64_t C, int64_t T,
+                                                      uint32_t K, const int32_t* __restrict__ row_of,
+                                                      const float* __restrict__ w, TY* __restrict__ y, int64_t ldy,
+                                                      uint32_t segs) {
+  const int64_t P = T * K;
+  const int64_t t = blockIdx.x / segs;
+  const int64_t col = ((int64_t)(blockIdx.x % segs) * blockDim.x + threadIdx.x) * 8;
+  const int64_t avail = C - col;
+  if (avail <= 0) return;
+  float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  for (uint32_t k0 = 0; k0 < K; k0 += 8) {
+    Raw8<TR> v[8];
+    bool on[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t k = k0 + j;
+      const int64_t r = k < K ? row_of[t * K + k] : -1;
+      on[j] = r >= 0 && r < P;
+      if (on[j]) load8(v[j], rows + r * ldr + col, avail);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!on[j]) continue;
+      const float wk = WEIGHTED ? w[t * K + k0 + j] : 1.0f;
+      float x[8];
+      unpack8(v[j], x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = WEIGHTED ? __builtin_fmaf(wk, x[i], acc[i]) : acc[i] + x[i];
+    }
+  }
+  store8(y + t * ldy + col, avail, acc);
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the combine: a workgroup takes one token, reads dy once, and for
+// eight experts at a time reads their rows, adds up the eight dot products
+// (FP32, lane by lane over the channels, then across lanes) and writes the
+// eight scaled copies of dy.
+// ---------------------------------------------------------------------------
+template <typename TY, typename TR, typename TD>
+__global__ __launch_bounds__(256) void k_moe_combine_backward(const TY* __restrict__ dy, int64_t lddy,
+                                                               const TR* __restrict__ rows, int64_t ldr, int64_t T,
+                                                               uint32_t K, int64_t C,
+                                                               const int32_t* __restrict__ row_of,
+                                                               const float* __restrict__ w, TD* __restrict__ drows,
+                                                               int64_t lddr, float* __restrict__ dw) {
+  __shared__ float red[2][4 * 8];
+  const int64_t P = T * K;
+  const int64_t t = blockIdx.x;
+  const int nw = blockDim.x >> 6;
+  int turn = 0;
+  for (uint32_t k0 = 0; k0 < K; k0 += 8) {
+    float dot[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t col = (int64_t)threadIdx.x * 8; col < C; col += (int64_t)blockDim.x * 8) {
+      const int64_t avail = C - col;
+      Raw8<TY> raw;
+      load8(raw, dy + t * lddy + col, avail);
+      float d[8];
+      unpack8(raw, d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t k = k0 + j;
+        if (k >= K) continue;
+        const int32_t r = row_of[t * K + k];
+        const int64_t row = r < 0 ? -1 - (int64_t)r : (int64_t)r;
+        if (row >= P) continue;
+        const float wk = w[t * K + k];
+        float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (r >= 0) {
+          Raw8<TR> v;
+          load8(v, rows + row * ldr + col, avail);
+          float x[8];
+          unpack8(v, x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dot[j] = __builtin_fmaf(d[i], x[i], dot[j]);
+            o[i] = wk * d[i];
+          }
+        }
+        store8(drows + row * lddr + col, avail, o);
+      }
+    }
+    block_sum<8>(dot, red[turn], nw);
+    turn ^= 1;
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (k0 + j < K) dw[t * K + k0 + j] = dot[j];
+    }
+  }
+}
+
+// Workgroups per row and lanes per workgroup (a multiple of 64, at most 256)
+// so that the row's chunks fill the lanes evenly.
+struct RowSplit {
+  uint32_t segs, lanes;
+};
+inline RowSplit split_row(int64_t chunks) {
+  RowSplit r;
+  if (chunks < 1) chunks = 1;
+  r.segs = (uint32_t)ceil_div(chunks, (int64_t)256);
+  r.lanes = (uint32_t)(ceil_div(ceil_div(chunks, (int64_t)r.segs), (int64_t)64) * 64);
+  return r;
+}
+
+constexpr int64_t kMaxPairs = 0x7FFFFFFF - (1 << 20);
+
+// A launch counts its lanes in 32 bits.
+inline bool grid_ok(int64_t blocks, int64_t lanes) { return blocks <= 0xFFFFFFFFll / lanes && blocks <= 0x7FFFFFFF; }
+
+// Sizes of a token matrix with K rows per token: FP8BLK_OK where they can be
+// worked on.
+inline fp8blk_status_t pairs_ok(int64_t T, int64_t K, int64_t C) {
+  if (T < 0 || K < 0 || C < 0) return FP8BLK_ERR_INVALID_ARG;
+  if (K > 0 && T > kMaxPairs / K) return FP8BLK_ERR_UNSUPPORTED;
+  return FP8BLK_OK;
+}
+
+inline int64_t sort_per_wave(int64_t P) {
+  return ceil_div(ceil_div(P, kSortBlocks * kSortWaves), (int64_t)64) * 64;
+}
+
+template <typename ID>
+fp8blk_status_t launch_sort(const ID* ids, int64_t ld, uint32_t K, int64_t P, int E, int32_t* offsets, int32_t* row_of,
+                            int32_t* slot_of, int32_t* hist, hipStream_t stream) {
+  int nbits = 0;
+  while ((E >> nbits) != 0) ++nbits;
+  if (P <= kSortOne) {
+    int64_t nw = ceil_div(P, (int64_t)64);
+    if (nw > kSortWaves) nw = kSortWaves;
+    if (nw < ceil_div((int64_t)E, (int64_t)64)) nw = ceil_div((int64_t)E, (int64_t)64);
+    if (nw < 1) nw = 1;
+    const uint32_t per_wave = (uint32_t)(ceil_div(ceil_div(P, nw), (int64_t)64) * 64);
+    const size_t lds = (size_t)(nw * (E + 1) + 2 * nw) * 4;
+    hipLaunchKernelGGL(k_moe_sort<ID>, dim3(1), dim3((unsigned)nw * 64), lds, stream, ids, ld, K, (uint32_t)P, E, nbits,
+                       per_wave, nullptr, offsets, row_of, slot_of);
+    return launch_status();
+  }
+  const uint32_t per_wave = (uint32_t)sort_per_wave(P), per_block = per_wave * kSortWaves;
+  const unsigned nb = (unsigned)ceil_div(P, (int64_t)per_block);
+  hipLaunchKernelGGL(k_moe_count<ID>, dim3(nb), dim3(1024), (size_t)(E + 1) * 4, stream, ids, ld, K, (uint32_t)P, E,
+                     per_block, hist);
+  const fp8blk_status_t st = launch_status();
+  if (st != FP8BLK_OK) return st;
+  const size_t lds = (size_t)(kSortWaves * (E + 1) + 2 * kSortWaves) * 4;
+  hipLaunchKernelGGL(k_moe_sort<ID>, dim3(nb), dim3(kSortWaves * 64), lds, stream, ids, ld, K, (uint32_t)P, E, nbits,
+                     per_wave, hist, offsets, row_of, slot_of);
+  return launch_status();
+}
+
+template <typename TR, typename TY>
+void launch_combine(const void* rows, int64_t ldr, int64_t C, int64_t T, uint32_t K, const int32_t* row_of,
+                    const float* w, void* y, int64_t ldy, hipStream_t stream) {
+  const RowSplit sp = split_row(ceil_div(C, (int64_t)8));
+  const dim3 grid((unsigned)(T * sp.segs)), block(sp.lanes);
+  if (w != nullptr)
+    hipLaunchKernelGGL((k_moe_combine<TR, TY, true>), grid, block, 0, stream, reinterpret_cast<const TR*>(rows), ldr, C,
+                       T, K, row_of, w, reinterpret_cast<TY*>(y), ldy, sp.segs);
+  else
+    hipLaunchKernelGGL((k_moe_combine<TR, TY, false>), grid, block, 0, stream, reinterpret_cast<const TR*>(rows), ldr, C,
+                       T, K, row_of, w, reinterpret_cast<TY*>(y), ldy, sp.segs);
+}
+
+template <typename TY, typename TR, typename TD>
+void launch_combine_backward(const void* dy, int64_t lddy, const void* rows, int64_t ldr, int64_t T, uint32_t K,
+                             int64_t C, const int32_t* row_of, const float* w, void* drows, int64_t lddr, float* dw,
+                             hipStream_t stream) {
+  const RowSplit sp = split_row(ceil_div(C, (int64_t)8));
+  hipLaunchKernelGGL((k_moe_combine_backward<TY, TR, TD>), dim3((unsigned)T), dim3(sp.lanes), 0, stream,
+                     reinterpret_cast<const TY*>(dy), lddy, reinterpret_cast<const TR*>(rows), ldr, T, K, C, row_of, w,
+                     reinterpret_cast<TD*>(drows), lddr, dw);
+}
+
+}  // namespace fp8blk
+
+using namespace fp8blk;
+
+extern "C" int fp8blk_layer_abi_version(void) { return 1; }
+
+extern "C" size_t fp8blk_moe_sort_workspace_bytes(int64_t T, int64_t K, int64_t E) {
+  if (pairs_ok(T, K, 0) != FP8BLK_OK || E < 0 || E > kMaxExperts || T * K <= kSortOne) return 0;
+  return (size_t)(ceil_div(T * K, sort_per_wave(T * K) * kSortWaves) * E) * 4;
+}
+
+extern "C" fp8blk_status_t fp8blk_moe_sort(const void* expert_ids, int64_t T, int64_t K, int64_t ld, int64_t E,
+                                           int32_t* offsets, int32_t* row_of, int32_t* slot_of, void* workspace,
+                                           size_t workspace_bytes, uint32_t flags, void* stream) {
+  if ((flags & ~FP8BLK_MOE_IDS_I64) || E < 0) return FP8BLK_ERR_INVALID_ARG;
+  const fp8blk_status_t st = pairs_ok(T, K, 0);
+  if (st != FP8BLK_OK) return st;
+  if (E > kMaxExperts) return FP8BLK_ERR_UNSUPPORTED;
+  const bool i64 = (flags & FP8BLK_MOE_IDS_I64) != 0;
+  const int64_t P = T * K;
+  if (!vec_ok(offsets, E + 1)) return FP8BLK_ERR_INVALID_ARG;
+  if (P > 0 && (ld < K || !vec_ok(expert_ids, P, i64 ? 8 : 4) || !vec_ok(row_of, P) || !vec_ok(slot_of, P)))
+    return FP8BLK_ERR_INVALID_ARG;
+  const size_t need = fp8blk_moe_sort_workspace_bytes(T, K, E);
+  if (need != 0 && (workspace == nullptr || !aligned(workspace, 4) || workspace_bytes < need))
+    return FP8BLK_ERR_INVALID_ARG;
+  if (i64)
+    return launch_sort(reinterpret_cast<const int64_t*>(expert_ids), ld, (uint32_t)K, P, (int)E, offsets, row_of,
+                       slot_of, reinterpret_cast<int32_t*>(workspace), as_stream(stream));
+  return launch_sort(reinterpret_cast<const int32_t*>(expert_ids), ld, (uint32_t)K, P, (int)E, offsets, row_of, slot_of,
+                     reinterpret_cast<int32_t*>(workspace), as_stream(stream));
+}
+
+extern "C" fp8blk_status_t fp8blk_moe_dispatch(const uint16_t* x, int64_t T, int64_t C, int64_t ldx, int64_t K,
+                                               const int32_t* row_of, uint16_t* out, int64_t ldo, void* stream) {
+  const fp8blk_status_t st = pairs_ok(T, K, C);
+  if (st != FP8BLK_OK) return st;
+  if (T == 0 || K == 0 || C == 0) return FP8BLK_OK;
+  if (!matrix_ok(x, T, C, ldx, 2) || !matrix_ok(out, T * K, C, ldo, 2) || !vec_ok(row_of, T * K))
+    return FP8BLK_ERR_INVALID_ARG;
+  const RowSplit sp = split_row(ceil_div(2 * C, (int64_t)16));
+  if (!grid_ok(T * sp.segs, sp.lanes)) return FP8BLK_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL((k_moe_dispatch<2, false>), dim3((unsigned)(T * sp.segs)), dim3(sp.lanes), 0, as_stream(stream),
+                     reinterpret_cast<const uint8_t*>(x), 2 * ldx, 2 * C, T, (uint32_t)K, row_of,
+                     reinterpret_cast<uint8_t*>(out), 2 * ldo, sp.segs, nullptr, (int64_t)0, nullptr, nullptr);
+  return launch_status();
+}
+
+extern "C" fp8blk_status_t fp8blk_moe_dispatch_fp8(const uint8_t* q, int64_t T, int64_t C, int64_t ldq, const float* s,
+                                                   int64_t K, const int32_t* row_of, const int32_t* slot_of,
+                                                   uint8_t* qr, int64_t ldqr, float* sr, void* stream) {
+  const fp8blk_status_t st = pairs_ok(T, K, C);
+  if (st != FP8BLK_OK) return st;
+  if (T == 0 || K == 0 || C == 0) return FP8BLK_OK;
+  const int64_t G = ceil_div(C, (int64_t)128), P = T * K;
+  if (!matrix_ok(q, T, C, ldq, 1) || !matrix_ok(qr, P, C, ldqr, 1) || !vec_ok(s, T) || !vec_ok(sr, P) ||
+      !vec_ok(row_of, P) || !vec_ok(slot_of, P))
+    return FP8BLK_ERR_INVALID_ARG;
+  RowSplit sp = split_row(ceil_div(C, (int64_t)16));
+  sp.lanes = 256;  // the scale workgroups take 256 rows each
+  const int64_t blocks = T * sp.segs + ceil_div(P, (int64_t)256) * ceil_div(G, (int64_t)kScaleGroups);
+  if (!grid_ok(blocks, sp.lanes)) return FP8BLK_ERR_UNSUPPORTED;
+  hipLaunchKernelGGL((k_moe_dispatch<1, true>), dim3((unsigned)blocks), dim3(sp.lanes), 0, as_stream(stream), q, ldq, C,
+                     T, (uint32_t)K, row_of, qr, ldqr, sp.segs, s, G, slot_of, sr);
+  return launch_status();
+}
+
+extern "C" fp8blk_status_t fp8blk_moe_combine(const void* rows, int64_t T, int64_t K, int64_t C, int64_t ldr,
+                                              const int32_t* row_of, const float* weights, void* y, int64_t ldy,
+                                              uint32_t flags, void* stream) {
+  if (flags & ~(FP8BLK_MOE_ROWS_F32 | FP8BLK_MOE_TOKENS_F32)) return FP8BLK_ERR_INVALID_ARG;
+  const fp8blk_status_t st = pairs_ok(T, K, C);
+  if (st != FP8BLK_OK) return st;
+  if (T == 0 || C == 0) return FP8BLK_OK;
+  const bool rf = (flags & FP8BLK_MOE_ROWS_F32) != 0, yf = (flags & FP8BLK_MOE_TOKENS_F32) != 0;
+  if (!matrix_ok(rows, T * K, C, ldr, rf ? 4 : 2) || !matrix_ok(y, T, C, ldy, yf ? 4 : 2) || !vec_ok(row_of, T * K) ||
+      (weights != nullptr && !aligned(weights, 4)))
+    return FP8BLK_ERR_INVALID_ARG;
+  const RowSplit sp = split_row(ceil_div(C, (int64_t)8));
+  if (!grid_ok(T * sp.segs, sp.lanes)) return FP8BLK_ERR_UNSUPPORTED;
+  auto* go = rf ? (yf ? launch_combine<float, float> : launch_combine<float, uint16_t>)
+                : (yf ? launch_combine<uint16_t, float> : launch_combine<uint16_t, uint16_t>);
+  go(rows, ldr, C, T, (uint32_t)K, row_of, weights, y, ldy, as_stream(stream));
+  return launch_status();
+}
+
+extern "C" fp8blk_status_t fp8blk_moe_combine_backward(const void* dy, int64_t lddy, const void* rows, int64_t ldr,
+                                                       int64_t T, int64_t K, int64_t C, const int32_t* row_of,
+                                                       const float* weights, void* drows, int64_t lddr,
+                                                       float* dweights, uint32_t flags, void* stream) {
+  if (flags & ~(FP8BLK_MOE_ROWS_F32 | FP8BLK_MOE_TOKENS_F32 | FP8BLK_MOE_DROWS_F32)) return FP8BLK_ERR_INVALID_ARG;
+  const fp8blk_status_t st = pairs_ok(T, K, C);
+  if (st != FP8BLK_OK) return st;
+  if (T == 0 || K == 0) return FP8BLK_OK;
+  const bool yf = (flags & FP8BLK_MOE_TOKENS_F32) != 0, rf = (flags & FP8BLK_MOE_ROWS_F32) != 0;
+  const bool df = (flags & FP8BLK_MOE_DROWS_F32) != 0;
+  if (!matrix_ok(dy, T, C, lddy, yf ? 4 : 2) || !matrix_ok(rows, T * K, C, ldr, rf ? 4 : 2) ||
+      !matrix_ok(drows, T * K, C, lddr, df ? 4 : 2) || !vec_ok(row_of, T * K) || !vec_ok(weights, T * K) ||
+      !vec_ok(dweights, T * K))
+    return FP8BLK_ERR_INVALID_ARG;
+  if (!grid_ok(T, split_row(ceil_div(C, (int64_t)8)).lanes)) return FP8BLK_ERR_UNSUPPORTED;
+  using U = uint16_t;
+  using F = float;
+  auto* go = yf ? (rf ? (df ? launch_combine_backward<F, F, F> : launch_combine_backward<F, F, U>)
+                      : (df ? launch_combine_backward<F, U, F> : launch_combine_backward<F, U, U>))
+                : (rf ? (df ? launch_combine_backward<U, F, F> : launch_combine_backward<U, F, U>)
+                      : (df ? launch_combine_backward<U, U, F> : launch_combine_backward<U, U, U>));
+  go(dy, lddy, rows, ldr, T, (uint32_t)K, C, row_of, weights, drows, lddr, dweights, as_stream(stream));
+  return launch_status();
+}
