@@ -121,17 +121,46 @@ __device__ __forceinline__ void store8(float* p, int64_t avail, const float (&v)
   }
 }
 
-// Sum over the wave's 64 lanes, the same in every lane.
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
+// Sum over the wave's 64 lanes, the same bits in every lane.  FP32: four DPP
+// steps inside each row of 16 lanes, then the rows and the halves exchanged by
+// register swaps; no LDS traffic, where a lane exchange by __shfl costs an LDS
+// round trip per step.
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float row16_sum(float v) {
+  v += dpp_f32<0xB1>(v);   // quad_perm 1,0,3,2
+  v += dpp_f32<0x4E>(v);   // quad_perm 2,3,0,1
+  v += dpp_f32<0x141>(v);  // row_half_mirror
+  v += dpp_f32<0x140>(v);  // row_mirror
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row16_sum(v);
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(h[0]) + __uint_as_float(h[1]);
+}
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
   return v;
 }
 
-// Sums of N values over the workgroup's `nw` waves, the same in every lane.
-// `red` holds N * nw values of LDS; one barrier, so consecutive calls take
-// turns over two LDS arrays (a wave may still read the last one's).
+// A barrier that orders LDS accesses only: global loads and stores in flight
+// stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Sums of N values over the workgroup's `nw` (at most 16) waves, the same bits
+// in every lane.  `red` holds N * 16 floats of LDS; there is one barrier, so
+// consecutive calls take turns over two LDS arrays (a slower wave may still
+// read the last one's).
 template <int N>
 __device__ __forceinline__ void block_sum(float (&v)[N], float* red, int nw) {
 #pragma unroll
@@ -139,15 +168,12 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float* red, int nw) {
   if (nw == 1) return;
   if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) red[(threadIdx.x >> 6) * N + i] = v[i];
+    for (int i = 0; i < N; ++i) red[i * 16 + (threadIdx.x >> 6)] = v[i];
   }
-  __syncthreads();
+  lds_barrier();
+  const int w = threadIdx.x & 15;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.0f;
-  for (int w = 0; w < nw; ++w) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += red[w * N + i];
-  }
+  for (int i = 0; i < N; ++i) v[i] = row16_sum(w < nw ? red[i * 16 + w] : 0.0f);
 }
 
 }  // namespace fp8blk

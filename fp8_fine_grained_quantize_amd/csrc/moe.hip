@@ -30,7 +30,7 @@ namespace fp8blk {
 // each workgroup's segment and every workgroup of k_moe_sort then sums the
 // counts before it.  Dropped pairs form the last bucket, key E.
 // ---------------------------------------------------------------------------
-constexpr int kMaxExperts = 960;       // 16 waves' counts stay within 64 KB of LDS
+constexpr int kMaxExperts = 960;       // 16 waves' counts, kept within 64 KB of LDS
 constexpr int64_t kSortOne = 4096;     // pairs that one workgroup sorts
 constexpr int64_t kSortBlocks = 256;   // most workgroups of the two-launch sort
 constexpr int kSortWaves = 16;
@@ -56,7 +56,8 @@ __global__ __launch_bounds__(1024) void k_moe_count(const ID* __restrict__ ids, 
 }
 
 // nb workgroups of nw waves; each wave takes per_wave (a multiple of 64)
-// consecutive pairs.  LDS: cnt[nw][E+1] and scan[2][nw].  blockDim >= E.
+// consecutive pairs.  LDS: cnt[nw][E+1], scan[2][nw] and, with hist and E at most
+// half of blockDim, 2 * blockDim partial counts.  blockDim >= E.
 template <typename ID>
 __global__ __launch_bounds__(1024) void k_moe_sort(const ID* __restrict__ ids, int64_t ld, uint32_t K, uint32_t P,
                                                     int E, int nbits, uint32_t per_wave,
@@ -80,15 +81,36 @@ __global__ __launch_bounds__(1024) void k_moe_sort(const ID* __restrict__ ids, i
   // Thread e: expert e's pairs in all workgroups, and in those before this one.
   const int e = threadIdx.x;
   int32_t total = 0, before = 0;
-  if (e < E) {
-    if (hist == nullptr) {
+  if (hist == nullptr) {
+    if (e < E)
       for (int w = 0; w < nw; ++w) total += cnt[w * EB + e];
-    } else {
-      for (uint32_t b = 0; b < gridDim.x; ++b) {
-        const int32_t h = hist[(int64_t)b * E + e];
-        total += h;
-        before += b < blockIdx.x ? h : 0;
+  } else {
+    // groups of EP threads share the workgroups' counts, eight loads in flight
+    const int EP = (E + 63) & ~63, groups = EP > 0 ? (int)blockDim.x / EP : 0;
+    const int grp = EP > 0 ? e / EP : 0, ee = e - grp * EP;
+    if (grp < groups && ee < E) {
+      for (uint32_t h0 = grp; h0 < gridDim.x; h0 += 8 * groups) {
+        int32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = h0 + i * groups < gridDim.x ? hist[(int64_t)(h0 + i * groups) * E + ee] : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          total += h[i];
+          before += h0 + i * groups < blockIdx.x ? h[i] : 0;
+        }
       }
+    }
+    if (groups > 1) {
+      int32_t* part = scan + 2 * nw;  // [2][blockDim.x]
+      part[e] = total;
+      part[blockDim.x + e] = before;
+      __syncthreads();
+      total = before = 0;
+      if (e < E)
+        for (int i = 0; i < groups; ++i) {
+          total += part[i * EP + e];
+          before += part[blockDim.x + i * EP + e];
+        }
     }
   }
   const int32_t incl = wave_inclusive_sum(total), incl_before = wave_inclusive_sum(before);
@@ -274,7 +296,7 @@ __global__ __launch_bounds__(256) void k_moe_combine_backward(const TY* __restri
                                                                const int32_t* __restrict__ row_of,
                                                                const float* __restrict__ w, TD* __restrict__ drows,
                                                                int64_t lddr, float* __restrict__ dw) {
-  __shared__ float red[2][4 * 8];
+  __shared__ float red[2][8 * 16];
   const int64_t P = T * K;
   const int64_t t = blockIdx.x;
   const int nw = blockDim.x >> 6;
@@ -372,7 +394,7 @@ fp8blk_status_t launch_sort(const ID* ids, int64_t ld, uint32_t K, int64_t P, in
                      per_block, hist);
   const fp8blk_status_t st = launch_status();
   if (st != FP8BLK_OK) return st;
-  const size_t lds = (size_t)(kSortWaves * (E + 1) + 2 * kSortWaves) * 4;
+  const size_t lds = (size_t)(kSortWaves * (E + 1) + 2 * kSortWaves + (E <= 512 ? 2 * kSortWaves * 64 : 0)) * 4;
   hipLaunchKernelGGL(k_moe_sort<ID>, dim3(nb), dim3(kSortWaves * 64), lds, stream, ids, ld, K, (uint32_t)P, E, nbits,
                      per_wave, hist, offsets, row_of, slot_of);
   return launch_status();

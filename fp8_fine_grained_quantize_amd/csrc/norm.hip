@@ -50,25 +50,23 @@ __device__ __forceinline__ void load_param8(const void* p, bool f32, int64_t col
   }
 }
 
-// The 1x128 tile of n that a row of 16 lanes holds, eight values each.  The
-// default quotient is fl32(n * fl64(1/s)), the correctly rounded n / s for all
-// FP32 n and s (see k_requant_128x1); power-of-two scales multiply by the
-// exact reciprocal.
+// The 1x128 tile of n that a row of 16 lanes holds, eight values each, scaled
+// and rounded as the BF16 quantizers do it (fp8_device.h): n / s by Markstein's
+// correction with the rounded reciprocal, for FP32 n within one unit in the
+// last place of the quotient, or by the exact reciprocal of a power of two.
 template <bool POW2>
 __device__ __forceinline__ uint2 quantize_tile(const float (&n)[8], float& s) {
   uint32_t a = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(n[i]) & 0x7FFFFFFFu);
-  const TileScale ts = make_scale<POW2, false>(row16_max(a));
+  const TileScale ts = make_scale<POW2, true>(row16_max(a));
   s = ts.s;
   float y[8];
-  if (POW2 && !ts.slow) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = n[i] * ts.r;
-  } else {
-    const double r = 1.0 / (double)ts.s;
+  for (int i = 0; i < 8; ++i) y[i] = quotient_fast<POW2, true>(n[i], ts);
+  if (__builtin_expect(ts.slow, 0)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf((float)((double)n[i] * r), -kE4M3Max), kE4M3Max);
+    for (int i = 0; i < 8; ++i) y[i] = quotient_slow(n[i], ts.s);
   }
   uint2 c;
   c.x = pack4_e4m3(y[0], y[1], y[2], y[3]);
@@ -86,100 +84,137 @@ __device__ __forceinline__ void store_codes8(uint8_t* p, int64_t avail, uint2 c)
     if (j < avail) p[j] = (uint8_t)((j < 4 ? c.x : c.y) >> ((j & 3) * 8));
 }
 
-// One workgroup per row; lane t holds the chunks of eight channels t, t + NT,
-// ... (NCH of them), so that a 1x128 tile is one row of 16 lanes.
-template <typename TX, int NCH>
-__global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
-  __shared__ float red[2][16];
-  const int nt = blockDim.x, nw = nt >> 6;
-  const int64_t row = blockIdx.x;
-  const float inv_c = 1.0f / (float)a.C;
-  const bool pf32 = (a.flags & FP8BLK_NORM_PARAM_F32) != 0;
-  float z[NCH][8];
+// The statistic of a row: (sum / C + eps)^(-1/2).
+__device__ __forceinline__ float rstd_of(float sum, float inv_c, float eps) { return 1.0f / sqrtf(sum * inv_c + eps); }
+
+// What a lane reads of one row, before it is unpacked.
+template <typename TX, int NCH, bool GATE_ROW>
+struct NormRow {
+  Raw8<TX> x[NCH];
+  Raw8<uint16_t> f[NCH], gate[GATE_ROW ? NCH : 1];
+};
+
+template <typename TX, int NCH, bool GATE_ROW>
+__device__ __forceinline__ void load_row(NormRow<TX, NCH, GATE_ROW>& r, const NormFwd& a, int64_t row) {
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
-    Raw8<TX> r;
-    load8(r, reinterpret_cast<const TX*>(a.x) + row * a.ldx + col, a.C - col);
-    unpack8(r, z[c]);
+    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * blockDim.x) * 8, avail = a.C - col;
+    load8(r.x[c], reinterpret_cast<const TX*>(a.x) + row * a.ldx + col, avail);
+    if (a.f != nullptr) load8(r.f[c], a.f + row * a.ldf + col, avail);
+    if (GATE_ROW) load8(r.gate[c], reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg + col, avail);
   }
-  if (a.f != nullptr) {
-    float f[NCH][8];
+}
+
+// A workgroup takes the rows blockIdx.x, blockIdx.x + gridDim.x, ...; lane t
+// holds the chunks of eight channels t, t + NT, ... (NCH of them), so that a
+// 1x128 tile is one row of 16 lanes, and the parameters of its channels.  The
+// next row is loaded before the present one is worked on: the reductions and
+// stores of one row cover the other's way from HBM.
+template <typename TX, int NCH, bool GATE_ROW>
+__global__ __launch_bounds__(512) void k_residual_norm(const NormFwd a) {
+  __shared__ float red[2][2][16];
+  const int nt = blockDim.x, nw = nt >> 6;
+  const float inv_c = 1.0f / (float)a.C;
+  const bool pf32 = (a.flags & FP8BLK_NORM_PARAM_F32) != 0;
+  float pc[NCH][8], wn[NCH][8];  // alpha * w_post * (gate per channel); w_pre
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
-      Raw8<uint16_t> r;
-      load8(r, a.f + row * a.ldf + col, a.C - col);
-      unpack8(r, f[c]);
-    }
+  for (int c = 0; c < NCH; ++c) {
+    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8, avail = a.C - col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pc[c][i] = a.alpha;
+    float w[8];
     if (a.w_post != nullptr) {
-      float sum[1] = {0.0f};
+      load_param8(a.w_post, pf32, col, avail, w);
 #pragma unroll
-      for (int c = 0; c < NCH; ++c)
+      for (int i = 0; i < 8; ++i) pc[c][i] *= w[i];
+    }
+    if (a.gate != nullptr && !GATE_ROW) {
+      load_param8(a.gate, pf32, col, avail, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(f[c][i], f[c][i], sum[0]);
-      block_sum<1>(sum, red[0], nw);
-      const float r = 1.0f / sqrtf(sum[0] * inv_c + a.eps);
-      if (a.rstd_post != nullptr && threadIdx.x == 0) a.rstd_post[row] = r;
+      for (int i = 0; i < 8; ++i) pc[c][i] *= w[i];
+    }
+    if (a.w_pre != nullptr) load_param8(a.w_pre, pf32, col, avail, wn[c]);
+  }
+  NormRow<TX, NCH, GATE_ROW> next;
+  load_row(next, a, blockIdx.x);
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
+    const NormRow<TX, NCH, GATE_ROW> cur = next;
+    if (row + gridDim.x < a.M) load_row(next, a, row + gridDim.x);
+    float z[NCH][8];
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) unpack8(cur.x[c], z[c]);
+    if (a.f != nullptr) {
+      float r = 1.0f;
+      if (a.w_post != nullptr) {
+        float sum[1] = {0.0f};
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+          float f[8];
+          unpack8(cur.f[c], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(f[i], f[i], sum[0]);
+        }
+        block_sum<1>(sum, red[turn][0], nw);
+        r = rstd_of(sum[0], inv_c, a.eps);
+        if (a.rstd_post != nullptr && threadIdx.x == 0) a.rstd_post[row] = r;
+      }
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
-        float w[8];
-        load_param8(a.w_post, pf32, col, a.C - col, w);
+        float f[8];
+        unpack8(cur.f[c], f);
+        if (GATE_ROW) {
+          float g[8];
+          unpack8(cur.gate[c], g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[c][i] = f[c][i] * r * w[i];
+          for (int i = 0; i < 8; ++i) f[i] *= g[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[c][i] = __builtin_fmaf(f[i] * r, pc[c][i], z[c][i]);
+        store8(reinterpret_cast<TX*>(a.x_out) + row * a.ldxo + col, a.C - col, z[c]);
       }
     }
+    if (a.w_pre == nullptr) continue;
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(z[c][i], z[c][i], sum[0]);
+    block_sum<1>(sum, red[turn][1], nw);
+    const float r = rstd_of(sum[0], inv_c, a.eps);
+    if (a.rstd_pre != nullptr && threadIdx.x == 0) a.rstd_pre[row] = r;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
-      if (a.gate != nullptr) {
-        float g[8];
-        if (a.flags & FP8BLK_NORM_GATE_ROW)
-          load_param8(reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg, false, col, a.C - col, g);
-        else
-          load_param8(a.gate, pf32, col, a.C - col, g);
+      const int64_t chunk = (int64_t)threadIdx.x + (int64_t)c * nt, col = chunk * 8, avail = a.C - col;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[c][i] *= g[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[c][i] = __builtin_fmaf(a.alpha, f[c][i], z[c][i]);
-      store8(reinterpret_cast<TX*>(a.x_out) + row * a.ldxo + col, a.C - col, z[c]);
-    }
-  }
-  if (a.w_pre == nullptr) return;
-  float sum[1] = {0.0f};
-#pragma unroll
-  for (int c = 0; c < NCH; ++c)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(z[c][i], z[c][i], sum[0]);
-  block_sum<1>(sum, red[1], nw);
-  const float r = 1.0f / sqrtf(sum[0] * inv_c + a.eps);
-  if (a.rstd_pre != nullptr && threadIdx.x == 0) a.rstd_pre[row] = r;
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int64_t chunk = (int64_t)threadIdx.x + (int64_t)c * nt, col = chunk * 8, avail = a.C - col;
-    float w[8];
-    load_param8(a.w_pre, pf32, col, avail, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[c][i] = z[c][i] * r * w[i];
-    if (a.n != nullptr) store8(a.n + row * a.ldn + col, avail, z[c]);
-    if (a.q != nullptr) {
-      float s;
-      const uint2 codes = a.flags & FP8BLK_SCALE_POW2 ? quantize_tile<true>(z[c], s) : quantize_tile<false>(z[c], s);
-      if (avail > 0) {
-        store_codes8(a.q + row * a.ldq + col, avail, codes);
-        if ((threadIdx.x & 15) == 0) a.s[(chunk >> 4) * a.M + row] = s;
+      for (int i = 0; i < 8; ++i) z[c][i] = z[c][i] * r * wn[c][i];
+      if (a.n != nullptr) store8(a.n + row * a.ldn + col, avail, z[c]);
+      if (a.q != nullptr) {
+        float s;
+        const uint2 codes = a.flags & FP8BLK_SCALE_POW2 ? quantize_tile<true>(z[c], s) : quantize_tile<false>(z[c], s);
+        if (avail > 0) {
+          store_codes8(a.q + row * a.ldq + col, avail, codes);
+          if ((threadIdx.x & 15) == 0) a.s[(chunk >> 4) * a.M + row] = s;
+        }
       }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Gradient.  A workgroup takes the rows blockIdx.x, blockIdx.x + gridDim.x, ...
-// and keeps its share of the sums over rows (dw_pre, dw_post, dgate) in
-// registers; at the end it writes them as one row of partials, which
-// k_norm_sums adds up in order.
+// Gradient.  With h = x' r_pre, v = dn w_pre, m = mean_c(v h) the gradient of
+// x' is g = dx_out + r_pre (v - h m), and with h' = f r_post and v' = p g,
+// p = alpha gate w_post, df = r_post (v' - h' m'), where
+//   m' = mean_c(v' h') = (sum_c p h' (dx_out + r_pre v) - r_pre m sum_c p h' h) / C,
+// so that all three sums of a row come from one pass and one barrier.  The
+// sums over rows need only two accumulators per channel, of dn h and of
+// g h' (times the gate where it is one per token): the channel's own factors
+// follow at the end,
+//   dw_post = alpha gate sum_m g h',   dgate = alpha w_post sum_m g h'.
+// A workgroup takes the rows blockIdx.x, blockIdx.x + gridDim.x, ... with the
+// next row's loads in flight, keeps the accumulators in registers and writes
+// them as one row of partials, which k_norm_sums adds up in order.
 // ---------------------------------------------------------------------------
 struct NormBwd {
   const void* x;
@@ -196,173 +231,246 @@ struct NormBwd {
   uint16_t* dgate_row;
   float* part_pre;   // [gridDim.x][C] each, or NULL
   float* part_post;
-  float* part_gate;
   int64_t M, C, ldx, lddxo, lddn, ldf, ldg, lddx, lddf, lddg;
   float alpha;
   uint32_t flags;
 };
 
-template <typename TX, int NCH>
-__global__ __launch_bounds__(1024) void k_residual_norm_backward(const NormBwd a) {
-  __shared__ float red[2][16];
+// What a lane reads of one chunk of one row, before it is unpacked.
+template <typename TX, bool GATE_ROW>
+struct NormBwdChunk {
+  Raw8<TX> x, dxo;
+  Raw8<uint16_t> dn, f, gate;
+};
+
+template <typename TX, bool GATE_ROW>
+__device__ __forceinline__ void load_chunk(NormBwdChunk<TX, GATE_ROW>& r, const NormBwd& a, int64_t row, int64_t col) {
+  const int64_t avail = a.C - col;
+  zero8(r.x);
+  zero8(r.dxo);
+  zero8(r.dn);
+  zero8(r.f);
+  if (a.w_pre != nullptr) {
+    load8(r.x, reinterpret_cast<const TX*>(a.x) + row * a.ldx + col, avail);
+    load8(r.dn, a.dn + row * a.lddn + col, avail);
+  }
+  if (a.dxo != nullptr) load8(r.dxo, reinterpret_cast<const TX*>(a.dxo) + row * a.lddxo + col, avail);
+  if (a.f != nullptr) load8(r.f, a.f + row * a.ldf + col, avail);
+  if (GATE_ROW) load8(r.gate, reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg + col, avail);
+}
+
+// The parameters of a chunk: alpha * w_post * (gate per channel), and w_pre.
+template <bool GATE_ROW>
+__device__ __forceinline__ void load_factors(const NormBwd& a, int64_t col, float (&pc)[8], float (&wn)[8]) {
+  const bool pf32 = (a.flags & FP8BLK_NORM_PARAM_F32) != 0;
+  const int64_t avail = a.C - col;
+  float w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    pc[i] = a.alpha;
+    wn[i] = 0.0f;
+  }
+  if (a.w_post != nullptr) {
+    load_param8(a.w_post, pf32, col, avail, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pc[i] *= w[i];
+  }
+  if (a.gate != nullptr && !GATE_ROW) {
+    load_param8(a.gate, pf32, col, avail, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pc[i] *= w[i];
+  }
+  if (a.w_pre != nullptr) load_param8(a.w_pre, pf32, col, avail, wn);
+}
+
+// With one or two chunks per lane the factors and the next row are held in
+// registers.  Where they would not fit beside the accumulators (four chunks, C
+// above 8192; two of FP32 x with a gate per token) factors and rows are read
+// chunk by chunk, and once more (from L2) after the reduction.
+template <typename TX, int NCH, bool GATE_ROW>
+__global__ __launch_bounds__(512) void k_residual_norm_backward(const NormBwd a) {
+  constexpr bool HOLD = NCH == 1 || (NCH == 2 && !(GATE_ROW && sizeof(TX) == 4));
+  constexpr int NH = HOLD ? NCH : 1;
+  __shared__ float red[2][3 * 16];
   const int nt = blockDim.x, nw = nt >> 6;
   const float inv_c = 1.0f / (float)a.C;
-  const bool pf32 = (a.flags & FP8BLK_NORM_PARAM_F32) != 0;
-  const bool gate_row = (a.flags & FP8BLK_NORM_GATE_ROW) != 0;
-  float s_pre[NCH][8], s_post[NCH][8], s_gate[NCH][8];
+  float s_pre[NCH][8], s_post[NCH][8], pc_[NH][8], wn_[NH][8];
+  NormBwdChunk<TX, GATE_ROW> next[NH], cur_[NH];
 #pragma unroll
-  for (int c = 0; c < NCH; ++c)
+  for (int c = 0; c < NCH; ++c) {
+    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_pre[c][i] = s_post[c][i] = s_gate[c][i] = 0.0f;
-
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
-    float g[NCH][8];
+    for (int i = 0; i < 8; ++i) s_pre[c][i] = s_post[c][i] = 0.0f;
+    if (HOLD) {
+      load_factors<GATE_ROW>(a, col, pc_[c], wn_[c]);
+      load_chunk(next[c], a, blockIdx.x, col);
+    }
+  }
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
+    const float r_pre = a.w_pre != nullptr ? a.rstd_pre[row] : 0.0f;
+    const float r_post = a.w_post != nullptr ? a.rstd_post[row] : 1.0f;
+    if (HOLD) {
+#pragma unroll
+      for (int c = 0; c < NH; ++c) {
+        cur_[c] = next[c];
+        if (row + gridDim.x < a.M)
+          load_chunk(next[c], a, row + gridDim.x, ((int64_t)threadIdx.x + (int64_t)c * nt) * 8);
+      }
+    }
+    float sum[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[c][i] = 0.0f;
-      if (a.dxo != nullptr) {
-        Raw8<TX> r;
-        load8(r, reinterpret_cast<const TX*>(a.dxo) + row * a.lddxo + col, a.C - col);
-        unpack8(r, g[c]);
-      }
-    }
-    if (a.w_pre != nullptr) {
-      float h[NCH][8], v[NCH][8];
-      float sum[1] = {0.0f};
-      const float r = a.rstd_pre[row];
-#pragma unroll
-      for (int c = 0; c < NCH; ++c) {
-        const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8, avail = a.C - col;
-        Raw8<TX> rx;
-        Raw8<uint16_t> rd;
-        float w[8];
-        load8(rx, reinterpret_cast<const TX*>(a.x) + row * a.ldx + col, avail);
-        load8(rd, a.dn + row * a.lddn + col, avail);
-        load_param8(a.w_pre, pf32, col, avail, w);
-        unpack8(rx, h[c]);
-        unpack8(rd, v[c]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          h[c][i] *= r;
-          s_pre[c][i] = __builtin_fmaf(v[c][i], h[c][i], s_pre[c][i]);
-          v[c][i] *= w[i];
-          sum[0] = __builtin_fmaf(v[c][i], h[c][i], sum[0]);
-        }
-      }
-      block_sum<1>(sum, red[0], nw);
-      const float mean = sum[0] * inv_c;
-#pragma unroll
-      for (int c = 0; c < NCH; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[c][i] += r * __builtin_fmaf(-h[c][i], mean, v[c][i]);
-    }
-    if (a.dx != nullptr) {
-#pragma unroll
-      for (int c = 0; c < NCH; ++c) {
+      float(&pc)[8] = pc_[HOLD ? c : 0];
+      float(&wn)[8] = wn_[HOLD ? c : 0];
+      NormBwdChunk<TX, GATE_ROW>& cur = cur_[HOLD ? c : 0];
+      if (!HOLD) {
         const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
-        store8(reinterpret_cast<TX*>(a.dx) + row * a.lddx + col, a.C - col, g[c]);
+        load_factors<GATE_ROW>(a, col, pc, wn);
+        load_chunk(cur, a, row, col);
+      }
+      float h[8], v[8], g[8], hf[8], gt[8];
+      unpack8(cur.x, h);
+      unpack8(cur.dn, v);
+      unpack8(cur.dxo, g);
+      unpack8(cur.f, hf);
+      if (GATE_ROW) unpack8(cur.gate, gt);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[i] *= r_pre;
+        s_pre[c][i] = __builtin_fmaf(v[i], h[i], s_pre[c][i]);
+        v[i] *= wn[i];
+        sum[0] = __builtin_fmaf(v[i], h[i], sum[0]);
+        float p = pc[i] * (hf[i] * r_post);
+        if (GATE_ROW) p *= gt[i];
+        sum[1] = __builtin_fmaf(p, __builtin_fmaf(r_pre, v[i], g[i]), sum[1]);
+        sum[2] = __builtin_fmaf(p, h[i], sum[2]);
       }
     }
-    if (a.f == nullptr) {
-      __syncthreads();  // red[0] is read by all before the next row writes it
-      continue;
-    }
-    float h[NCH][8];
-    float sum[1] = {0.0f};
-    const float r = a.w_post != nullptr ? a.rstd_post[row] : 1.0f;
+    block_sum<3>(sum, red[turn], nw);
+    const float m = sum[0] * inv_c;
+    const float m_post = a.w_post != nullptr ? (sum[1] - r_pre * m * sum[2]) * inv_c : 0.0f;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8, avail = a.C - col;
-      Raw8<uint16_t> rf;
-      float w[8], gt[8], dg[8];
-      load8(rf, a.f + row * a.ldf + col, avail);
-      unpack8(rf, h[c]);
-      if (a.w_post != nullptr) load_param8(a.w_post, pf32, col, avail, w);
-      if (a.gate != nullptr) {
-        if (gate_row)
-          load_param8(reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg, false, col, avail, gt);
-        else
-          load_param8(a.gate, pf32, col, avail, gt);
+      float(&pc)[8] = pc_[HOLD ? c : 0];
+      float(&wn)[8] = wn_[HOLD ? c : 0];
+      NormBwdChunk<TX, GATE_ROW>& cur = cur_[HOLD ? c : 0];
+      if (!HOLD) {
+        load_factors<GATE_ROW>(a, col, pc, wn);
+        load_chunk(cur, a, row, col);
       }
+      float h[8], v[8], g[8];
+      unpack8(cur.x, h);
+      unpack8(cur.dn, v);
+      unpack8(cur.dxo, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        g[i] = __builtin_fmaf(r_pre, __builtin_fmaf(-(h[i] * r_pre), m, v[i] * wn[i]), g[i]);
+      if (a.dx != nullptr) store8(reinterpret_cast<TX*>(a.dx) + row * a.lddx + col, avail, g);
+      if (a.f == nullptr) continue;
+      unpack8(cur.f, h);
+      float gt[8];
+      if (GATE_ROW) unpack8(cur.gate, gt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float d = a.alpha * g[c][i];
-        h[c][i] *= r;
-        dg[i] = d * (a.w_post != nullptr ? h[c][i] * w[i] : h[c][i]);
-        if (a.gate != nullptr) d *= gt[i];
-        if (a.w_post != nullptr) {
-          s_post[c][i] = __builtin_fmaf(d, h[c][i], s_post[c][i]);
-          d *= w[i];
-          sum[0] = __builtin_fmaf(d, h[c][i], sum[0]);
-        }
-        s_gate[c][i] += dg[i];
-        g[c][i] = d;
+        h[i] *= r_post;
+        v[i] = g[i] * h[i];  // times its factors: the terms of dw_post and dgate
+        float d = pc[i] * g[i];
+        if (GATE_ROW) d *= gt[i];
+        s_post[c][i] += GATE_ROW ? v[i] * gt[i] : v[i];
+        g[i] = r_post * __builtin_fmaf(-h[i], m_post, d);
       }
-      if (a.dgate_row != nullptr) store8(a.dgate_row + row * a.lddg + col, avail, dg);
-    }
-    if (a.w_post != nullptr) {
-      block_sum<1>(sum, red[1], nw);
-      const float mean = sum[0] * inv_c;
+      if (GATE_ROW) {
 #pragma unroll
-      for (int c = 0; c < NCH; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[c][i] = r * __builtin_fmaf(-h[c][i], mean, g[c][i]);
+        for (int i = 0; i < 8; ++i) v[i] *= pc[i];
+        store8(a.dgate_row + row * a.lddg + col, avail, v);
+      }
+      store8(a.df + row * a.lddf + col, avail, g);
     }
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
-      store8(a.df + row * a.lddf + col, a.C - col, g[c]);
-    }
-    __syncthreads();
   }
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8, avail = a.C - col;
     if (a.part_pre != nullptr) store8(a.part_pre + (int64_t)blockIdx.x * a.C + col, avail, s_pre[c]);
     if (a.part_post != nullptr) store8(a.part_post + (int64_t)blockIdx.x * a.C + col, avail, s_post[c]);
-    if (a.part_gate != nullptr) store8(a.part_gate + (int64_t)blockIdx.x * a.C + col, avail, s_gate[c]);
   }
 }
 
-// out[c] = sum over the nb rows of part, in a fixed order: 64 columns per
-// workgroup, sixteen row classes, then the sixteen sums in order.
+// Sums over the nb rows of partials in a fixed order: 64 columns per
+// workgroup, sixteen row classes, then the sixteen sums in order; blockIdx.y
+// picks the vector.  Of the second, both dw_post and dgate are made.
 struct NormSums {
-  const float* part[3];
-  float* out[3];
+  const float* part[2];
+  float* dw_pre;
+  float* dw_post;
+  float* dgate;
+  const void* w_post;
+  const void* gate;  // per channel
+  float alpha;
+  bool pf32;
 };
-__global__ __launch_bounds__(1024) void k_norm_sums(const NormSums a, int64_t nb, int64_t C) {
+__device__ __forceinline__ float param_at(const void* p, bool f32, int64_t i) {
+  return f32 ? reinterpret_cast<const float*>(p)[i] : to_f32(reinterpret_cast<const uint16_t*>(p)[i]);
+}
+__global__ __launch_bounds__(1024) void k_norm_sums(const NormSums a, int first, int64_t nb, int64_t C) {
   __shared__ float acc[16][64];
-  const float* part = a.part[blockIdx.y];
+  const int vec = first + blockIdx.y;
+  const float* part = a.part[vec];
   const int lane = threadIdx.x & 63, cls = threadIdx.x >> 6;
   const int64_t col = (int64_t)blockIdx.x * 64 + lane;
   float sum = 0.0f;
-  if (col < C)
-    for (int64_t b = cls; b < nb; b += 16) sum += part[b * C + col];
+  if (col < C) {
+    for (int64_t b = cls; b < nb; b += 16 * 8) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = b + 16 * i < nb ? part[(b + 16 * i) * C + col] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += v[i];
+    }
+  }
   acc[cls][lane] = sum;
   __syncthreads();
   if (cls == 0 && col < C) {
     float t = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) t += acc[i][lane];
-    a.out[blockIdx.y][col] = t;
+    if (vec == 0) {
+      a.dw_pre[col] = t;
+    } else {
+      t *= a.alpha;
+      if (a.dw_post != nullptr) a.dw_post[col] = a.gate != nullptr ? t * param_at(a.gate, a.pf32, col) : t;
+      if (a.dgate != nullptr) a.dgate[col] = a.w_post != nullptr ? t * param_at(a.w_post, a.pf32, col) : t;
+    }
   }
 }
 
-// Lanes of a row's workgroup, and chunks per lane (1 or 2).
+// Chunks of eight channels per lane, 1, 2 or 4, and lanes of a row's workgroup,
+// at most 512.
+inline int norm_chunks(int64_t C) { return C > 8192 ? 4 : C > 4096 ? 2 : 1; }
 inline int norm_lanes(int64_t C) {
-  const int64_t chunks = ceil_div(C, (int64_t)8);
-  const int64_t per = chunks > 1024 ? ceil_div(chunks, (int64_t)2) : chunks;
-  return (int)(ceil_div(per, (int64_t)64) * 64);
+  return (int)(ceil_div(ceil_div(C, (int64_t)8 * norm_chunks(C)), (int64_t)64) * 64);
 }
 
-// Workgroups of the gradient kernel.
-inline int64_t norm_backward_blocks(int64_t M, int64_t C) {
-  int64_t per_cu = 2048 / norm_lanes(C);
-  if (per_cu > 4) per_cu = 4;
-  const int64_t cap = per_cu * device_cus();
-  return M < cap ? M : cap;
+// Workgroups of either kernel: as many as the GPU holds at a time, `per_cu`
+// lanes on a compute unit.
+inline int64_t norm_blocks(int64_t M, int64_t C, int64_t per_cu) {
+  int64_t n = per_cu / norm_lanes(C);
+  n = (n < 1 ? 1 : n) * device_cus();
+  return M < n ? M : n;
+}
+inline int64_t norm_forward_blocks(int64_t M, int64_t C) { return norm_blocks(M, C, 1024); }
+inline int64_t norm_backward_blocks(int64_t M, int64_t C) { return norm_blocks(M, C, 512); }
+
+template <typename TX, int NCH, bool GATE_ROW>
+void launch_forward(const NormFwd& a, hipStream_t stream) {
+  hipLaunchKernelGGL((k_residual_norm<TX, NCH, GATE_ROW>), dim3((unsigned)norm_forward_blocks(a.M, a.C)),
+                     dim3((unsigned)norm_lanes(a.C)), 0, stream, a);
+}
+template <typename TX, int NCH, bool GATE_ROW>
+void launch_backward(const NormBwd& a, hipStream_t stream) {
+  hipLaunchKernelGGL((k_residual_norm_backward<TX, NCH, GATE_ROW>), dim3((unsigned)norm_backward_blocks(a.M, a.C)),
+                     dim3((unsigned)norm_lanes(a.C)), 0, stream, a);
 }
 
 }  // namespace fp8blk
@@ -401,21 +509,18 @@ extern "C" fp8blk_status_t fp8blk_residual_norm(int64_t M, int64_t C, const void
   if ((flags & FP8BLK_SCALE_POW2) && q == nullptr) return FP8BLK_ERR_INVALID_ARG;
   const NormFwd a{x, f, w_post, gate, w_pre, x_out, n, q, s, rstd_post, rstd_pre,
                   M, C, ldx, ldf, ldg, ldxo, ldn, ldq, alpha, eps, flags};
-  const dim3 grid((unsigned)M), block((unsigned)norm_lanes(C));
-  const bool two = C > 8192;
-  if (xf) {
-    if (two) hipLaunchKernelGGL((k_residual_norm<float, 2>), grid, block, 0, as_stream(stream), a);
-    else hipLaunchKernelGGL((k_residual_norm<float, 1>), grid, block, 0, as_stream(stream), a);
-  } else {
-    if (two) hipLaunchKernelGGL((k_residual_norm<uint16_t, 2>), grid, block, 0, as_stream(stream), a);
-    else hipLaunchKernelGGL((k_residual_norm<uint16_t, 1>), grid, block, 0, as_stream(stream), a);
-  }
+#define FP8BLK_NORM_PICK(GO, TX, GR) \
+  (norm_chunks(C) == 1 ? GO<TX, 1, GR> : norm_chunks(C) == 2 ? GO<TX, 2, GR> : GO<TX, 4, GR>)
+  auto* go = xf ? (gr ? FP8BLK_NORM_PICK(launch_forward, float, true) : FP8BLK_NORM_PICK(launch_forward, float, false))
+                : (gr ? FP8BLK_NORM_PICK(launch_forward, uint16_t, true)
+                      : FP8BLK_NORM_PICK(launch_forward, uint16_t, false));
+  go(a, as_stream(stream));
   return launch_status();
 }
 
 extern "C" size_t fp8blk_residual_norm_backward_workspace_bytes(int64_t M, int64_t C) {
   if (M <= 0 || C <= 0 || C > kNormMaxC) return 0;
-  return (size_t)(norm_backward_blocks(M, C) * C) * 3 * sizeof(float);
+  return (size_t)(norm_backward_blocks(M, C) * C) * 2 * sizeof(float);
 }
 
 extern "C" fp8blk_status_t fp8blk_residual_norm_backward(
@@ -460,38 +565,26 @@ extern "C" fp8blk_status_t fp8blk_residual_norm_backward(
       (workspace == nullptr || !aligned(workspace, 16) ||
        workspace_bytes < fp8blk_residual_norm_backward_workspace_bytes(M, C)))
     return FP8BLK_ERR_INVALID_ARG;
-  float* ws = reinterpret_cast<float*>(workspace);
-  NormSums ns{};
-  int nv = 0;
-  auto part = [&](void* out) -> float* {
-    if (out == nullptr) return nullptr;
-    float* p = ws + (int64_t)nv * nb * C;
-    ns.part[nv] = p;
-    ns.out[nv++] = reinterpret_cast<float*>(out);
-    return nb > 0 ? p : nullptr;
-  };
-  float* part_pre = part(dw_pre);
-  float* part_post = part(dw_post);
-  float* part_gate = part(gr ? nullptr : dgate);
+  float* part_pre = pre && nb > 0 ? reinterpret_cast<float*>(workspace) : nullptr;
+  float* part_post =
+      (postw || (gated && !gr)) && nb > 0 ? reinterpret_cast<float*>(workspace) + nb * C : nullptr;
   if (nb > 0) {
     const NormBwd a{x_out, dx_out, dn, rstd_pre, w_pre, f, rstd_post, w_post, gate, dx, df,
-                    gr ? reinterpret_cast<uint16_t*>(dgate) : nullptr, part_pre, part_post, part_gate,
+                    gr ? reinterpret_cast<uint16_t*>(dgate) : nullptr, part_pre, part_post,
                     M, C, ldx, lddxo, lddn, ldf, ldg, lddx, lddf, lddg, alpha, flags};
-    const dim3 grid((unsigned)nb), block((unsigned)norm_lanes(C));
-    const bool two = C > 8192;
-    if (xf) {
-      if (two) hipLaunchKernelGGL((k_residual_norm_backward<float, 2>), grid, block, 0, as_stream(stream), a);
-      else hipLaunchKernelGGL((k_residual_norm_backward<float, 1>), grid, block, 0, as_stream(stream), a);
-    } else {
-      if (two) hipLaunchKernelGGL((k_residual_norm_backward<uint16_t, 2>), grid, block, 0, as_stream(stream), a);
-      else hipLaunchKernelGGL((k_residual_norm_backward<uint16_t, 1>), grid, block, 0, as_stream(stream), a);
-    }
+    auto* go = xf ? (gr ? FP8BLK_NORM_PICK(launch_backward, float, true) : FP8BLK_NORM_PICK(launch_backward, float, false))
+                  : (gr ? FP8BLK_NORM_PICK(launch_backward, uint16_t, true)
+                        : FP8BLK_NORM_PICK(launch_backward, uint16_t, false));
+    go(a, as_stream(stream));
     const fp8blk_status_t st = launch_status();
     if (st != FP8BLK_OK) return st;
   }
-  if (nv > 0) {
-    hipLaunchKernelGGL(k_norm_sums, dim3((unsigned)ceil_div(C, (int64_t)64), (unsigned)nv), dim3(1024), 0,
-                       as_stream(stream), ns, nb, C);
+  if (sums) {
+    const int first = pre ? 0 : 1, last = postw || (gated && !gr) ? 1 : 0;
+    const NormSums a{{part_pre, part_post}, dw_pre, dw_post, gr ? nullptr : reinterpret_cast<float*>(dgate), w_post,
+                     gr ? nullptr : gate, alpha, (flags & FP8BLK_NORM_PARAM_F32) != 0};
+    hipLaunchKernelGGL(k_norm_sums, dim3((unsigned)ceil_div(C, (int64_t)64), (unsigned)(last - first + 1)), dim3(1024),
+                       0, as_stream(stream), a, first, nb, C);
     return launch_status();
   }
   return FP8BLK_OK;

@@ -66,25 +66,45 @@ def _need(t: torch.Tensor, dtype, what: str) -> None:
 
 
 def _shape(t: torch.Tensor, shape, what: str) -> None:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _dense(t: torch.Tensor, dtype, shape, what: str) -> None:
-    _need(t, dtype, what)
-    _shape(t, shape, what)
-    if not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _need(t, dtype, what)
+        _shape(t, shape, what)
         raise ValueError(f"{what} must be contiguous")
 
 
-def _same_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
-    """The library works on the current device: every tensor has to be there."""
-    dev = first.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"expected tensors on the current GPU, got {dev}")
+def _current_stream(first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    """The current stream's handle.  The library works on the current device:
+    every tensor has to be there.  (The handle is taken directly: a small call
+    spends more time building torch.cuda.Stream objects than in its kernel.)"""
+    i = first.get_device()
+    if i < 0 or i != torch._C._cuda_getDevice():
+        raise ValueError(f"expected tensors on the current GPU, got {first.device}")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+        if t is not None and t.get_device() != i:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    return torch._C._cuda_getCurrentRawStream(i)
+
+
+def _addr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _ld(t: Optional[torch.Tensor]) -> int:
+    """Row pitch (elements) of a row-major matrix; 0 without one."""
+    if t is None:
+        return 0
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if rows == 0 or cols == 0:
+        return _fb._pad16(cols, t.element_size())
+    if step != 1 and cols != 1:
+        raise ValueError("expected a row-major matrix (unit column stride)")
+    return ld if ld >= cols else cols
 
 
 # --------------------------------------------------------------------------
@@ -99,7 +119,7 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, offsets=None, row_of=No
     pairs (their rows follow offsets[E]); slot_of holds each row's pair."""
     if expert_ids.dtype not in (torch.int32, torch.int64) or expert_ids.dim() != 2:
         raise TypeError("expert_ids must be an int32 or int64 matrix [T][K]")
-    _same_device(expert_ids, offsets, row_of, slot_of, workspace)
+    stream = _current_stream(expert_ids, offsets, row_of, slot_of, workspace)
     T, K = expert_ids.shape
     if (K > 1 and expert_ids.stride(1) != 1) or (T > 1 and expert_ids.stride(0) < K):
         expert_ids = expert_ids.contiguous()
@@ -122,10 +142,10 @@ def moe_sort(expert_ids: torch.Tensor, num_experts: int, offsets=None, row_of=No
     need = L.fp8blk_moe_sort_workspace_bytes(T, K, E)
     if need and workspace is None:
         workspace = new(need // 4, dtype=torch.int32, device=dev)
-    _fb._check(L.fp8blk_moe_sort(_fb._ptr(expert_ids), T, K, expert_ids.stride(0) if T > 1 else K, E,
-                                 _fb._ptr(offsets), _fb._ptr(row_of), _fb._ptr(slot_of), _fb._ptr(workspace),
+    _fb._check(L.fp8blk_moe_sort(_addr(expert_ids), T, K, expert_ids.stride(0) if T > 1 else K, E,
+                                 _addr(offsets), _addr(row_of), _addr(slot_of), _addr(workspace),
                                  0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                 _IDS_I64 if expert_ids.dtype == torch.int64 else 0, _fb._stream()), "moe_sort")
+                                 _IDS_I64 if expert_ids.dtype == torch.int64 else 0, stream), "moe_sort")
     return offsets, row_of, slot_of
 
 
@@ -140,7 +160,7 @@ def moe_dispatch(x: torch.Tensor, row_of: torch.Tensor, out=None) -> torch.Tenso
     """x [T][C] bf16 into expert order: out[row_of[t][k]] = x[t], zeros in the
     rows of dropped pairs.  Returns out bf16 [T*K][C]."""
     _need(x, torch.bfloat16, "x")
-    _same_device(x, row_of, out)
+    stream = _current_stream(x, row_of, out)
     T, C = x.shape
     K = _pairs(row_of, T)
     if out is None:
@@ -148,8 +168,8 @@ def moe_dispatch(x: torch.Tensor, row_of: torch.Tensor, out=None) -> torch.Tenso
     else:
         _need(out, torch.bfloat16, "out")
         _shape(out, (T * K, C), "out")
-    _fb._check(_fb.lib().fp8blk_moe_dispatch(_fb._ptr(x), T, C, _fb._pitch(x), K, _fb._ptr(row_of), _fb._ptr(out),
-                                             _fb._pitch(out), _fb._stream()), "moe_dispatch")
+    _fb._check(_fb.lib().fp8blk_moe_dispatch(_addr(x), T, C, _ld(x), K, _addr(row_of), _addr(out),
+                                             _ld(out), stream), "moe_dispatch")
     return out
 
 
@@ -158,7 +178,7 @@ def moe_dispatch_fp8(q: torch.Tensor, s: torch.Tensor, row_of: torch.Tensor, slo
     order, as the grouped GEMM takes them: returns (qr uint8 [T*K][C],
     sr float32 [ceil(C/128)][T*K])."""
     _need(q, torch.uint8, "q")
-    _same_device(q, s, row_of, slot_of, qr, sr)
+    stream = _current_stream(q, s, row_of, slot_of, qr, sr)
     T, C = q.shape
     K = _pairs(row_of, T)
     G = (C + 127) // 128
@@ -173,9 +193,9 @@ def moe_dispatch_fp8(q: torch.Tensor, s: torch.Tensor, row_of: torch.Tensor, slo
         sr = torch.empty(G, T * K, dtype=torch.float32, device=q.device)
     else:
         _dense(sr, torch.float32, (G, T * K), "sr")
-    _fb._check(_fb.lib().fp8blk_moe_dispatch_fp8(_fb._ptr(q), T, C, _fb._pitch(q), _fb._ptr(s), K, _fb._ptr(row_of),
-                                                 _fb._ptr(slot_of), _fb._ptr(qr), _fb._pitch(qr), _fb._ptr(sr),
-                                                 _fb._stream()), "moe_dispatch_fp8")
+    _fb._check(_fb.lib().fp8blk_moe_dispatch_fp8(_addr(q), T, C, _ld(q), _addr(s), K, _addr(row_of),
+                                                 _addr(slot_of), _addr(qr), _ld(qr), _addr(sr),
+                                                 stream), "moe_dispatch_fp8")
     return qr, sr
 
 
@@ -187,7 +207,7 @@ def moe_combine(rows: torch.Tensor, row_of: torch.Tensor, weights: Optional[torc
     out_dtype (bfloat16 or float32)."""
     T = row_of.shape[0]
     K = _pairs(row_of, T)
-    _same_device(rows, row_of, weights, out)
+    stream = _current_stream(rows, row_of, weights, out)
     C = rows.shape[1]
     _shape(rows, (T * K, C), "rows")
     if weights is not None:
@@ -199,8 +219,8 @@ def moe_combine(rows: torch.Tensor, row_of: torch.Tensor, weights: Optional[torc
         _shape(out, (T, C), "out")
     if _is_f32(out, "out"):
         flags |= _TOKENS_F32
-    _fb._check(_fb.lib().fp8blk_moe_combine(_fb._ptr(rows), T, K, C, _fb._pitch(rows), _fb._ptr(row_of),
-                                            _fb._ptr(weights), _fb._ptr(out), _fb._pitch(out), flags, _fb._stream()),
+    _fb._check(_fb.lib().fp8blk_moe_combine(_addr(rows), T, K, C, _ld(rows), _addr(row_of),
+                                            _addr(weights), _addr(out), _ld(out), flags, stream),
                "moe_combine")
     return out
 
@@ -212,7 +232,7 @@ def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, row_of: torch.Ten
     zeros in the rows of dropped pairs; dweights float32 [T][K])."""
     T, C = dy.shape
     K = _pairs(row_of, T)
-    _same_device(dy, rows, row_of, weights, drows, dweights)
+    stream = _current_stream(dy, rows, row_of, weights, drows, dweights)
     _shape(rows, (T * K, C), "rows")
     _dense(weights, torch.float32, (T, K), "weights")
     flags = (_TOKENS_F32 if _is_f32(dy, "dy") else 0) | (_ROWS_F32 if _is_f32(rows, "rows") else 0)
@@ -228,8 +248,8 @@ def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, row_of: torch.Ten
     else:
         _dense(dweights, torch.float32, (T, K), "dweights")
     _fb._check(_fb.lib().fp8blk_moe_combine_backward(
-        _fb._ptr(dy), _fb._pitch(dy), _fb._ptr(rows), _fb._pitch(rows), T, K, C, _fb._ptr(row_of), _fb._ptr(weights),
-        _fb._ptr(drows), _fb._pitch(drows), _fb._ptr(dweights), flags, _fb._stream()), "moe_combine_backward")
+        _addr(dy), _ld(dy), _addr(rows), _ld(rows), T, K, C, _addr(row_of), _addr(weights),
+        _addr(drows), _ld(drows), _addr(dweights), flags, stream), "moe_combine_backward")
     return drows, dweights
 
 
@@ -277,7 +297,7 @@ def _gate(gate, M: int, C: int):
         return gate, 0, 0
     _need(gate, torch.bfloat16, "a gate per token")
     _shape(gate, (M, C), "gate")
-    return None, _NORM_GATE_ROW, _fb._pitch(gate)
+    return None, _NORM_GATE_ROW, _ld(gate)
 
 
 def residual_norm(x: torch.Tensor, w_pre=None, f=None, w_post=None, gate=None, alpha: float = 1.0, eps: float = 1e-6,
@@ -291,7 +311,7 @@ def residual_norm(x: torch.Tensor, w_pre=None, f=None, w_post=None, gate=None, a
     two with pow2), quantized from the FP32 values; want_n=False then leaves n
     out.  x_out may be x."""
     M, C = x.shape
-    _same_device(x, w_pre, f, w_post, gate, x_out, n, q, s)
+    stream = _current_stream(x, w_pre, f, w_post, gate, x_out, n, q, s)
     gate_c, flags, ldg = _gate(gate, M, C)
     flags |= _params(C, (w_pre, "w_pre"), (w_post, "w_post"), (gate_c, "gate"))
     if _is_f32(x, "x"):
@@ -338,11 +358,11 @@ def residual_norm(x: torch.Tensor, w_pre=None, f=None, w_post=None, gate=None, a
                 flags |= _fb.SCALE_POW2
         else:
             q = s = None
-    p, pitch = _fb._ptr, _fb._pitch
+    p, ld = _addr, _ld
     _fb._check(_fb.lib().fp8blk_residual_norm(
-        M, C, p(x), pitch(x), p(f), 0 if f is None else pitch(f), p(w_post), p(gate), ldg, alpha, p(w_pre), eps,
-        p(x_out), 0 if x_out is None else pitch(x_out), p(n), 0 if n is None else pitch(n), p(q),
-        0 if q is None else pitch(q), p(s), p(rstd_post), p(rstd_pre), flags, _fb._stream()), "residual_norm")
+        M, C, p(x), ld(x), p(f), ld(f), p(w_post), p(gate), ldg, alpha, p(w_pre), eps,
+        p(x_out), ld(x_out), p(n), ld(n), p(q),
+        ld(q), p(s), p(rstd_post), p(rstd_pre), flags, stream), "residual_norm")
     return ResidualNorm(x if f is None else x_out, n, q, s, rstd_post, rstd_pre)
 
 
@@ -353,7 +373,7 @@ def residual_norm_backward(x_out: torch.Tensor, dx_out=None, dn=None, rstd_pre=N
     forward, dx_out the gradient into its x (or None), dn the one into n.
     Without w_pre the gradient of x is dx_out itself, which is returned."""
     M, C = x_out.shape
-    _same_device(x_out, dx_out, dn, rstd_pre, w_pre, f, rstd_post, w_post, gate, dx, df, workspace)
+    stream = _current_stream(x_out, dx_out, dn, rstd_pre, w_pre, f, rstd_post, w_post, gate, dx, df, workspace)
     gate_c, flags, ldg = _gate(gate, M, C)
     flags |= _params(C, (w_pre, "w_pre"), (w_post, "w_post"), (gate_c, "gate"))
     if _is_f32(x_out, "x_out"):
@@ -398,7 +418,7 @@ def residual_norm_backward(x_out: torch.Tensor, dx_out=None, dn=None, rstd_pre=N
             dgate = new(C, dtype=torch.float32, device=dev)
         elif gate is not None:
             dgate = _fb._empty_pitched(M, C, torch.bfloat16, dev, 2)
-            lddg = _fb._pitch(dgate)
+            lddg = _ld(dgate)
     L = _fb.lib()
     ws_bytes = 0
     if workspace is not None:
@@ -406,14 +426,14 @@ def residual_norm_backward(x_out: torch.Tensor, dx_out=None, dn=None, rstd_pre=N
     elif dw_pre is not None or dw_post is not None or (dgate is not None and dgate.dim() == 1):
         ws_bytes = L.fp8blk_residual_norm_backward_workspace_bytes(M, C)
         workspace = new((ws_bytes + 3) // 4, dtype=torch.float32, device=dev)
-    p, pitch = _fb._ptr, _fb._pitch
+    p, ld = _addr, _ld
     if dx is not None or f is not None:
         _fb._check(L.fp8blk_residual_norm_backward(
-            M, C, p(x_out), pitch(x_out), p(dx_out), 0 if dx_out is None else pitch(dx_out), p(dn),
-            0 if dn is None else pitch(dn), p(rstd_pre), p(w_pre), p(f), 0 if f is None else pitch(f), p(rstd_post),
-            p(w_post), p(gate), ldg, alpha, p(dx), 0 if dx is None else pitch(dx), p(df),
-            0 if df is None else pitch(df), p(dw_pre), p(dw_post), p(dgate), lddg, p(workspace), ws_bytes, flags,
-            _fb._stream()), "residual_norm_backward")
+            M, C, p(x_out), ld(x_out), p(dx_out), ld(dx_out), p(dn),
+            ld(dn), p(rstd_pre), p(w_pre), p(f), ld(f), p(rstd_post),
+            p(w_post), p(gate), ldg, alpha, p(dx), ld(dx), p(df),
+            ld(df), p(dw_pre), p(dw_post), p(dgate), lddg, p(workspace), ws_bytes, flags,
+            stream), "residual_norm_backward")
     return ResidualNormGrad(dx_out if dx is None else dx, df, dw_pre, dw_post, dgate)
 
 
@@ -483,7 +503,7 @@ class GradTable:
             self.device = torch.device("cuda", torch.cuda.current_device())
         else:
             self.device = self.tensors[0].device
-            _same_device(self.tensors[0], *self.tensors, *(self.outs or ()))
+            _current_stream(self.tensors[0], *self.tensors, *(self.outs or ()))
         entries = []
         for i, t in enumerate(self.tensors):
             o = t if self.outs is None else self.outs[i]
@@ -499,11 +519,11 @@ class GradTable:
         host = torch.empty(nbytes // 8, dtype=torch.int64)
         chunks = _i64(0)
         array = (_Grad * max(self.n, 1))(*entries)
-        _fb._check(L.fp8blk_grad_table_build(ctypes.cast(array, _vp), self.n, _fb._ptr(host), nbytes,
+        _fb._check(L.fp8blk_grad_table_build(ctypes.cast(array, _vp), self.n, _addr(host), nbytes,
                                              ctypes.cast(ctypes.pointer(chunks), _vp)), "grad_table")
         self.chunks = chunks.value
         self.device_table = host.to(self.device)
-        self._stream = torch.cuda.current_stream()
+        self._stream = torch._C._cuda_getCurrentRawStream(self.device.index)
 
 
 def grad_table(tensors, outs=None) -> GradTable:
@@ -512,15 +532,15 @@ def grad_table(tensors, outs=None) -> GradTable:
     return GradTable(tensors, outs)
 
 
-def _table(grads) -> GradTable:
-    if not isinstance(grads, GradTable):
-        return GradTable(grads)
-    if grads.device.index != torch.cuda.current_device():
-        raise ValueError(f"expected gradients on the current GPU, got {grads.device}")
-    stream = torch.cuda.current_stream()
-    if stream != grads._stream:  # the table's memory must outlive the work of this stream too
-        grads.device_table.record_stream(stream)
-    return grads
+def _table(grads):
+    """(table, current stream) of a GradTable or a list of tensors."""
+    t = grads if isinstance(grads, GradTable) else GradTable(grads)
+    if t.device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"expected gradients on the current GPU, got {t.device}")
+    stream = torch._C._cuda_getCurrentRawStream(t.device.index)
+    if stream != t._stream:  # the table's memory must outlive this stream's work too
+        t.device_table.record_stream(torch.cuda.current_stream())
+    return t, stream
 
 
 def _grad_workspace(t: GradTable) -> torch.Tensor:
@@ -530,11 +550,11 @@ def _grad_workspace(t: GradTable) -> torch.Tensor:
 def grad_norm(grads) -> torch.Tensor:
     """Global 2-norm over all gradients (a GradTable or a list of tensors): a
     float32 scalar on the device."""
-    t = _table(grads)
+    t, stream = _table(grads)
     norm = torch.empty((), dtype=torch.float32, device=t.device)
     ws = _grad_workspace(t)
-    _fb._check(_fb.lib().fp8blk_grad_norm(_fb._ptr(t.device_table), t.n, t.chunks, _fb._ptr(norm),
-                                          _fb._ptr(ws), _GRAD_WORKSPACE_BYTES, _fb._stream()),
+    _fb._check(_fb.lib().fp8blk_grad_norm(_addr(t.device_table), t.n, t.chunks, _addr(norm),
+                                          _addr(ws), _GRAD_WORKSPACE_BYTES, stream),
                "grad_norm")
     return norm
 
@@ -543,20 +563,20 @@ def grad_clip(grads, norm: torch.Tensor, max_norm: float, eps: float = 1e-6) -> 
     """Scale every gradient by min(1, max_norm / (norm + eps)), norm a float32
     scalar on the device (e.g. reduced over ranks): in place, or into the
     table's outputs."""
-    t = _table(grads)
+    t, stream = _table(grads)
     _need(norm, torch.float32, "norm")
     if norm.numel() != 1 or norm.device != t.device:
         raise ValueError("norm must be one value on the gradients' device")
-    _fb._check(_fb.lib().fp8blk_grad_clip(_fb._ptr(t.device_table), t.n, t.chunks, _fb._ptr(norm), max_norm, eps,
-                                          _fb._stream()), "grad_clip")
+    _fb._check(_fb.lib().fp8blk_grad_clip(_addr(t.device_table), t.n, t.chunks, _addr(norm), max_norm, eps,
+                                          stream), "grad_clip")
 
 
 def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6) -> torch.Tensor:
     """grad_norm and grad_clip by it; returns the norm before clipping."""
-    t = _table(grads)
+    t, stream = _table(grads)
     norm = torch.empty((), dtype=torch.float32, device=t.device)
     ws = _grad_workspace(t)
-    _fb._check(_fb.lib().fp8blk_grad_clip_norm(_fb._ptr(t.device_table), t.n, t.chunks, max_norm, eps, _fb._ptr(norm),
-                                               _fb._ptr(ws), _GRAD_WORKSPACE_BYTES, _fb._stream()),
+    _fb._check(_fb.lib().fp8blk_grad_clip_norm(_addr(t.device_table), t.n, t.chunks, max_norm, eps, _addr(norm),
+                                               _addr(ws), _GRAD_WORKSPACE_BYTES, stream),
                "clip_grad_norm")
     return norm

@@ -137,7 +137,8 @@ fp8blk_status_t fp8blk_moe_combine_backward(const void* dy, int64_t lddy, const 
  * All in FP32; x' enters the second norm, and n the quantizer, before being
  * rounded for storage.  A tile's scale is fl32(amax / 448) of its FP32 values
  * (the smallest power of two not below amax / 448 with FP8BLK_SCALE_POW2 in
- * flags; 1 for a tile of zeros) and its codes are E4M3(fl32(n / s)).
+ * flags; 1 for a tile of zeros) and its codes are E4M3(n / s), the quotient
+ * within one unit in the last place of FP32.
  *   x      [M][C] BF16 or FP32, pitch ldx.
  *   f      [M][C] BF16, pitch ldf, or NULL.
  *   w_post, w_pre  [C], element aligned, or NULL.
