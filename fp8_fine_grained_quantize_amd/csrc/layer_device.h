@@ -27,19 +27,94 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ uint16_t from_f32<uint16_t>(float v) { return (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu); }
 
-// 16 bytes at an address aligned only to the element: one dwordx4 access (the
-// hardware takes unaligned global accesses).
-struct __attribute__((packed, aligned(2))) U128 {
-  uint32_t w[4];
+// Pointers to global memory, told to the compiler where it cannot see it.
+template <typename T>
+using Global = __attribute__((address_space(1))) T;
+template <typename T>
+__device__ __forceinline__ Global<T>* global(T* p) { return (Global<T>*)p; }
+
+// V elements of either type at an address aligned only to the element (the
+// hardware takes unaligned global accesses), as FP32.  NT: streamed past the
+// caches (see kStreamBytes in layer_host.h).
+template <int N>
+struct Words {
+  typedef uint32_t type __attribute__((ext_vector_type(N)));
+  typedef type unaligned __attribute__((aligned(2)));
 };
-__device__ __forceinline__ uint4 load_u128(const void* p) {
-  const U128 u = *reinterpret_cast<const U128*>(p);
-  return make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]);
+template <typename T, int V>
+using RawV = typename Words<V * (int)sizeof(T) / 4>::type;
+template <int V, bool NT, typename T>
+__device__ __forceinline__ RawV<T, V> load_raw(const Global<const T>* p) {
+  auto* q = (const Global<const typename Words<V * (int)sizeof(T) / 4>::unaligned>*)p;
+  return NT ? __builtin_nontemporal_load(q) : *q;
 }
+template <typename T, int V>
+__device__ __forceinline__ void unpack_v(const RawV<T, V>& r, float (&v)[V]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = __uint_as_float(r[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+      v[2 * j] = bf16_lo(r[j]);
+      v[2 * j + 1] = bf16_hi(r[j]);
+    }
+  }
+}
+template <bool NT, int N>
+__device__ __forceinline__ void store_words(Global<void>* p, const typename Words<N>::type& r) {
+  auto* q = (Global<typename Words<N>::unaligned>*)p;
+  if (NT) __builtin_nontemporal_store(r, q);
+  else *q = r;
+}
+template <int V, bool NT>
+__device__ __forceinline__ void store_v(Global<float>* p, const float (&v)[V]) {
+  typename Words<V>::type r;
+#pragma unroll
+  for (int j = 0; j < V; ++j) r[j] = __float_as_uint(v[j]);
+  store_words<NT, V>(p, r);
+}
+template <int V, bool NT>
+__device__ __forceinline__ void store_v(Global<uint16_t>* p, const float (&v)[V]) {
+  typename Words<V / 2>::type r;
+#pragma unroll
+  for (int j = 0; j < V / 2; ++j) r[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+  store_words<NT, V / 2>(p, r);
+}
+// The same where only `avail` elements are left in the row: those past its end
+// read as zero and are not touched in memory.  EXACT: rows are multiples of V.
+template <int V, bool EXACT, bool NT, typename T>
+__device__ __forceinline__ RawV<T, V> load_end(const T* p, int64_t avail) {
+  if (EXACT || avail >= V) return load_raw<V, NT>(global(p));
+  RawV<T, V> r{};
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (j >= avail) continue;
+    if constexpr (sizeof(T) == 4) r[j] = __float_as_uint(p[j]);
+    else r[j >> 1] |= (uint32_t)p[j] << ((j & 1) * 16);
+  }
+  return r;
+}
+template <int V, bool EXACT, bool NT, typename T>
+__device__ __forceinline__ void store_end(T* p, int64_t avail, const float (&v)[V]) {
+  if (EXACT || avail >= V) {
+    store_v<V, NT>(global(p), v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j < avail) p[j] = from_f32<T>(v[j]);
+  }
+}
+
+template <bool NT = false>
+__device__ __forceinline__ uint4 load_u128(const void* p) {
+  auto* q = (const Global<const Words<4>::unaligned>*)p;
+  const Words<4>::type r = NT ? __builtin_nontemporal_load(q) : *q;
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+template <bool NT = false>
 __device__ __forceinline__ void store_u128(void* p, const uint4& v) {
-  U128 u;
-  u.w[0] = v.x; u.w[1] = v.y; u.w[2] = v.z; u.w[3] = v.w;
-  *reinterpret_cast<U128*>(p) = u;
+  store_words<NT, 4>((Global<void>*)p, Words<4>::type{v.x, v.y, v.z, v.w});
 }
 
 // Eight raw elements of a row: one 16-byte word for BF16, two for FP32.
@@ -58,12 +133,15 @@ __device__ __forceinline__ void zero8(Raw8<uint16_t>& r) { r.a = make_uint4(0u, 
 __device__ __forceinline__ void zero8(Raw8<float>& r) { r.a = r.b = make_uint4(0u, 0u, 0u, 0u); }
 
 // `avail` elements are left in the row; those past its end read as zero and
-// are not touched in memory.
+// are not touched in memory.  EXACT: the row is a multiple of eight elements,
+// so a chunk is all there or not at all (without the element-wise ends the
+// kernels are a third of the size).
+template <bool EXACT, bool NT>
 __device__ __forceinline__ void load8(Raw8<uint16_t>& r, const uint16_t* p, int64_t avail) {
   zero8(r);
-  if (avail >= 8) {
-    r.a = load_u128(p);
-  } else {
+  if (EXACT ? avail > 0 : avail >= 8) {
+    r.a = load_u128<NT>(p);
+  } else if (!EXACT) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -71,12 +149,13 @@ __device__ __forceinline__ void load8(Raw8<uint16_t>& r, const uint16_t* p, int6
     r.a = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
+template <bool EXACT, bool NT>
 __device__ __forceinline__ void load8(Raw8<float>& r, const float* p, int64_t avail) {
   zero8(r);
-  if (avail >= 8) {
-    r.a = load_u128(p);
-    r.b = load_u128(p + 4);
-  } else {
+  if (EXACT ? avail > 0 : avail >= 8) {
+    r.a = load_u128<NT>(p);
+    r.b = load_u128<NT>(p + 4);
+  } else if (!EXACT) {
     uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -99,22 +178,24 @@ __device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
   v[6] = __uint_as_float(r.b.z); v[7] = __uint_as_float(r.b.w);
 }
 
+template <bool EXACT, bool NT>
 __device__ __forceinline__ void store8(uint16_t* p, int64_t avail, const float (&v)[8]) {
   const uint4 w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-  if (avail >= 8) {
-    store_u128(p, w);
-  } else {
+  if (EXACT ? avail > 0 : avail >= 8) {
+    store_u128<NT>(p, w);
+  } else if (!EXACT) {
     const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j < avail) p[j] = (uint16_t)(a[j >> 1] >> ((j & 1) * 16));
   }
 }
+template <bool EXACT, bool NT>
 __device__ __forceinline__ void store8(float* p, int64_t avail, const float (&v)[8]) {
-  if (avail >= 8) {
-    store_u128(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
-    store_u128(p + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
-  } else {
+  if (EXACT ? avail > 0 : avail >= 8) {
+    store_u128<NT>(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+    store_u128<NT>(p + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+  } else if (!EXACT) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j < avail) p[j] = v[j];
@@ -143,9 +224,20 @@ __device__ __forceinline__ float wave_sum(float v) {
   const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(h[0]) + __uint_as_float(h[1]);
 }
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  v += dpp_f64<0xB1>(v);
+  v += dpp_f64<0x4E>(v);
+  v += dpp_f64<0x141>(v);
+  v += dpp_f64<0x140>(v);
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
   return v;
 }
 

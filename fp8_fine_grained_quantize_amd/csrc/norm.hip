@@ -15,6 +15,7 @@
 #include "../../include/libfp8blk_layer.h"
 #include "host_common.h"
 #include "layer_device.h"
+#include "layer_host.h"
 
 namespace fp8blk {
 
@@ -38,14 +39,15 @@ struct NormFwd {
 };
 
 // Eight parameters of either type from an element-aligned vector.
+template <bool EXACT>
 __device__ __forceinline__ void load_param8(const void* p, bool f32, int64_t col, int64_t avail, float (&v)[8]) {
   if (f32) {
     Raw8<float> r;
-    load8(r, reinterpret_cast<const float*>(p) + col, avail);
+    load8<EXACT, false>(r, reinterpret_cast<const float*>(p) + col, avail);
     unpack8(r, v);
   } else {
     Raw8<uint16_t> r;
-    load8(r, reinterpret_cast<const uint16_t*>(p) + col, avail);
+    load8<EXACT, false>(r, reinterpret_cast<const uint16_t*>(p) + col, avail);
     unpack8(r, v);
   }
 }
@@ -74,11 +76,13 @@ __device__ __forceinline__ uint2 quantize_tile(const float (&n)[8], float& s) {
   return c;
 }
 
+template <bool EXACT, bool NT>
 __device__ __forceinline__ void store_codes8(uint8_t* p, int64_t avail, uint2 c) {
-  if (avail >= 8) {
-    *reinterpret_cast<uint2*>(p) = c;
+  if (EXACT ? avail > 0 : avail >= 8) {
+    store_words<NT, 2>((Global<void>*)p, Words<2>::type{c.x, c.y});
     return;
   }
+  if (EXACT) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     if (j < avail) p[j] = (uint8_t)((j < 4 ? c.x : c.y) >> ((j & 3) * 8));
@@ -88,20 +92,20 @@ __device__ __forceinline__ void store_codes8(uint8_t* p, int64_t avail, uint2 c)
 __device__ __forceinline__ float rstd_of(float sum, float inv_c, float eps) { return 1.0f / sqrtf(sum * inv_c + eps); }
 
 // What a lane reads of one row, before it is unpacked.
-template <typename TX, int NCH, bool GATE_ROW>
+template <typename TX, int NCH, bool GATE_ROW, bool EXACT>
 struct NormRow {
   Raw8<TX> x[NCH];
   Raw8<uint16_t> f[NCH], gate[GATE_ROW ? NCH : 1];
 };
 
-template <typename TX, int NCH, bool GATE_ROW>
-__device__ __forceinline__ void load_row(NormRow<TX, NCH, GATE_ROW>& r, const NormFwd& a, int64_t row) {
+template <bool NT, typename TX, int NCH, bool GATE_ROW, bool EXACT>
+__device__ __forceinline__ void load_row(NormRow<TX, NCH, GATE_ROW, EXACT>& r, const NormFwd& a, int64_t row) {
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * blockDim.x) * 8, avail = a.C - col;
-    load8(r.x[c], reinterpret_cast<const TX*>(a.x) + row * a.ldx + col, avail);
-    if (a.f != nullptr) load8(r.f[c], a.f + row * a.ldf + col, avail);
-    if (GATE_ROW) load8(r.gate[c], reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg + col, avail);
+    load8<EXACT, NT>(r.x[c], reinterpret_cast<const TX*>(a.x) + row * a.ldx + col, avail);
+    if (a.f != nullptr) load8<EXACT, NT>(r.f[c], a.f + row * a.ldf + col, avail);
+    if (GATE_ROW) load8<EXACT, NT>(r.gate[c], reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg + col, avail);
   }
 }
 
@@ -110,7 +114,7 @@ __device__ __forceinline__ void load_row(NormRow<TX, NCH, GATE_ROW>& r, const No
 // 1x128 tile is one row of 16 lanes, and the parameters of its channels.  The
 // next row is loaded before the present one is worked on: the reductions and
 // stores of one row cover the other's way from HBM.
-template <typename TX, int NCH, bool GATE_ROW>
+template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT>
 __global__ __launch_bounds__(512) void k_residual_norm(const NormFwd a) {
   __shared__ float red[2][2][16];
   const int nt = blockDim.x, nw = nt >> 6;
@@ -124,23 +128,23 @@ __global__ __launch_bounds__(512) void k_residual_norm(const NormFwd a) {
     for (int i = 0; i < 8; ++i) pc[c][i] = a.alpha;
     float w[8];
     if (a.w_post != nullptr) {
-      load_param8(a.w_post, pf32, col, avail, w);
+      load_param8<EXACT>(a.w_post, pf32, col, avail, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) pc[c][i] *= w[i];
     }
     if (a.gate != nullptr && !GATE_ROW) {
-      load_param8(a.gate, pf32, col, avail, w);
+      load_param8<EXACT>(a.gate, pf32, col, avail, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) pc[c][i] *= w[i];
     }
-    if (a.w_pre != nullptr) load_param8(a.w_pre, pf32, col, avail, wn[c]);
+    if (a.w_pre != nullptr) load_param8<EXACT>(a.w_pre, pf32, col, avail, wn[c]);
   }
-  NormRow<TX, NCH, GATE_ROW> next;
-  load_row(next, a, blockIdx.x);
+  NormRow<TX, NCH, GATE_ROW, EXACT> next;
+  load_row<NT>(next, a, blockIdx.x);
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
-    const NormRow<TX, NCH, GATE_ROW> cur = next;
-    if (row + gridDim.x < a.M) load_row(next, a, row + gridDim.x);
+    const NormRow<TX, NCH, GATE_ROW, EXACT> cur = next;
+    if (row + gridDim.x < a.M) load_row<NT>(next, a, row + gridDim.x);
     float z[NCH][8];
 #pragma unroll
     for (int c = 0; c < NCH; ++c) unpack8(cur.x[c], z[c]);
@@ -172,7 +176,7 @@ __global__ __launch_bounds__(512) void k_residual_norm(const NormFwd a) {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[c][i] = __builtin_fmaf(f[i] * r, pc[c][i], z[c][i]);
-        store8(reinterpret_cast<TX*>(a.x_out) + row * a.ldxo + col, a.C - col, z[c]);
+        store8<EXACT, NT>(reinterpret_cast<TX*>(a.x_out) + row * a.ldxo + col, a.C - col, z[c]);
       }
     }
     if (a.w_pre == nullptr) continue;
@@ -189,12 +193,12 @@ __global__ __launch_bounds__(512) void k_residual_norm(const NormFwd a) {
       const int64_t chunk = (int64_t)threadIdx.x + (int64_t)c * nt, col = chunk * 8, avail = a.C - col;
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[c][i] = z[c][i] * r * wn[c][i];
-      if (a.n != nullptr) store8(a.n + row * a.ldn + col, avail, z[c]);
+      if (a.n != nullptr) store8<EXACT, NT>(a.n + row * a.ldn + col, avail, z[c]);
       if (a.q != nullptr) {
         float s;
         const uint2 codes = a.flags & FP8BLK_SCALE_POW2 ? quantize_tile<true>(z[c], s) : quantize_tile<false>(z[c], s);
         if (avail > 0) {
-          store_codes8(a.q + row * a.ldq + col, avail, codes);
+          store_codes8<EXACT, NT>(a.q + row * a.ldq + col, avail, codes);
           if ((threadIdx.x & 15) == 0) a.s[(chunk >> 4) * a.M + row] = s;
         }
       }
@@ -243,7 +247,7 @@ struct NormBwdChunk {
   Raw8<uint16_t> dn, f, gate;
 };
 
-template <typename TX, bool GATE_ROW>
+template <bool EXACT, bool NT, typename TX, bool GATE_ROW>
 __device__ __forceinline__ void load_chunk(NormBwdChunk<TX, GATE_ROW>& r, const NormBwd& a, int64_t row, int64_t col) {
   const int64_t avail = a.C - col;
   zero8(r.x);
@@ -251,16 +255,16 @@ __device__ __forceinline__ void load_chunk(NormBwdChunk<TX, GATE_ROW>& r, const 
   zero8(r.dn);
   zero8(r.f);
   if (a.w_pre != nullptr) {
-    load8(r.x, reinterpret_cast<const TX*>(a.x) + row * a.ldx + col, avail);
-    load8(r.dn, a.dn + row * a.lddn + col, avail);
+    load8<EXACT, NT>(r.x, reinterpret_cast<const TX*>(a.x) + row * a.ldx + col, avail);
+    load8<EXACT, NT>(r.dn, a.dn + row * a.lddn + col, avail);
   }
-  if (a.dxo != nullptr) load8(r.dxo, reinterpret_cast<const TX*>(a.dxo) + row * a.lddxo + col, avail);
-  if (a.f != nullptr) load8(r.f, a.f + row * a.ldf + col, avail);
-  if (GATE_ROW) load8(r.gate, reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg + col, avail);
+  if (a.dxo != nullptr) load8<EXACT, NT>(r.dxo, reinterpret_cast<const TX*>(a.dxo) + row * a.lddxo + col, avail);
+  if (a.f != nullptr) load8<EXACT, NT>(r.f, a.f + row * a.ldf + col, avail);
+  if (GATE_ROW) load8<EXACT, NT>(r.gate, reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg + col, avail);
 }
 
 // The parameters of a chunk: alpha * w_post * (gate per channel), and w_pre.
-template <bool GATE_ROW>
+template <bool GATE_ROW, bool EXACT>
 __device__ __forceinline__ void load_factors(const NormBwd& a, int64_t col, float (&pc)[8], float (&wn)[8]) {
   const bool pf32 = (a.flags & FP8BLK_NORM_PARAM_F32) != 0;
   const int64_t avail = a.C - col;
@@ -271,23 +275,23 @@ __device__ __forceinline__ void load_factors(const NormBwd& a, int64_t col, floa
     wn[i] = 0.0f;
   }
   if (a.w_post != nullptr) {
-    load_param8(a.w_post, pf32, col, avail, w);
+    load_param8<EXACT>(a.w_post, pf32, col, avail, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) pc[i] *= w[i];
   }
   if (a.gate != nullptr && !GATE_ROW) {
-    load_param8(a.gate, pf32, col, avail, w);
+    load_param8<EXACT>(a.gate, pf32, col, avail, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) pc[i] *= w[i];
   }
-  if (a.w_pre != nullptr) load_param8(a.w_pre, pf32, col, avail, wn);
+  if (a.w_pre != nullptr) load_param8<EXACT>(a.w_pre, pf32, col, avail, wn);
 }
 
 // With one or two chunks per lane the factors and the next row are held in
 // registers.  Where they would not fit beside the accumulators (four chunks, C
 // above 8192; two of FP32 x with a gate per token) factors and rows are read
 // chunk by chunk, and once more (from L2) after the reduction.
-template <typename TX, int NCH, bool GATE_ROW>
+template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT>
 __global__ __launch_bounds__(512) void k_residual_norm_backward(const NormBwd a) {
   constexpr bool HOLD = NCH == 1 || (NCH == 2 && !(GATE_ROW && sizeof(TX) == 4));
   constexpr int NH = HOLD ? NCH : 1;
@@ -302,8 +306,8 @@ __global__ __launch_bounds__(512) void k_residual_norm_backward(const NormBwd a)
 #pragma unroll
     for (int i = 0; i < 8; ++i) s_pre[c][i] = s_post[c][i] = 0.0f;
     if (HOLD) {
-      load_factors<GATE_ROW>(a, col, pc_[c], wn_[c]);
-      load_chunk(next[c], a, blockIdx.x, col);
+      load_factors<GATE_ROW, EXACT>(a, col, pc_[c], wn_[c]);
+      load_chunk<EXACT, NT>(next[c], a, blockIdx.x, col);
     }
   }
   int turn = 0;
@@ -315,19 +319,20 @@ __global__ __launch_bounds__(512) void k_residual_norm_backward(const NormBwd a)
       for (int c = 0; c < NH; ++c) {
         cur_[c] = next[c];
         if (row + gridDim.x < a.M)
-          load_chunk(next[c], a, row + gridDim.x, ((int64_t)threadIdx.x + (int64_t)c * nt) * 8);
+          load_chunk<EXACT, NT>(next[c], a, row + gridDim.x, ((int64_t)threadIdx.x + (int64_t)c * nt) * 8);
       }
     }
     float sum[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
+      if (!HOLD) __builtin_amdgcn_sched_barrier(0);  // one chunk after the other
       float(&pc)[8] = pc_[HOLD ? c : 0];
       float(&wn)[8] = wn_[HOLD ? c : 0];
       NormBwdChunk<TX, GATE_ROW>& cur = cur_[HOLD ? c : 0];
       if (!HOLD) {
         const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
-        load_factors<GATE_ROW>(a, col, pc, wn);
-        load_chunk(cur, a, row, col);
+        load_factors<GATE_ROW, EXACT>(a, col, pc, wn);
+        load_chunk<EXACT, NT && HOLD>(cur, a, row, col);
       }
       float h[8], v[8], g[8], hf[8], gt[8];
       unpack8(cur.x, h);
@@ -352,13 +357,14 @@ __global__ __launch_bounds__(512) void k_residual_norm_backward(const NormBwd a)
     const float m_post = a.w_post != nullptr ? (sum[1] - r_pre * m * sum[2]) * inv_c : 0.0f;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
+      if (!HOLD) __builtin_amdgcn_sched_barrier(0);
       const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8, avail = a.C - col;
       float(&pc)[8] = pc_[HOLD ? c : 0];
       float(&wn)[8] = wn_[HOLD ? c : 0];
       NormBwdChunk<TX, GATE_ROW>& cur = cur_[HOLD ? c : 0];
       if (!HOLD) {
-        load_factors<GATE_ROW>(a, col, pc, wn);
-        load_chunk(cur, a, row, col);
+        load_factors<GATE_ROW, EXACT>(a, col, pc, wn);
+        load_chunk<EXACT, NT && HOLD>(cur, a, row, col);
       }
       float h[8], v[8], g[8];
       unpack8(cur.x, h);
@@ -367,7 +373,7 @@ __global__ __launch_bounds__(512) void k_residual_norm_backward(const NormBwd a)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         g[i] = __builtin_fmaf(r_pre, __builtin_fmaf(-(h[i] * r_pre), m, v[i] * wn[i]), g[i]);
-      if (a.dx != nullptr) store8(reinterpret_cast<TX*>(a.dx) + row * a.lddx + col, avail, g);
+      if (a.dx != nullptr) store8<EXACT, NT>(reinterpret_cast<TX*>(a.dx) + row * a.lddx + col, avail, g);
       if (a.f == nullptr) continue;
       unpack8(cur.f, h);
       float gt[8];
@@ -384,16 +390,16 @@ __global__ __launch_bounds__(512) void k_residual_norm_backward(const NormBwd a)
       if (GATE_ROW) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= pc[i];
-        store8(a.dgate_row + row * a.lddg + col, avail, v);
+        store8<EXACT, NT>(a.dgate_row + row * a.lddg + col, avail, v);
       }
-      store8(a.df + row * a.lddf + col, avail, g);
+      store8<EXACT, NT>(a.df + row * a.lddf + col, avail, g);
     }
   }
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8, avail = a.C - col;
-    if (a.part_pre != nullptr) store8(a.part_pre + (int64_t)blockIdx.x * a.C + col, avail, s_pre[c]);
-    if (a.part_post != nullptr) store8(a.part_post + (int64_t)blockIdx.x * a.C + col, avail, s_post[c]);
+    if (a.part_pre != nullptr) store8<EXACT, false>(a.part_pre + (int64_t)blockIdx.x * a.C + col, avail, s_pre[c]);
+    if (a.part_post != nullptr) store8<EXACT, false>(a.part_post + (int64_t)blockIdx.x * a.C + col, avail, s_post[c]);
   }
 }
 
@@ -462,15 +468,40 @@ inline int64_t norm_blocks(int64_t M, int64_t C, int64_t per_cu) {
 inline int64_t norm_forward_blocks(int64_t M, int64_t C) { return norm_blocks(M, C, 1024); }
 inline int64_t norm_backward_blocks(int64_t M, int64_t C) { return norm_blocks(M, C, 512); }
 
-template <typename TX, int NCH, bool GATE_ROW>
-void launch_forward(const NormFwd& a, hipStream_t stream) {
-  hipLaunchKernelGGL((k_residual_norm<TX, NCH, GATE_ROW>), dim3((unsigned)norm_forward_blocks(a.M, a.C)),
+template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT>
+void launch(const NormFwd& a, hipStream_t stream) {
+  hipLaunchKernelGGL((k_residual_norm<TX, NCH, GATE_ROW, EXACT, NT>), dim3((unsigned)norm_forward_blocks(a.M, a.C)),
                      dim3((unsigned)norm_lanes(a.C)), 0, stream, a);
 }
-template <typename TX, int NCH, bool GATE_ROW>
-void launch_backward(const NormBwd& a, hipStream_t stream) {
-  hipLaunchKernelGGL((k_residual_norm_backward<TX, NCH, GATE_ROW>), dim3((unsigned)norm_backward_blocks(a.M, a.C)),
-                     dim3((unsigned)norm_lanes(a.C)), 0, stream, a);
+template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT>
+void launch(const NormBwd& a, hipStream_t stream) {
+  hipLaunchKernelGGL((k_residual_norm_backward<TX, NCH, GATE_ROW, EXACT, NT>),
+                     dim3((unsigned)norm_backward_blocks(a.M, a.C)), dim3((unsigned)norm_lanes(a.C)), 0, stream, a);
+}
+
+// The kernel for the arguments' types and sizes.
+template <typename TX, bool GATE_ROW, bool EXACT, bool NT, typename A>
+void launch_chunks(const A& a, hipStream_t stream) {
+  switch (norm_chunks(a.C)) {
+    case 1: return launch<TX, 1, GATE_ROW, EXACT, NT>(a, stream);
+    case 2: return launch<TX, 2, GATE_ROW, EXACT, NT>(a, stream);
+    default: return launch<TX, 4, GATE_ROW, EXACT, NT>(a, stream);
+  }
+}
+template <typename TX, bool GATE_ROW, typename A>
+void launch_exact(const A& a, bool nt, hipStream_t stream) {
+  if (a.C % 8 != 0) return launch_chunks<TX, GATE_ROW, false, false>(a, stream);
+  if (nt) return launch_chunks<TX, GATE_ROW, true, true>(a, stream);
+  return launch_chunks<TX, GATE_ROW, true, false>(a, stream);
+}
+// moved: bytes that the call reads and writes.
+template <typename A>
+void launch_norm(const A& a, int64_t moved, hipStream_t stream) {
+  const bool nt = moved >= kStreamBytes, gate_row = (a.flags & FP8BLK_NORM_GATE_ROW) != 0;
+  if (a.flags & FP8BLK_NORM_RES_F32)
+    gate_row ? launch_exact<float, true>(a, nt, stream) : launch_exact<float, false>(a, nt, stream);
+  else
+    gate_row ? launch_exact<uint16_t, true>(a, nt, stream) : launch_exact<uint16_t, false>(a, nt, stream);
 }
 
 }  // namespace fp8blk
@@ -509,12 +540,9 @@ extern "C" fp8blk_status_t fp8blk_residual_norm(int64_t M, int64_t C, const void
   if ((flags & FP8BLK_SCALE_POW2) && q == nullptr) return FP8BLK_ERR_INVALID_ARG;
   const NormFwd a{x, f, w_post, gate, w_pre, x_out, n, q, s, rstd_post, rstd_pre,
                   M, C, ldx, ldf, ldg, ldxo, ldn, ldq, alpha, eps, flags};
-#define FP8BLK_NORM_PICK(GO, TX, GR) \
-  (norm_chunks(C) == 1 ? GO<TX, 1, GR> : norm_chunks(C) == 2 ? GO<TX, 2, GR> : GO<TX, 4, GR>)
-  auto* go = xf ? (gr ? FP8BLK_NORM_PICK(launch_forward, float, true) : FP8BLK_NORM_PICK(launch_forward, float, false))
-                : (gr ? FP8BLK_NORM_PICK(launch_forward, uint16_t, true)
-                      : FP8BLK_NORM_PICK(launch_forward, uint16_t, false));
-  go(a, as_stream(stream));
+  const int64_t xe = xf ? 4 : 2;
+  launch_norm(a, M * C * (xe + (f != nullptr ? 2 + xe : 0) + (gr ? 2 : 0) + (n != nullptr ? 2 : 0) + (q != nullptr ? 1 : 0)),
+              as_stream(stream));
   return launch_status();
 }
 
@@ -572,10 +600,8 @@ extern "C" fp8blk_status_t fp8blk_residual_norm_backward(
     const NormBwd a{x_out, dx_out, dn, rstd_pre, w_pre, f, rstd_post, w_post, gate, dx, df,
                     gr ? reinterpret_cast<uint16_t*>(dgate) : nullptr, part_pre, part_post,
                     M, C, ldx, lddxo, lddn, ldf, ldg, lddx, lddf, lddg, alpha, flags};
-    auto* go = xf ? (gr ? FP8BLK_NORM_PICK(launch_backward, float, true) : FP8BLK_NORM_PICK(launch_backward, float, false))
-                  : (gr ? FP8BLK_NORM_PICK(launch_backward, uint16_t, true)
-                        : FP8BLK_NORM_PICK(launch_backward, uint16_t, false));
-    go(a, as_stream(stream));
+    launch_norm(a, M * C * ((pre ? xe + 2 : 0) + (dx_out != nullptr ? xe : 0) + (dx != nullptr ? xe : 0) +
+                            (f != nullptr ? 4 : 0) + (gr ? 4 : 0)), as_stream(stream));
     const fp8blk_status_t st = launch_status();
     if (st != FP8BLK_OK) return st;
   }
