@@ -56,9 +56,26 @@ __global__ __launch_bounds__(1024) void k_moe_count(const ID* __restrict__ ids, 
   for (int e = threadIdx.x; e < E; e += blockDim.x) hist[(int64_t)blockIdx.x * E + e] = lds[e];
 }
 
-// nb workgroups of nw waves; each wave takes per_wave (a multiple of 64)
-// consecutive pairs.  LDS: cnt[nw][E+1], scan[2][nw] and, with hist and E at most
-// half of blockDim, 2 * blockDim partial counts.  blockDim >= E.
+// Inclusive sum over the wave's 64 lanes by DPP row shifts and broadcasts: no
+// lane exchange through LDS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int32_t dpp_add(int32_t v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int32_t wave_scan(int32_t v) {
+  v = dpp_add<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8: inside rows of 16 lanes
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
+  return dpp_add<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
+}
+
+// nb workgroups of nw waves (at most kSortWaves); each wave takes per_wave (a
+// multiple of 64) consecutive pairs.  LDS: cnt[nw][E+1], scan[2][nw] and, with
+// hist and E at most half of blockDim, 2 * blockDim partial counts.
+// blockDim > E: thread e deals with the bucket of expert e, thread E with that
+// of the dropped pairs.
 template <typename ID>
 __global__ __launch_bounds__(1024) void k_moe_sort(const ID* __restrict__ ids, int64_t ld, uint32_t K, uint32_t P,
                                                     int E, int nbits, uint32_t per_wave,
@@ -68,83 +85,79 @@ __global__ __launch_bounds__(1024) void k_moe_sort(const ID* __restrict__ ids, i
   const int nw = blockDim.x >> 6;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int EB = E + 1;
-  int32_t* cnt = lds;                    // [nw][E+1]
-  int32_t* scan = lds + nw * EB;         // [2][nw]
+  int32_t* cnt = lds;             // [nw][E+1]
+  int32_t* scan = lds + nw * EB;  // [2][nw]
   const uint32_t b0 = blockIdx.x * per_wave * nw;
   const uint32_t w0 = min(b0 + wave * per_wave, P);
   const uint32_t w1 = min(w0 + per_wave, P);
-
-  for (int i = threadIdx.x; i < nw * EB; i += blockDim.x) cnt[i] = 0;
-  __syncthreads();
-  for (uint32_t p = w0 + lane; p < w1; p += 64) atomicAdd(&cnt[wave * EB + sort_key(ids, ld, K, p, E)], 1);
-  __syncthreads();
-
-  // Thread e: expert e's pairs in all workgroups, and in those before this one.
   const int e = threadIdx.x;
+
+  // Expert e's pairs in all workgroups, and in those before this one: groups
+  // of EP threads share the workgroups' counts, eight loads in flight.
+  const int EP = (E + 63) & ~63, groups = hist != nullptr && EP > 0 ? (int)blockDim.x / EP : 0;
   int32_t total = 0, before = 0;
-  if (hist == nullptr) {
-    if (e < E)
-      for (int w = 0; w < nw; ++w) total += cnt[w * EB + e];
-  } else {
-    // groups of EP threads share the workgroups' counts, eight loads in flight
-    const int EP = (E + 63) & ~63, groups = EP > 0 ? (int)blockDim.x / EP : 0;
-    const int grp = EP > 0 ? e / EP : 0, ee = e - grp * EP;
+  if (groups > 0) {
+    const int grp = e / EP, ee = e - grp * EP;
     if (grp < groups && ee < E) {
-      for (uint32_t h0 = grp; h0 < gridDim.x; h0 += 8 * groups) {
+      const uint32_t last = gridDim.x - 1;
+      for (uint32_t h0 = grp; h0 <= last; h0 += 8 * groups) {
         int32_t h[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = h0 + i * groups < gridDim.x ? hist[(int64_t)(h0 + i * groups) * E + ee] : 0;
+        for (int i = 0; i < 8; ++i) h[i] = hist[(int64_t)min(h0 + i * groups, last) * E + ee];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          total += h[i];
+          total += h0 + i * groups <= last ? h[i] : 0;
           before += h0 + i * groups < blockIdx.x ? h[i] : 0;
         }
       }
     }
-    if (groups > 1) {
-      int32_t* part = scan + 2 * nw;  // [2][blockDim.x]
-      part[e] = total;
-      part[blockDim.x + e] = before;
-      __syncthreads();
-      total = before = 0;
-      if (e < E)
-        for (int i = 0; i < groups; ++i) {
-          total += part[i * EP + e];
-          before += part[blockDim.x + i * EP + e];
-        }
-    }
   }
-  const int32_t incl = wave_inclusive_sum(total), incl_before = wave_inclusive_sum(before);
+  for (int i = threadIdx.x; i < nw * EB; i += blockDim.x) cnt[i] = 0;
+  __syncthreads();
+  for (uint32_t p = w0 + lane; p < w1; p += 64) atomicAdd(&cnt[wave * EB + sort_key(ids, ld, K, p, E)], 1);
+  int32_t* part = scan + 2 * nw;  // [2][blockDim.x]
+  if (groups > 1) {
+    part[e] = total;
+    part[blockDim.x + e] = before;
+  }
+  __syncthreads();
+
+  int32_t c[kSortWaves];  // of bucket e in each wave
+  if (e <= E) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) c[w] = cnt[min(w, nw - 1) * EB + e];
+  }
+  if (groups > 1) {
+    total = before = 0;
+    if (e < E)
+      for (int i = 0; i < groups; ++i) {
+        total += part[i * EP + e];
+        before += part[blockDim.x + i * EP + e];
+      }
+  } else if (groups == 0 && e < E) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) total += w < nw ? c[w] : 0;
+  }
+  const int32_t incl = wave_scan(total), incl_before = wave_scan(before);
   if (lane == 63) {
     scan[wave] = incl;
     scan[nw + wave] = incl_before;
   }
   __syncthreads();
   int32_t off = incl - total, kept = 0, kept_before = 0;
-  for (int w = 0; w < nw; ++w) {
+  for (int w = 0; w < EP >> 6; ++w) {  // the waves that hold experts
     off += w < wave ? scan[w] : 0;
     kept += scan[w];
     kept_before += scan[nw + w];
   }
-  if (blockIdx.x == 0) {
-    if (e < E) offsets[e] = off;
-    if (threadIdx.x == 0) offsets[E] = kept;
-  }
-  // The row at which each wave's pairs of each key start.
-  if (e < E) {
-    int32_t run = off + before;
-    for (int w = 0; w < nw; ++w) {
-      const int32_t c = cnt[w * EB + e];
-      cnt[w * EB + e] = run;
-      run += c;
-    }
-  }
-  if (threadIdx.x == 0) {
-    int32_t run = kept + (int32_t)min(b0, P) - kept_before;
-    for (int w = 0; w < nw; ++w) {
-      const int32_t c = cnt[w * EB + E];
-      cnt[w * EB + E] = run;
-      run += c;
+  if (e <= E) {
+    if (blockIdx.x == 0) offsets[e] = e < E ? off : kept;
+    // the row at which each wave's pairs of the bucket start
+    int32_t run = e < E ? off + before : kept + (int32_t)min(b0, P) - kept_before;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      if (w < nw) cnt[w * EB + e] = run;
+      run += c[w];
     }
   }
   __syncthreads();
@@ -391,8 +404,7 @@ fp8blk_status_t launch_sort(const ID* ids, int64_t ld, uint32_t K, int64_t P, in
   if (P <= kSortOne) {
     int64_t nw = ceil_div(P, (int64_t)64);
     if (nw > kSortWaves) nw = kSortWaves;
-    if (nw < ceil_div((int64_t)E, (int64_t)64)) nw = ceil_div((int64_t)E, (int64_t)64);
-    if (nw < 1) nw = 1;
+    if (nw < ceil_div((int64_t)E + 1, (int64_t)64)) nw = ceil_div((int64_t)E + 1, (int64_t)64);
     const uint32_t per_wave = (uint32_t)(ceil_div(ceil_div(P, nw), (int64_t)64) * 64);
     const size_t lds = (size_t)(nw * (E + 1) + 2 * nw) * 4;
     hipLaunchKernelGGL(k_moe_sort<ID>, dim3(1), dim3((unsigned)nw * 64), lds, stream, ids, ld, K, (uint32_t)P, E, nbits,
