@@ -521,7 +521,7 @@ extern "C" fp8blk_status_t fp8blk_residual_norm(int64_t M, int64_t C, const void
   if ((w_post != nullptr || gate != nullptr || rstd_post != nullptr) && f == nullptr && M > 0 && C > 0)
     return FP8BLK_ERR_INVALID_ARG;
   if (M == 0 || C == 0) return FP8BLK_OK;
-  if (C > kNormMaxC || M > 0x3FFFFF) return FP8BLK_ERR_UNSUPPORTED;
+  if (C > kNormMaxC) return FP8BLK_ERR_UNSUPPORTED;
   if (f == nullptr && w_pre == nullptr) return FP8BLK_ERR_INVALID_ARG;
   if (!matrix_ok(x, M, C, ldx, xf ? 4 : 2)) return FP8BLK_ERR_INVALID_ARG;
   if (f != nullptr && (!matrix_ok(f, M, C, ldf, 2) || !matrix_ok(x_out, M, C, ldxo, xf ? 4 : 2)))

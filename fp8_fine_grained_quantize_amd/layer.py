@@ -102,8 +102,8 @@ def _ld(t: Optional[torch.Tensor]) -> int:
     ld, step = t.stride()
     if rows == 0 or cols == 0:
         return _fb._pad16(cols, t.element_size())
-    if step != 1 and cols != 1:
-        raise ValueError("expected a row-major matrix (unit column stride)")
+    if (step != 1 and cols != 1) or (ld < cols and rows != 1):
+        raise ValueError(f"expected a row-major matrix of separate rows, got strides {(ld, step)}")
     return ld if ld >= cols else cols
 
 

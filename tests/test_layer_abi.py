@@ -118,7 +118,6 @@ def test_norm_refuses():
         assert call(**bad) == INVALID, bad
     wide = 16385 + 7
     assert call(C=wide, ldx=16392, ldf=16392, ldxo=16392, ldn=16392, ldq=16400) == UNSUPPORTED
-    assert call(M=2 ** 22) == UNSUPPORTED
     assert call(M=0, x=NULL) == OK and call(C=0, x=NULL) == OK
 
 
@@ -165,7 +164,9 @@ def _build(*gs, nbytes=None):
 
 def test_grad_table():
     assert _build(_grad()) == (OK, 1)
-    assert _build(_grad(cols=8192, ld=8192, ldo=8192), _grad(out=0x200000, rows=3, cols=8192, ld=9000, ldo=8192)) == (OK, 4)
+    one = _build(_grad(cols=8192, ld=8192, ldo=8192))[1]
+    assert _build(_grad(cols=8192, ld=8192, ldo=8192), _grad(out=0x200000, rows=3, cols=8192, ld=9000, ldo=8192)) == \
+        (OK, 4 * one)
     assert _build() == (OK, 0)
     for bad in (dict(grad=0), dict(out=0), dict(grad=0x100002), dict(out=0x100001, flags=0), dict(rows=0), dict(cols=0),
                 dict(rows=-1), dict(ld=99), dict(ldo=99), dict(flags=4), dict(reserved=1), dict(flags=1),
@@ -226,3 +227,7 @@ def test_binding_refuses():
         fb.residual_norm(x, w_pre=torch.ones(64))
     with pytest.raises(ValueError):
         fb.grad_norm([x])
+    for bad in (x[:1].expand(4, 64), x.t(), x[:, ::2]):  # rows on top of each other, columns apart
+        with pytest.raises(ValueError):
+            layer._ld(bad)
+    assert layer._ld(x[:1].expand(1, 64)) == 64 and layer._ld(x[:, :40]) == 64 and layer._ld(None) == 0
