@@ -306,10 +306,12 @@ __global__ __launch_bounds__(256) void k_moe_combine(const TR* __restrict__ rows
 // Gradient of the combine: a workgroup takes one token, reads dy once, and for
 // eight experts at a time reads their rows, adds up the eight dot products
 // (FP32, lane by lane over the channels, then across lanes) and writes the
-// eight scaled copies of dy.
+// eight scaled copies of dy.  Up to 1024 lanes, so that each part of a row is
+// read and written in one piece (8192 tokens, 8 rows of 7168: 390 us, 396 with
+// 256 lanes).
 // ---------------------------------------------------------------------------
 template <typename TY, typename TR, typename TD, bool EXACT, bool NT>
-__global__ __launch_bounds__(256) void k_moe_combine_backward(const TY* __restrict__ dy, int64_t lddy,
+__global__ __launch_bounds__(1024) void k_moe_combine_backward(const TY* __restrict__ dy, int64_t lddy,
                                                                const TR* __restrict__ rows, int64_t ldr, int64_t T,
                                                                uint32_t K, int64_t C,
                                                                const int32_t* __restrict__ row_of,
@@ -369,15 +371,15 @@ __global__ __launch_bounds__(256) void k_moe_combine_backward(const TY* __restri
   }
 }
 
-// Workgroups per row and lanes per workgroup (a multiple of 64, at most 256)
-// so that the row's chunks fill the lanes evenly.
+// Parts of a row and lanes per part (a multiple of 64, at most `most`) so that
+// the row's chunks fill the lanes evenly.
 struct RowSplit {
   uint32_t segs, lanes;
 };
-inline RowSplit split_row(int64_t chunks) {
+inline RowSplit split_row(int64_t chunks, int64_t most = 256) {
   RowSplit r;
   if (chunks < 1) chunks = 1;
-  r.segs = (uint32_t)ceil_div(chunks, (int64_t)256);
+  r.segs = (uint32_t)ceil_div(chunks, most);
   r.lanes = (uint32_t)(ceil_div(ceil_div(chunks, (int64_t)r.segs), (int64_t)64) * 64);
   return r;
 }
@@ -469,7 +471,7 @@ template <typename TY, typename TR, typename TD, bool EXACT, bool NT>
 void launch_combine_backward(const CombineGradArgs& a, hipStream_t stream) {
   const int64_t V = sizeof(TY) == 2 && sizeof(TR) == 2 && sizeof(TD) == 2 ? 8 : 4;
   hipLaunchKernelGGL((k_moe_combine_backward<TY, TR, TD, EXACT, NT>), dim3((unsigned)a.T),
-                     dim3(split_row(ceil_div(a.C, V)).lanes), 0, stream, reinterpret_cast<const TY*>(a.dy), a.lddy,
+                     dim3(split_row(ceil_div(a.C, V), 1024).lanes), 0, stream, reinterpret_cast<const TY*>(a.dy), a.lddy,
                      reinterpret_cast<const TR*>(a.rows), a.ldr, a.T, a.K, a.C, a.row_of, a.w,
                      reinterpret_cast<TD*>(a.drows), a.lddr, a.dw);
 }
@@ -584,7 +586,7 @@ extern "C" fp8blk_status_t fp8blk_moe_combine_backward(const void* dy, int64_t l
       !matrix_ok(drows, T * K, C, lddr, df ? 4 : 2) || !vec_ok(row_of, T * K) || !vec_ok(weights, T * K) ||
       !vec_ok(dweights, T * K))
     return FP8BLK_ERR_INVALID_ARG;
-  if (!grid_ok(T, 256)) return FP8BLK_ERR_UNSUPPORTED;
+  if (!grid_ok(T, 1024)) return FP8BLK_ERR_UNSUPPORTED;
   using U = uint16_t;
   using F = float;
   const CombineGradArgs a{dy, lddy, rows, ldr, T, (uint32_t)K, C, row_of, weights, drows, lddr, dweights};

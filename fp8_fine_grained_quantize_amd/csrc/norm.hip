@@ -115,7 +115,7 @@ __device__ __forceinline__ void load_row(NormRow<TX, NCH, GATE_ROW, EXACT>& r, c
 // next row is loaded before the present one is worked on: the reductions and
 // stores of one row cover the other's way from HBM.
 template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT>
-__global__ __launch_bounds__(512) void k_residual_norm(const NormFwd a) {
+__global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
   __shared__ float red[2][2][16];
   const int nt = blockDim.x, nw = nt >> 6;
   const float inv_c = 1.0f / (float)a.C;
@@ -451,38 +451,50 @@ __global__ __launch_bounds__(1024) void k_norm_sums(const NormSums a, int first,
   }
 }
 
-// Chunks of eight channels per lane, 1, 2 or 4, and lanes of a row's workgroup,
-// at most 512.
-inline int norm_chunks(int64_t C) { return C > 8192 ? 4 : C > 4096 ? 2 : 1; }
-inline int norm_lanes(int64_t C) {
-  return (int)(ceil_div(ceil_div(C, (int64_t)8 * norm_chunks(C)), (int64_t)64) * 64);
+// Chunks of eight channels per lane, and lanes of a row's workgroup (a multiple
+// of 64).  Forward: one chunk up to 1024 lanes, then two (8192 x 7168 took 97 us
+// with 896 lanes of one chunk, 99 with 448 of two).  Gradient: at most 512
+// lanes, so that each may hold 256 registers (123 us with 448 lanes of two
+// chunks, 128 with 896 of one).
+inline int forward_chunks(int64_t C) { return C > 8192 ? 2 : 1; }
+inline int backward_chunks(int64_t C) { return C > 8192 ? 4 : C > 4096 ? 2 : 1; }
+inline int norm_lanes(int64_t C, int chunks) {
+  return (int)(ceil_div(ceil_div(C, (int64_t)8 * chunks), (int64_t)64) * 64);
 }
 
-// Workgroups of either kernel: as many as the GPU holds at a time, `per_cu`
-// lanes on a compute unit.
-inline int64_t norm_blocks(int64_t M, int64_t C, int64_t per_cu) {
-  int64_t n = per_cu / norm_lanes(C);
+// Workgroups of either kernel: `per_cu` lanes on a compute unit, as many as the
+// registers allow at a time.
+inline int64_t norm_blocks(int64_t M, int lanes, int64_t per_cu) {
+  int64_t n = per_cu / lanes;
   n = (n < 1 ? 1 : n) * device_cus();
   return M < n ? M : n;
 }
-inline int64_t norm_forward_blocks(int64_t M, int64_t C) { return norm_blocks(M, C, 1024); }
-inline int64_t norm_backward_blocks(int64_t M, int64_t C) { return norm_blocks(M, C, 512); }
+inline int64_t norm_backward_blocks(int64_t M, int64_t C) {
+  return norm_blocks(M, norm_lanes(C, backward_chunks(C)), 512);
+}
 
 template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT>
 void launch(const NormFwd& a, hipStream_t stream) {
-  hipLaunchKernelGGL((k_residual_norm<TX, NCH, GATE_ROW, EXACT, NT>), dim3((unsigned)norm_forward_blocks(a.M, a.C)),
-                     dim3((unsigned)norm_lanes(a.C)), 0, stream, a);
+  const int lanes = norm_lanes(a.C, NCH);
+  hipLaunchKernelGGL((k_residual_norm<TX, NCH, GATE_ROW, EXACT, NT>), dim3((unsigned)norm_blocks(a.M, lanes, 2048)),
+                     dim3((unsigned)lanes), 0, stream, a);
 }
 template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT>
 void launch(const NormBwd& a, hipStream_t stream) {
   hipLaunchKernelGGL((k_residual_norm_backward<TX, NCH, GATE_ROW, EXACT, NT>),
-                     dim3((unsigned)norm_backward_blocks(a.M, a.C)), dim3((unsigned)norm_lanes(a.C)), 0, stream, a);
+                     dim3((unsigned)norm_backward_blocks(a.M, a.C)), dim3((unsigned)norm_lanes(a.C, NCH)), 0, stream,
+                     a);
 }
 
 // The kernel for the arguments' types and sizes.
-template <typename TX, bool GATE_ROW, bool EXACT, bool NT, typename A>
-void launch_chunks(const A& a, hipStream_t stream) {
-  switch (norm_chunks(a.C)) {
+template <typename TX, bool GATE_ROW, bool EXACT, bool NT>
+void launch_chunks(const NormFwd& a, hipStream_t stream) {
+  if (forward_chunks(a.C) == 1) launch<TX, 1, GATE_ROW, EXACT, NT>(a, stream);
+  else launch<TX, 2, GATE_ROW, EXACT, NT>(a, stream);
+}
+template <typename TX, bool GATE_ROW, bool EXACT, bool NT>
+void launch_chunks(const NormBwd& a, hipStream_t stream) {
+  switch (backward_chunks(a.C)) {
     case 1: return launch<TX, 1, GATE_ROW, EXACT, NT>(a, stream);
     case 2: return launch<TX, 2, GATE_ROW, EXACT, NT>(a, stream);
     default: return launch<TX, 4, GATE_ROW, EXACT, NT>(a, stream);

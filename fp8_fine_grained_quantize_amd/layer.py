@@ -107,6 +107,18 @@ def _ld(t: Optional[torch.Tensor]) -> int:
     return ld if ld >= cols else cols
 
 
+def _out(t: Optional[torch.Tensor], rows: int, cols: int, dtype, device, what: str):
+    """(t, its pitch): the given output, checked, or a new one."""
+    if t is not None:
+        _need(t, dtype, what)
+        _shape(t, (rows, cols), what)
+        return t, _ld(t)
+    per = 16 // dtype.itemsize
+    ld = -(-cols // per) * per
+    t = torch.empty((rows, ld), dtype=dtype, device=device)
+    return (t if ld == cols else t[:, :cols]), ld
+
+
 # --------------------------------------------------------------------------
 # tokens by expert
 # --------------------------------------------------------------------------
@@ -163,13 +175,9 @@ def moe_dispatch(x: torch.Tensor, row_of: torch.Tensor, out=None) -> torch.Tenso
     stream = _current_stream(x, row_of, out)
     T, C = x.shape
     K = _pairs(row_of, T)
-    if out is None:
-        out = _fb._empty_pitched(T * K, C, torch.bfloat16, x.device, 2)
-    else:
-        _need(out, torch.bfloat16, "out")
-        _shape(out, (T * K, C), "out")
-    _fb._check(_fb.lib().fp8blk_moe_dispatch(_addr(x), T, C, _ld(x), K, _addr(row_of), _addr(out),
-                                             _ld(out), stream), "moe_dispatch")
+    out, ldo = _out(out, T * K, C, torch.bfloat16, x.device, "out")
+    _fb._check(_fb.lib().fp8blk_moe_dispatch(_addr(x), T, C, _ld(x), K, _addr(row_of), _addr(out), ldo, stream),
+               "moe_dispatch")
     return out
 
 
@@ -184,17 +192,13 @@ def moe_dispatch_fp8(q: torch.Tensor, s: torch.Tensor, row_of: torch.Tensor, slo
     G = (C + 127) // 128
     _dense(s, torch.float32, (G, T), "s")
     _dense(slot_of, torch.int32, (T * K,), "slot_of")
-    if qr is None:
-        qr = _fb._empty_pitched(T * K, C, torch.uint8, q.device, 1)
-    else:
-        _need(qr, torch.uint8, "qr")
-        _shape(qr, (T * K, C), "qr")
+    qr, ldqr = _out(qr, T * K, C, torch.uint8, q.device, "qr")
     if sr is None:
         sr = torch.empty(G, T * K, dtype=torch.float32, device=q.device)
     else:
         _dense(sr, torch.float32, (G, T * K), "sr")
     _fb._check(_fb.lib().fp8blk_moe_dispatch_fp8(_addr(q), T, C, _ld(q), _addr(s), K, _addr(row_of),
-                                                 _addr(slot_of), _addr(qr), _ld(qr), _addr(sr),
+                                                 _addr(slot_of), _addr(qr), ldqr, _addr(sr),
                                                  stream), "moe_dispatch_fp8")
     return qr, sr
 
@@ -213,14 +217,11 @@ def moe_combine(rows: torch.Tensor, row_of: torch.Tensor, weights: Optional[torc
     if weights is not None:
         _dense(weights, torch.float32, (T, K), "weights")
     flags = _ROWS_F32 if _is_f32(rows, "rows") else 0
-    if out is None:
-        out = _fb._empty_pitched(T, C, out_dtype, rows.device, 4 if out_dtype == torch.float32 else 2)
-    else:
-        _shape(out, (T, C), "out")
+    out, ldo = _out(out, T, C, out_dtype if out is None else out.dtype, rows.device, "out")
     if _is_f32(out, "out"):
         flags |= _TOKENS_F32
     _fb._check(_fb.lib().fp8blk_moe_combine(_addr(rows), T, K, C, _ld(rows), _addr(row_of),
-                                            _addr(weights), _addr(out), _ld(out), flags, stream),
+                                            _addr(weights), _addr(out), ldo, flags, stream),
                "moe_combine")
     return out
 
@@ -236,11 +237,8 @@ def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, row_of: torch.Ten
     _shape(rows, (T * K, C), "rows")
     _dense(weights, torch.float32, (T, K), "weights")
     flags = (_TOKENS_F32 if _is_f32(dy, "dy") else 0) | (_ROWS_F32 if _is_f32(rows, "rows") else 0)
-    if drows is None:
-        dt = rows.dtype if drows_dtype is None else drows_dtype
-        drows = _fb._empty_pitched(T * K, C, dt, dy.device, 4 if dt == torch.float32 else 2)
-    else:
-        _shape(drows, (T * K, C), "drows")
+    dt = drows.dtype if drows is not None else rows.dtype if drows_dtype is None else drows_dtype
+    drows, lddr = _out(drows, T * K, C, dt, dy.device, "drows")
     if _is_f32(drows, "drows"):
         flags |= _DROWS_F32
     if dweights is None:
@@ -249,7 +247,7 @@ def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, row_of: torch.Ten
         _dense(dweights, torch.float32, (T, K), "dweights")
     _fb._check(_fb.lib().fp8blk_moe_combine_backward(
         _addr(dy), _ld(dy), _addr(rows), _ld(rows), T, K, C, _addr(row_of), _addr(weights),
-        _addr(drows), _ld(drows), _addr(dweights), flags, stream), "moe_combine_backward")
+        _addr(drows), lddr, _addr(dweights), flags, stream), "moe_combine_backward")
     return drows, dweights
 
 
@@ -275,20 +273,19 @@ class ResidualNormGrad(NamedTuple):
     dgate: Optional[torch.Tensor]
 
 
-def _params(C: int, *named):
+def _params(C: int, w_pre, w_post, gate) -> int:
     """The flag of the parameters' common type, checked."""
-    dt = None
-    for t, what in named:
+    flag = None
+    for t in (w_pre, w_post, gate):
         if t is None:
             continue
-        _shape(t, (C,), what)
-        if C > 1 and t.stride(0) != 1:
-            raise ValueError(f"{what} must be contiguous")
-        f = _is_f32(t, what)
-        if dt is not None and f != dt:
-            raise TypeError("w_post, w_pre and a gate per channel must have one type")
-        dt = f
-    return _NORM_PARAM_F32 if dt else 0
+        if t.shape != (C,) or not t.is_contiguous():
+            raise ValueError(f"w_pre, w_post and a gate per channel must be contiguous vectors of {C}, got {tuple(t.shape)}")
+        f = _NORM_PARAM_F32 if _is_f32(t, "w_pre, w_post and a gate per channel") else 0
+        if flag is not None and f != flag:
+            raise TypeError("w_pre, w_post and a gate per channel must have one type")
+        flag = f
+    return flag or 0
 
 
 def _gate(gate, M: int, C: int):
@@ -313,10 +310,10 @@ def residual_norm(x: torch.Tensor, w_pre=None, f=None, w_post=None, gate=None, a
     M, C = x.shape
     stream = _current_stream(x, w_pre, f, w_post, gate, x_out, n, q, s)
     gate_c, flags, ldg = _gate(gate, M, C)
-    flags |= _params(C, (w_pre, "w_pre"), (w_post, "w_post"), (gate_c, "gate"))
+    flags |= _params(C, w_pre, w_post, gate_c)
     if _is_f32(x, "x"):
         flags |= _NORM_RES_F32
-    dev, elem = x.device, x.element_size()
+    dev = x.device
     if (w_post is not None or gate is not None) and f is None:
         raise ValueError("w_post and gate need f")
     if f is None and w_pre is None:
@@ -324,45 +321,34 @@ def residual_norm(x: torch.Tensor, w_pre=None, f=None, w_post=None, gate=None, a
     if w_pre is None and (quantize or n is not None):
         raise ValueError("n and its quantization need w_pre")
     rstd_post = rstd_pre = None
+    ldf = ldxo = ldn = ldq = 0
     if f is not None:
         _need(f, torch.bfloat16, "f")
         _shape(f, (M, C), "f")
-        if x_out is None:
-            x_out = _fb._empty_pitched(M, C, x.dtype, dev, elem)
-        else:
-            _need(x_out, x.dtype, "x_out")
-            _shape(x_out, (M, C), "x_out")
+        ldf = _ld(f)
+        x_out, ldxo = _out(x_out, M, C, x.dtype, dev, "x_out")
         if w_post is not None:
             rstd_post = torch.empty(M, dtype=torch.float32, device=dev)
     elif x_out is not None:
         raise ValueError("x_out without f: x would not change")
     if w_pre is not None:
         rstd_pre = torch.empty(M, dtype=torch.float32, device=dev)
-        if n is not None:
-            _need(n, torch.bfloat16, "n")
-            _shape(n, (M, C), "n")
-        elif want_n or not quantize:
-            n = _fb._empty_pitched(M, C, torch.bfloat16, dev, 2)
+        if n is not None or want_n or not quantize:
+            n, ldn = _out(n, M, C, torch.bfloat16, dev, "n")
         if quantize:
-            G = (C + 127) // 128
-            if q is None:
-                q = _fb._empty_pitched(M, C, torch.uint8, dev, 1)
-            else:
-                _need(q, torch.uint8, "q")
-                _shape(q, (M, C), "q")
+            q, ldq = _out(q, M, C, torch.uint8, dev, "q")
             if s is None:
-                s = torch.empty(G, M, dtype=torch.float32, device=dev)
+                s = torch.empty((C + 127) // 128, M, dtype=torch.float32, device=dev)
             else:
-                _dense(s, torch.float32, (G, M), "s")
+                _dense(s, torch.float32, ((C + 127) // 128, M), "s")
             if pow2:
                 flags |= _fb.SCALE_POW2
         else:
             q = s = None
-    p, ld = _addr, _ld
     _fb._check(_fb.lib().fp8blk_residual_norm(
-        M, C, p(x), ld(x), p(f), ld(f), p(w_post), p(gate), ldg, alpha, p(w_pre), eps,
-        p(x_out), ld(x_out), p(n), ld(n), p(q),
-        ld(q), p(s), p(rstd_post), p(rstd_pre), flags, stream), "residual_norm")
+        M, C, x.data_ptr(), _ld(x), _addr(f), ldf, _addr(w_post), _addr(gate), ldg, alpha, _addr(w_pre), eps,
+        _addr(x_out), ldxo, _addr(n), ldn, _addr(q), ldq, _addr(s), _addr(rstd_post), _addr(rstd_pre), flags, stream),
+        "residual_norm")
     return ResidualNorm(x if f is None else x_out, n, q, s, rstd_post, rstd_pre)
 
 
@@ -375,7 +361,7 @@ def residual_norm_backward(x_out: torch.Tensor, dx_out=None, dn=None, rstd_pre=N
     M, C = x_out.shape
     stream = _current_stream(x_out, dx_out, dn, rstd_pre, w_pre, f, rstd_post, w_post, gate, dx, df, workspace)
     gate_c, flags, ldg = _gate(gate, M, C)
-    flags |= _params(C, (w_pre, "w_pre"), (w_post, "w_post"), (gate_c, "gate"))
+    flags |= _params(C, w_pre, w_post, gate_c)
     if _is_f32(x_out, "x_out"):
         flags |= _NORM_RES_F32
     dev = x_out.device
@@ -397,28 +383,20 @@ def residual_norm_backward(x_out: torch.Tensor, dx_out=None, dn=None, rstd_pre=N
         _shape(dn, (M, C), "dn")
         _dense(rstd_pre, torch.float32, (M,), "rstd_pre")
         dw_pre = new(C, dtype=torch.float32, device=dev)
-        if dx is None:
-            dx = _fb._empty_pitched(M, C, x_out.dtype, dev, x_out.element_size())
-    if dx is not None:
-        _need(dx, x_out.dtype, "dx")
-        _shape(dx, (M, C), "dx")
-    lddg = 0
+    lddx = lddf = lddg = 0
+    if w_pre is not None or dx is not None:
+        dx, lddx = _out(dx, M, C, x_out.dtype, dev, "dx")
     if f is not None:
         _need(f, torch.bfloat16, "f")
         _shape(f, (M, C), "f")
-        if df is None:
-            df = _fb._empty_pitched(M, C, torch.bfloat16, dev, 2)
-        else:
-            _need(df, torch.bfloat16, "df")
-            _shape(df, (M, C), "df")
+        df, lddf = _out(df, M, C, torch.bfloat16, dev, "df")
         if w_post is not None:
             _dense(rstd_post, torch.float32, (M,), "rstd_post")
             dw_post = new(C, dtype=torch.float32, device=dev)
         if gate_c is not None:
             dgate = new(C, dtype=torch.float32, device=dev)
         elif gate is not None:
-            dgate = _fb._empty_pitched(M, C, torch.bfloat16, dev, 2)
-            lddg = _ld(dgate)
+            dgate, lddg = _out(None, M, C, torch.bfloat16, dev, "dgate")
     L = _fb.lib()
     ws_bytes = 0
     if workspace is not None:
@@ -426,13 +404,11 @@ def residual_norm_backward(x_out: torch.Tensor, dx_out=None, dn=None, rstd_pre=N
     elif dw_pre is not None or dw_post is not None or (dgate is not None and dgate.dim() == 1):
         ws_bytes = L.fp8blk_residual_norm_backward_workspace_bytes(M, C)
         workspace = new((ws_bytes + 3) // 4, dtype=torch.float32, device=dev)
-    p, ld = _addr, _ld
     if dx is not None or f is not None:
         _fb._check(L.fp8blk_residual_norm_backward(
-            M, C, p(x_out), ld(x_out), p(dx_out), ld(dx_out), p(dn),
-            ld(dn), p(rstd_pre), p(w_pre), p(f), ld(f), p(rstd_post),
-            p(w_post), p(gate), ldg, alpha, p(dx), ld(dx), p(df),
-            ld(df), p(dw_pre), p(dw_post), p(dgate), lddg, p(workspace), ws_bytes, flags,
+            M, C, x_out.data_ptr(), _ld(x_out), _addr(dx_out), _ld(dx_out), _addr(dn), _ld(dn), _addr(rstd_pre),
+            _addr(w_pre), _addr(f), _ld(f), _addr(rstd_post), _addr(w_post), _addr(gate), ldg, alpha, _addr(dx), lddx,
+            _addr(df), lddf, _addr(dw_pre), _addr(dw_post), _addr(dgate), lddg, _addr(workspace), ws_bytes, flags,
             stream), "residual_norm_backward")
     return ResidualNormGrad(dx_out if dx is None else dx, df, dw_pre, dw_post, dgate)
 
