@@ -107,16 +107,19 @@ def _ld(t: Optional[torch.Tensor]) -> int:
     return ld if ld >= cols else cols
 
 
-def _out(t: Optional[torch.Tensor], rows: int, cols: int, dtype, device, what: str):
-    """(t, its pitch): the given output, checked, or a new one."""
+def _out(t: Optional[torch.Tensor], rows: int, cols: int, dtype, like: torch.Tensor, what: str):
+    """(t, its pitch): the given output, checked, or a new one beside `like`."""
     if t is not None:
         _need(t, dtype, what)
         _shape(t, (rows, cols), what)
         return t, _ld(t)
     per = 16 // dtype.itemsize
-    ld = -(-cols // per) * per
-    t = torch.empty((rows, ld), dtype=dtype, device=device)
-    return (t if ld == cols else t[:, :cols]), ld
+    if cols % per == 0:
+        if like.dtype == dtype and like.shape == (rows, cols) and like.is_contiguous():
+            return torch.empty_like(like), cols  # fewer arguments to parse than torch.empty
+        return torch.empty(rows, cols, dtype=dtype, device=like.device), cols
+    ld = (cols // per + 1) * per
+    return torch.empty(rows, ld, dtype=dtype, device=like.device)[:, :cols], ld
 
 
 # --------------------------------------------------------------------------
@@ -175,7 +178,7 @@ def moe_dispatch(x: torch.Tensor, row_of: torch.Tensor, out=None) -> torch.Tenso
     stream = _current_stream(x, row_of, out)
     T, C = x.shape
     K = _pairs(row_of, T)
-    out, ldo = _out(out, T * K, C, torch.bfloat16, x.device, "out")
+    out, ldo = _out(out, T * K, C, torch.bfloat16, x, "out")
     _fb._check(_fb.lib().fp8blk_moe_dispatch(_addr(x), T, C, _ld(x), K, _addr(row_of), _addr(out), ldo, stream),
                "moe_dispatch")
     return out
@@ -192,7 +195,7 @@ def moe_dispatch_fp8(q: torch.Tensor, s: torch.Tensor, row_of: torch.Tensor, slo
     G = (C + 127) // 128
     _dense(s, torch.float32, (G, T), "s")
     _dense(slot_of, torch.int32, (T * K,), "slot_of")
-    qr, ldqr = _out(qr, T * K, C, torch.uint8, q.device, "qr")
+    qr, ldqr = _out(qr, T * K, C, torch.uint8, q, "qr")
     if sr is None:
         sr = torch.empty(G, T * K, dtype=torch.float32, device=q.device)
     else:
@@ -217,7 +220,7 @@ def moe_combine(rows: torch.Tensor, row_of: torch.Tensor, weights: Optional[torc
     if weights is not None:
         _dense(weights, torch.float32, (T, K), "weights")
     flags = _ROWS_F32 if _is_f32(rows, "rows") else 0
-    out, ldo = _out(out, T, C, out_dtype if out is None else out.dtype, rows.device, "out")
+    out, ldo = _out(out, T, C, out_dtype if out is None else out.dtype, rows, "out")
     if _is_f32(out, "out"):
         flags |= _TOKENS_F32
     _fb._check(_fb.lib().fp8blk_moe_combine(_addr(rows), T, K, C, _ld(rows), _addr(row_of),
@@ -238,7 +241,7 @@ def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, row_of: torch.Ten
     _dense(weights, torch.float32, (T, K), "weights")
     flags = (_TOKENS_F32 if _is_f32(dy, "dy") else 0) | (_ROWS_F32 if _is_f32(rows, "rows") else 0)
     dt = drows.dtype if drows is not None else rows.dtype if drows_dtype is None else drows_dtype
-    drows, lddr = _out(drows, T * K, C, dt, dy.device, "drows")
+    drows, lddr = _out(drows, T * K, C, dt, rows, "drows")
     if _is_f32(drows, "drows"):
         flags |= _DROWS_F32
     if dweights is None:
@@ -326,7 +329,7 @@ def residual_norm(x: torch.Tensor, w_pre=None, f=None, w_post=None, gate=None, a
         _need(f, torch.bfloat16, "f")
         _shape(f, (M, C), "f")
         ldf = _ld(f)
-        x_out, ldxo = _out(x_out, M, C, x.dtype, dev, "x_out")
+        x_out, ldxo = _out(x_out, M, C, x.dtype, x, "x_out")
         if w_post is not None:
             rstd_post = torch.empty(M, dtype=torch.float32, device=dev)
     elif x_out is not None:
@@ -334,9 +337,9 @@ def residual_norm(x: torch.Tensor, w_pre=None, f=None, w_post=None, gate=None, a
     if w_pre is not None:
         rstd_pre = torch.empty(M, dtype=torch.float32, device=dev)
         if n is not None or want_n or not quantize:
-            n, ldn = _out(n, M, C, torch.bfloat16, dev, "n")
+            n, ldn = _out(n, M, C, torch.bfloat16, x if f is None else f, "n")
         if quantize:
-            q, ldq = _out(q, M, C, torch.uint8, dev, "q")
+            q, ldq = _out(q, M, C, torch.uint8, x, "q")
             if s is None:
                 s = torch.empty((C + 127) // 128, M, dtype=torch.float32, device=dev)
             else:
@@ -385,18 +388,18 @@ def residual_norm_backward(x_out: torch.Tensor, dx_out=None, dn=None, rstd_pre=N
         dw_pre = new(C, dtype=torch.float32, device=dev)
     lddx = lddf = lddg = 0
     if w_pre is not None or dx is not None:
-        dx, lddx = _out(dx, M, C, x_out.dtype, dev, "dx")
+        dx, lddx = _out(dx, M, C, x_out.dtype, x_out, "dx")
     if f is not None:
         _need(f, torch.bfloat16, "f")
         _shape(f, (M, C), "f")
-        df, lddf = _out(df, M, C, torch.bfloat16, dev, "df")
+        df, lddf = _out(df, M, C, torch.bfloat16, f, "df")
         if w_post is not None:
             _dense(rstd_post, torch.float32, (M,), "rstd_post")
             dw_post = new(C, dtype=torch.float32, device=dev)
         if gate_c is not None:
             dgate = new(C, dtype=torch.float32, device=dev)
         elif gate is not None:
-            dgate, lddg = _out(None, M, C, torch.bfloat16, dev, "dgate")
+            dgate, lddg = _out(None, M, C, torch.bfloat16, f, "dgate")
     L = _fb.lib()
     ws_bytes = 0
     if workspace is not None:
