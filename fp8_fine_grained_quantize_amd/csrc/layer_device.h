@@ -81,125 +81,73 @@ __device__ __forceinline__ void store_v(Global<uint16_t>* p, const float (&v)[V]
   for (int j = 0; j < V / 2; ++j) r[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
   store_words<NT, V / 2>(p, r);
 }
-// The same where only `avail` elements are left in the row: those past its end
-// read as zero and are not touched in memory.  EXACT: rows are multiples of V.
-template <int V, bool EXACT, bool NT, typename T>
-__device__ __forceinline__ RawV<T, V> load_end(const T* p, int64_t avail) {
-  if (EXACT || avail >= V) return load_raw<V, NT>(global(p));
+// V elements of a row of C from column col on, where the row may end inside
+// them or before: values past its end are zero and memory past it is not
+// touched.  EXACT: C is a multiple of V.  Otherwise the last V elements of the
+// row are loaded and unpack_end moves them to their places, so that a row's
+// end costs no branch and no wait where it is loaded (rows shorter than V come
+// element by element; LONG: there are none).
+template <int V, bool EXACT, bool NT, bool LONG = false, typename T>
+__device__ __forceinline__ RawV<T, V> load_end(const T* row, int64_t col, int64_t C) {
+  if (EXACT) {
+    RawV<T, V> r{};
+    if (col < C) r = load_raw<V, NT>(global(row + col));
+    return r;
+  }
+  if (LONG || C >= V) return load_raw<V, NT>(global(row + (col < C - V ? col : C - V)));
   RawV<T, V> r{};
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    if (j >= avail) continue;
-    if constexpr (sizeof(T) == 4) r[j] = __float_as_uint(p[j]);
-    else r[j >> 1] |= (uint32_t)p[j] << ((j & 1) * 16);
+    if (col + j >= C) continue;
+    if constexpr (sizeof(T) == 4) r[j] = __float_as_uint(row[col + j]);
+    else r[j >> 1] |= (uint32_t)row[col + j] << ((j & 1) * 16);
   }
   return r;
 }
-template <int V, bool EXACT, bool NT, typename T>
-__device__ __forceinline__ void store_end(T* p, int64_t avail, const float (&v)[V]) {
-  if (EXACT || avail >= V) {
-    store_v<V, NT>(global(p), v);
-  } else {
+template <typename T, int V, bool EXACT, bool LONG = false>
+__device__ __forceinline__ void unpack_end(const RawV<T, V>& r, int64_t col, int64_t C, float (&v)[V]) {
+  unpack_v<T, V>(r, v);
+  if (EXACT || (!LONG && C < V)) return;
+  const int64_t d = col + V - C;  // elements that precede column col in r
+  if (d <= 0) return;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j < avail) p[j] = from_f32<T>(v[j]);
+  for (int k = 1; k < V; k *= 2) {
+    const bool move = (d & k) != 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = move ? (j + k < V ? v[j + k] : 0.0f) : v[j];
+  }
+  if (d >= V) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = 0.0f;
+  }
+}
+// The elements inside the row are stored, an end in pieces of four, two and one.
+template <int V, bool EXACT, bool NT, typename T>
+__device__ __forceinline__ void store_end(T* row, int64_t col, int64_t C, const float (&v)[V]) {
+  const int64_t avail = C - col;
+  if (EXACT ? avail > 0 : avail >= V) {
+    store_v<V, NT>(global(row + col), v);
+    return;
+  }
+  if (EXACT || avail <= 0) return;
+  T* p = row + col;
+  int at = 0;  // elements stored so far: a multiple of the piece's size
+#pragma unroll
+  for (int n = V / 2; n >= 1; n /= 2) {
+    if (!(avail & n)) continue;
+#pragma unroll
+    for (int s = 0; s < V; s += n) {
+      if (s != at) continue;
+#pragma unroll
+      for (int j = 0; j < n; ++j) p[s + j] = from_f32<T>(v[s + j]);
+    }
+    at += n;
   }
 }
 
-template <bool NT = false>
-__device__ __forceinline__ uint4 load_u128(const void* p) {
-  auto* q = (const Global<const Words<4>::unaligned>*)p;
-  const Words<4>::type r = NT ? __builtin_nontemporal_load(q) : *q;
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
-template <bool NT = false>
+template <bool NT>
 __device__ __forceinline__ void store_u128(void* p, const uint4& v) {
   store_words<NT, 4>((Global<void>*)p, Words<4>::type{v.x, v.y, v.z, v.w});
-}
-
-// Eight raw elements of a row: one 16-byte word for BF16, two for FP32.
-template <typename T>
-struct Raw8;
-template <>
-struct Raw8<uint16_t> {
-  uint4 a;
-};
-template <>
-struct Raw8<float> {
-  uint4 a, b;
-};
-
-__device__ __forceinline__ void zero8(Raw8<uint16_t>& r) { r.a = make_uint4(0u, 0u, 0u, 0u); }
-__device__ __forceinline__ void zero8(Raw8<float>& r) { r.a = r.b = make_uint4(0u, 0u, 0u, 0u); }
-
-// `avail` elements are left in the row; those past its end read as zero and
-// are not touched in memory.  EXACT: the row is a multiple of eight elements,
-// so a chunk is all there or not at all (without the element-wise ends the
-// kernels are a third of the size).
-template <bool EXACT, bool NT>
-__device__ __forceinline__ void load8(Raw8<uint16_t>& r, const uint16_t* p, int64_t avail) {
-  zero8(r);
-  if (EXACT ? avail > 0 : avail >= 8) {
-    r.a = load_u128<NT>(p);
-  } else if (!EXACT) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < avail) w[j >> 1] |= (uint32_t)p[j] << ((j & 1) * 16);
-    r.a = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-template <bool EXACT, bool NT>
-__device__ __forceinline__ void load8(Raw8<float>& r, const float* p, int64_t avail) {
-  zero8(r);
-  if (EXACT ? avail > 0 : avail >= 8) {
-    r.a = load_u128<NT>(p);
-    r.b = load_u128<NT>(p + 4);
-  } else if (!EXACT) {
-    uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < avail) w[j] = __float_as_uint(p[j]);
-    r.a = make_uint4(w[0], w[1], w[2], w[3]);
-    r.b = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-}
-
-__device__ __forceinline__ void unpack8(const Raw8<uint16_t>& r, float (&v)[8]) {
-  v[0] = bf16_lo(r.a.x); v[1] = bf16_hi(r.a.x);
-  v[2] = bf16_lo(r.a.y); v[3] = bf16_hi(r.a.y);
-  v[4] = bf16_lo(r.a.z); v[5] = bf16_hi(r.a.z);
-  v[6] = bf16_lo(r.a.w); v[7] = bf16_hi(r.a.w);
-}
-__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
-  v[0] = __uint_as_float(r.a.x); v[1] = __uint_as_float(r.a.y);
-  v[2] = __uint_as_float(r.a.z); v[3] = __uint_as_float(r.a.w);
-  v[4] = __uint_as_float(r.b.x); v[5] = __uint_as_float(r.b.y);
-  v[6] = __uint_as_float(r.b.z); v[7] = __uint_as_float(r.b.w);
-}
-
-template <bool EXACT, bool NT>
-__device__ __forceinline__ void store8(uint16_t* p, int64_t avail, const float (&v)[8]) {
-  const uint4 w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-  if (EXACT ? avail > 0 : avail >= 8) {
-    store_u128<NT>(p, w);
-  } else if (!EXACT) {
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < avail) p[j] = (uint16_t)(a[j >> 1] >> ((j & 1) * 16));
-  }
-}
-template <bool EXACT, bool NT>
-__device__ __forceinline__ void store8(float* p, int64_t avail, const float (&v)[8]) {
-  if (EXACT ? avail > 0 : avail >= 8) {
-    store_u128<NT>(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
-    store_u128<NT>(p + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
-  } else if (!EXACT) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < avail) p[j] = v[j];
-  }
 }
 
 // Sum over the wave's 64 lanes, the same bits in every lane.  FP32: four DPP

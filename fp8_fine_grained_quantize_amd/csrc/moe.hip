@@ -274,8 +274,7 @@ __global__ __launch_bounds__(256) void k_moe_combine(const TR* __restrict__ rows
   const int64_t P = T * K;
   const int64_t t = blockIdx.x / segs;
   const int64_t col = ((int64_t)(blockIdx.x % segs) * blockDim.x + threadIdx.x) * V;
-  const int64_t avail = C - col;
-  if (avail <= 0) return;
+  if (col >= C) return;
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.0f;
@@ -287,19 +286,19 @@ __global__ __launch_bounds__(256) void k_moe_combine(const TR* __restrict__ rows
       const uint32_t k = k0 + j;
       const int64_t r = k < K ? row_of[t * K + k] : -1;
       on[j] = r >= 0 && r < P;
-      if (on[j]) raw[j] = load_end<V, EXACT, NT>(rows + r * ldr + col, avail);
+      if (on[j]) raw[j] = load_end<V, EXACT, NT>(rows + r * ldr, col, C);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (!on[j]) continue;
       const float wk = WEIGHTED ? w[t * K + k0 + j] : 1.0f;
       float v[V];
-      unpack_v<TR, V>(raw[j], v);
+      unpack_end<TR, V, EXACT>(raw[j], col, C, v);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] = WEIGHTED ? __builtin_fmaf(wk, v[i], acc[i]) : acc[i] + v[i];
     }
   }
-  store_end<V, EXACT, NT>(y + t * ldy + col, avail, acc);
+  store_end<V, EXACT, NT>(y + t * ldy, col, C, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -338,14 +337,13 @@ __global__ __launch_bounds__(1024) void k_moe_combine_backward(const TY* __restr
       dot[j] = 0.0f;
     }
     for (int64_t col = (int64_t)threadIdx.x * V; col < C; col += (int64_t)blockDim.x * V) {
-      const int64_t avail = C - col;
       float d[V];
-      const RawV<TY, V> raw_dy = load_end<V, EXACT, false>(dy + t * lddy + col, avail);
+      const RawV<TY, V> raw_dy = load_end<V, EXACT, false>(dy + t * lddy, col, C);
       RawV<TR, V> raw[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (on[j]) raw[j] = load_end<V, EXACT, NT>(rows + row[j] * ldr + col, avail);
-      unpack_v<TY, V>(raw_dy, d);
+        if (on[j]) raw[j] = load_end<V, EXACT, NT>(rows + row[j] * ldr, col, C);
+      unpack_end<TY, V, EXACT>(raw_dy, col, C, d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (row[j] < 0) continue;
@@ -354,11 +352,11 @@ __global__ __launch_bounds__(1024) void k_moe_combine_backward(const TY* __restr
         for (int i = 0; i < V; ++i) o[i] = on[j] ? wk[j] * d[i] : 0.0f;
         if (on[j]) {
           float v[V];
-          unpack_v<TR, V>(raw[j], v);
+          unpack_end<TR, V, EXACT>(raw[j], col, C, v);
 #pragma unroll
           for (int i = 0; i < V; ++i) dot[j] = __builtin_fmaf(d[i], v[i], dot[j]);
         }
-        store_end<V, EXACT, NT>(drows + row[j] * lddr + col, avail, o);
+        store_end<V, EXACT, NT>(drows + row[j] * lddr, col, C, o);
       }
     }
     block_sum<8>(dot, red[turn], nw);

@@ -40,16 +40,11 @@ struct NormFwd {
 
 // Eight parameters of either type from an element-aligned vector.
 template <bool EXACT>
-__device__ __forceinline__ void load_param8(const void* p, bool f32, int64_t col, int64_t avail, float (&v)[8]) {
-  if (f32) {
-    Raw8<float> r;
-    load8<EXACT, false>(r, reinterpret_cast<const float*>(p) + col, avail);
-    unpack8(r, v);
-  } else {
-    Raw8<uint16_t> r;
-    load8<EXACT, false>(r, reinterpret_cast<const uint16_t*>(p) + col, avail);
-    unpack8(r, v);
-  }
+__device__ __forceinline__ void load_param8(const void* p, bool f32, int64_t col, int64_t C, float (&v)[8]) {
+  if (f32)
+    unpack_end<float, 8, EXACT>(load_end<8, EXACT, false>(reinterpret_cast<const float*>(p), col, C), col, C, v);
+  else
+    unpack_end<uint16_t, 8, EXACT>(load_end<8, EXACT, false>(reinterpret_cast<const uint16_t*>(p), col, C), col, C, v);
 }
 
 // The 1x128 tile of n that a row of 16 lanes holds, eight values each, scaled
@@ -94,18 +89,18 @@ __device__ __forceinline__ float rstd_of(float sum, float inv_c, float eps) { re
 // What a lane reads of one row, before it is unpacked.
 template <typename TX, int NCH, bool GATE_ROW, bool EXACT>
 struct NormRow {
-  Raw8<TX> x[NCH];
-  Raw8<uint16_t> f[NCH], gate[GATE_ROW ? NCH : 1];
+  RawV<TX, 8> x[NCH];
+  RawV<uint16_t, 8> f[NCH], gate[GATE_ROW ? NCH : 1];
 };
 
 template <bool NT, typename TX, int NCH, bool GATE_ROW, bool EXACT>
 __device__ __forceinline__ void load_row(NormRow<TX, NCH, GATE_ROW, EXACT>& r, const NormFwd& a, int64_t row) {
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * blockDim.x) * 8, avail = a.C - col;
-    load8<EXACT, NT>(r.x[c], reinterpret_cast<const TX*>(a.x) + row * a.ldx + col, avail);
-    if (a.f != nullptr) load8<EXACT, NT>(r.f[c], a.f + row * a.ldf + col, avail);
-    if (GATE_ROW) load8<EXACT, NT>(r.gate[c], reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg + col, avail);
+    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * blockDim.x) * 8;
+    r.x[c] = load_end<8, EXACT, NT, (NCH > 1)>(reinterpret_cast<const TX*>(a.x) + row * a.ldx, col, a.C);
+    if (a.f != nullptr) r.f[c] = load_end<8, EXACT, NT, (NCH > 1)>(a.f + row * a.ldf, col, a.C);
+    if (GATE_ROW) r.gate[c] = load_end<8, EXACT, NT, (NCH > 1)>(reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg, col, a.C);
   }
 }
 
@@ -123,21 +118,21 @@ __global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
   float pc[NCH][8], wn[NCH][8];  // alpha * w_post * (gate per channel); w_pre
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8, avail = a.C - col;
+    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) pc[c][i] = a.alpha;
     float w[8];
     if (a.w_post != nullptr) {
-      load_param8<EXACT>(a.w_post, pf32, col, avail, w);
+      load_param8<EXACT>(a.w_post, pf32, col, a.C, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) pc[c][i] *= w[i];
     }
     if (a.gate != nullptr && !GATE_ROW) {
-      load_param8<EXACT>(a.gate, pf32, col, avail, w);
+      load_param8<EXACT>(a.gate, pf32, col, a.C, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) pc[c][i] *= w[i];
     }
-    if (a.w_pre != nullptr) load_param8<EXACT>(a.w_pre, pf32, col, avail, wn[c]);
+    if (a.w_pre != nullptr) load_param8<EXACT>(a.w_pre, pf32, col, a.C, wn[c]);
   }
   NormRow<TX, NCH, GATE_ROW, EXACT> next;
   load_row<NT>(next, a, blockIdx.x);
@@ -147,7 +142,8 @@ __global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
     if (row + gridDim.x < a.M) load_row<NT>(next, a, row + gridDim.x);
     float z[NCH][8];
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) unpack8(cur.x[c], z[c]);
+    for (int c = 0; c < NCH; ++c)
+      unpack_end<TX, 8, EXACT, (NCH > 1)>(cur.x[c], ((int64_t)threadIdx.x + (int64_t)c * nt) * 8, a.C, z[c]);
     if (a.f != nullptr) {
       float r = 1.0f;
       if (a.w_post != nullptr) {
@@ -155,7 +151,7 @@ __global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
           float f[8];
-          unpack8(cur.f[c], f);
+          unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.f[c], ((int64_t)threadIdx.x + (int64_t)c * nt) * 8, a.C, f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(f[i], f[i], sum[0]);
         }
@@ -167,16 +163,16 @@ __global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
       for (int c = 0; c < NCH; ++c) {
         const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
         float f[8];
-        unpack8(cur.f[c], f);
+        unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.f[c], col, a.C, f);
         if (GATE_ROW) {
           float g[8];
-          unpack8(cur.gate[c], g);
+          unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.gate[c], col, a.C, g);
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] *= g[i];
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[c][i] = __builtin_fmaf(f[i] * r, pc[c][i], z[c][i]);
-        store8<EXACT, NT>(reinterpret_cast<TX*>(a.x_out) + row * a.ldxo + col, a.C - col, z[c]);
+        store_end<8, EXACT, NT>(reinterpret_cast<TX*>(a.x_out) + row * a.ldxo, col, a.C, z[c]);
       }
     }
     if (a.w_pre == nullptr) continue;
@@ -193,7 +189,7 @@ __global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
       const int64_t chunk = (int64_t)threadIdx.x + (int64_t)c * nt, col = chunk * 8, avail = a.C - col;
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[c][i] = z[c][i] * r * wn[c][i];
-      if (a.n != nullptr) store8<EXACT, NT>(a.n + row * a.ldn + col, avail, z[c]);
+      if (a.n != nullptr) store_end<8, EXACT, NT>(a.n + row * a.ldn, col, a.C, z[c]);
       if (a.q != nullptr) {
         float s;
         const uint2 codes = a.flags & FP8BLK_SCALE_POW2 ? quantize_tile<true>(z[c], s) : quantize_tile<false>(z[c], s);
@@ -243,31 +239,26 @@ struct NormBwd {
 // What a lane reads of one chunk of one row, before it is unpacked.
 template <typename TX, bool GATE_ROW>
 struct NormBwdChunk {
-  Raw8<TX> x, dxo;
-  Raw8<uint16_t> dn, f, gate;
+  RawV<TX, 8> x, dxo;
+  RawV<uint16_t, 8> dn, f, gate;
 };
 
-template <bool EXACT, bool NT, typename TX, bool GATE_ROW>
+template <bool EXACT, bool NT, bool LONG, typename TX, bool GATE_ROW>
 __device__ __forceinline__ void load_chunk(NormBwdChunk<TX, GATE_ROW>& r, const NormBwd& a, int64_t row, int64_t col) {
-  const int64_t avail = a.C - col;
-  zero8(r.x);
-  zero8(r.dxo);
-  zero8(r.dn);
-  zero8(r.f);
+  r = {};
   if (a.w_pre != nullptr) {
-    load8<EXACT, NT>(r.x, reinterpret_cast<const TX*>(a.x) + row * a.ldx + col, avail);
-    load8<EXACT, NT>(r.dn, a.dn + row * a.lddn + col, avail);
+    r.x = load_end<8, EXACT, NT, LONG>(reinterpret_cast<const TX*>(a.x) + row * a.ldx, col, a.C);
+    r.dn = load_end<8, EXACT, NT, LONG>(a.dn + row * a.lddn, col, a.C);
   }
-  if (a.dxo != nullptr) load8<EXACT, NT>(r.dxo, reinterpret_cast<const TX*>(a.dxo) + row * a.lddxo + col, avail);
-  if (a.f != nullptr) load8<EXACT, NT>(r.f, a.f + row * a.ldf + col, avail);
-  if (GATE_ROW) load8<EXACT, NT>(r.gate, reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg + col, avail);
+  if (a.dxo != nullptr) r.dxo = load_end<8, EXACT, NT, LONG>(reinterpret_cast<const TX*>(a.dxo) + row * a.lddxo, col, a.C);
+  if (a.f != nullptr) r.f = load_end<8, EXACT, NT, LONG>(a.f + row * a.ldf, col, a.C);
+  if (GATE_ROW) r.gate = load_end<8, EXACT, NT, LONG>(reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg, col, a.C);
 }
 
 // The parameters of a chunk: alpha * w_post * (gate per channel), and w_pre.
 template <bool GATE_ROW, bool EXACT>
 __device__ __forceinline__ void load_factors(const NormBwd& a, int64_t col, float (&pc)[8], float (&wn)[8]) {
   const bool pf32 = (a.flags & FP8BLK_NORM_PARAM_F32) != 0;
-  const int64_t avail = a.C - col;
   float w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -275,39 +266,45 @@ __device__ __forceinline__ void load_factors(const NormBwd& a, int64_t col, floa
     wn[i] = 0.0f;
   }
   if (a.w_post != nullptr) {
-    load_param8<EXACT>(a.w_post, pf32, col, avail, w);
+    load_param8<EXACT>(a.w_post, pf32, col, a.C, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) pc[i] *= w[i];
   }
   if (a.gate != nullptr && !GATE_ROW) {
-    load_param8<EXACT>(a.gate, pf32, col, avail, w);
+    load_param8<EXACT>(a.gate, pf32, col, a.C, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) pc[i] *= w[i];
   }
-  if (a.w_pre != nullptr) load_param8<EXACT>(a.w_pre, pf32, col, avail, wn);
+  if (a.w_pre != nullptr) load_param8<EXACT>(a.w_pre, pf32, col, a.C, wn);
 }
 
-// With one or two chunks per lane the factors and the next row are held in
-// registers.  Where they would not fit beside the accumulators (four chunks, C
-// above 8192; two of FP32 x with a gate per token) factors and rows are read
-// chunk by chunk, and once more (from L2) after the reduction.
-template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT>
-__global__ __launch_bounds__(512) void k_residual_norm_backward(const NormBwd a) {
-  constexpr bool HOLD = NCH == 1 || (NCH == 2 && !(GATE_ROW && sizeof(TX) == 4));
-  constexpr int NH = HOLD ? NCH : 1;
+// HOLD: the factors and the next row are held in registers, up to 256 of 512
+// lanes.  Where they would not fit beside the accumulators (C above 8192; FP32
+// x with a gate per token above 4096) 1024 lanes read factors and rows chunk
+// by chunk, and once more (from L2) after the reduction, with the accumulators
+// in LDS.
+template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT, bool HOLD>
+__global__ __launch_bounds__(HOLD ? 512 : 1024) void k_residual_norm_backward(const NormBwd a) {
+  constexpr int NH = HOLD ? NCH : 1, UNROLL = NH;  // without HOLD one chunk after the other
   __shared__ float red[2][3 * 16];
   const int nt = blockDim.x, nw = nt >> 6;
   const float inv_c = 1.0f / (float)a.C;
-  float s_pre[NCH][8], s_post[NCH][8], pc_[NH][8], wn_[NH][8];
+  __shared__ float acc[HOLD ? 1 : 2 * NCH * 8 * 1024];
+  float s_pre[NH][8], s_post[NH][8], pc_[NH][8], wn_[NH][8];
+  // this lane's accumulator `vec` (0: dn h, 1: g h') of channel i of chunk c in LDS
+  auto slot = [&](int vec, int c, int i) -> float& { return acc[((vec * NCH + c) * 8 + i) * 1024 + threadIdx.x]; };
   NormBwdChunk<TX, GATE_ROW> next[NH], cur_[NH];
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_pre[c][i] = s_post[c][i] = 0.0f;
+    for (int i = 0; i < 8; ++i) {
+      if (HOLD) s_pre[c][i] = s_post[c][i] = 0.0f;
+      else slot(0, c, i) = slot(1, c, i) = 0.0f;
+    }
     if (HOLD) {
       load_factors<GATE_ROW, EXACT>(a, col, pc_[c], wn_[c]);
-      load_chunk<EXACT, NT>(next[c], a, blockIdx.x, col);
+      load_chunk<EXACT, NT, (NCH > 1)>(next[c], a, blockIdx.x, col);
     }
   }
   int turn = 0;
@@ -319,31 +316,31 @@ __global__ __launch_bounds__(512) void k_residual_norm_backward(const NormBwd a)
       for (int c = 0; c < NH; ++c) {
         cur_[c] = next[c];
         if (row + gridDim.x < a.M)
-          load_chunk<EXACT, NT>(next[c], a, row + gridDim.x, ((int64_t)threadIdx.x + (int64_t)c * nt) * 8);
+          load_chunk<EXACT, NT, (NCH > 1)>(next[c], a, row + gridDim.x, ((int64_t)threadIdx.x + (int64_t)c * nt) * 8);
       }
     }
     float sum[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
+#pragma unroll UNROLL
     for (int c = 0; c < NCH; ++c) {
-      if (!HOLD) __builtin_amdgcn_sched_barrier(0);  // one chunk after the other
       float(&pc)[8] = pc_[HOLD ? c : 0];
       float(&wn)[8] = wn_[HOLD ? c : 0];
       NormBwdChunk<TX, GATE_ROW>& cur = cur_[HOLD ? c : 0];
+      const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
       if (!HOLD) {
-        const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
         load_factors<GATE_ROW, EXACT>(a, col, pc, wn);
-        load_chunk<EXACT, NT && HOLD>(cur, a, row, col);
+        load_chunk<EXACT, NT && HOLD, (NCH > 1)>(cur, a, row, col);
       }
       float h[8], v[8], g[8], hf[8], gt[8];
-      unpack8(cur.x, h);
-      unpack8(cur.dn, v);
-      unpack8(cur.dxo, g);
-      unpack8(cur.f, hf);
-      if (GATE_ROW) unpack8(cur.gate, gt);
+      unpack_end<TX, 8, EXACT, (NCH > 1)>(cur.x, col, a.C, h);
+      unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.dn, col, a.C, v);
+      unpack_end<TX, 8, EXACT, (NCH > 1)>(cur.dxo, col, a.C, g);
+      unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.f, col, a.C, hf);
+      if (GATE_ROW) unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.gate, col, a.C, gt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         h[i] *= r_pre;
-        s_pre[c][i] = __builtin_fmaf(v[i], h[i], s_pre[c][i]);
+        float& sp = HOLD ? s_pre[HOLD ? c : 0][i] : slot(0, c, i);
+        sp = __builtin_fmaf(v[i], h[i], sp);
         v[i] *= wn[i];
         sum[0] = __builtin_fmaf(v[i], h[i], sum[0]);
         float p = pc[i] * (hf[i] * r_post);
@@ -355,51 +352,58 @@ __global__ __launch_bounds__(512) void k_residual_norm_backward(const NormBwd a)
     block_sum<3>(sum, red[turn], nw);
     const float m = sum[0] * inv_c;
     const float m_post = a.w_post != nullptr ? (sum[1] - r_pre * m * sum[2]) * inv_c : 0.0f;
-#pragma unroll
+#pragma unroll UNROLL
     for (int c = 0; c < NCH; ++c) {
-      if (!HOLD) __builtin_amdgcn_sched_barrier(0);
-      const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8, avail = a.C - col;
+      const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
       float(&pc)[8] = pc_[HOLD ? c : 0];
       float(&wn)[8] = wn_[HOLD ? c : 0];
       NormBwdChunk<TX, GATE_ROW>& cur = cur_[HOLD ? c : 0];
       if (!HOLD) {
         load_factors<GATE_ROW, EXACT>(a, col, pc, wn);
-        load_chunk<EXACT, NT && HOLD>(cur, a, row, col);
+        load_chunk<EXACT, NT && HOLD, (NCH > 1)>(cur, a, row, col);
       }
       float h[8], v[8], g[8];
-      unpack8(cur.x, h);
-      unpack8(cur.dn, v);
-      unpack8(cur.dxo, g);
+      unpack_end<TX, 8, EXACT, (NCH > 1)>(cur.x, col, a.C, h);
+      unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.dn, col, a.C, v);
+      unpack_end<TX, 8, EXACT, (NCH > 1)>(cur.dxo, col, a.C, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         g[i] = __builtin_fmaf(r_pre, __builtin_fmaf(-(h[i] * r_pre), m, v[i] * wn[i]), g[i]);
-      if (a.dx != nullptr) store8<EXACT, NT>(reinterpret_cast<TX*>(a.dx) + row * a.lddx + col, avail, g);
+      if (a.dx != nullptr) store_end<8, EXACT, NT>(reinterpret_cast<TX*>(a.dx) + row * a.lddx, col, a.C, g);
       if (a.f == nullptr) continue;
-      unpack8(cur.f, h);
+      unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.f, col, a.C, h);
       float gt[8];
-      if (GATE_ROW) unpack8(cur.gate, gt);
+      if (GATE_ROW) unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.gate, col, a.C, gt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         h[i] *= r_post;
         v[i] = g[i] * h[i];  // times its factors: the terms of dw_post and dgate
         float d = pc[i] * g[i];
         if (GATE_ROW) d *= gt[i];
-        s_post[c][i] += GATE_ROW ? v[i] * gt[i] : v[i];
+        float& sp = HOLD ? s_post[HOLD ? c : 0][i] : slot(1, c, i);
+        sp += GATE_ROW ? v[i] * gt[i] : v[i];
         g[i] = r_post * __builtin_fmaf(-h[i], m_post, d);
       }
       if (GATE_ROW) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= pc[i];
-        store8<EXACT, NT>(a.dgate_row + row * a.lddg + col, avail, v);
+        store_end<8, EXACT, NT>(a.dgate_row + row * a.lddg, col, a.C, v);
       }
-      store8<EXACT, NT>(a.df + row * a.lddf + col, avail, g);
+      store_end<8, EXACT, NT>(a.df + row * a.lddf, col, a.C, g);
     }
   }
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8, avail = a.C - col;
-    if (a.part_pre != nullptr) store8<EXACT, false>(a.part_pre + (int64_t)blockIdx.x * a.C + col, avail, s_pre[c]);
-    if (a.part_post != nullptr) store8<EXACT, false>(a.part_post + (int64_t)blockIdx.x * a.C + col, avail, s_post[c]);
+    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
+    if (!HOLD) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s_pre[0][i] = slot(0, c, i);
+        s_post[0][i] = slot(1, c, i);
+      }
+    }
+    if (a.part_pre != nullptr) store_end<8, EXACT, false>(a.part_pre + (int64_t)blockIdx.x * a.C, col, a.C, s_pre[HOLD ? c : 0]);
+    if (a.part_post != nullptr) store_end<8, EXACT, false>(a.part_post + (int64_t)blockIdx.x * a.C, col, a.C, s_post[HOLD ? c : 0]);
   }
 }
 
@@ -454,10 +458,14 @@ __global__ __launch_bounds__(1024) void k_norm_sums(const NormSums a, int first,
 // Chunks of eight channels per lane, and lanes of a row's workgroup (a multiple
 // of 64).  Forward: one chunk up to 1024 lanes, then two (8192 x 7168 took 97 us
 // with 896 lanes of one chunk, 99 with 448 of two).  Gradient: at most 512
-// lanes, so that each may hold 256 registers (123 us with 448 lanes of two
-// chunks, 128 with 896 of one).
+// lanes where they hold a row ahead, so that each may have 256 registers (123
+// us with 448 lanes of two chunks, 128 with 896 of one).
 inline int forward_chunks(int64_t C) { return C > 8192 ? 2 : 1; }
-inline int backward_chunks(int64_t C) { return C > 8192 ? 4 : C > 4096 ? 2 : 1; }
+inline bool backward_holds(int64_t C, uint32_t flags) {
+  return C <= 4096 || (C <= 8192 && (flags & (FP8BLK_NORM_RES_F32 | FP8BLK_NORM_GATE_ROW)) !=
+                                        (FP8BLK_NORM_RES_F32 | FP8BLK_NORM_GATE_ROW));
+}
+inline int backward_chunks(int64_t C) { return C > 4096 ? 2 : 1; }
 inline int norm_lanes(int64_t C, int chunks) {
   return (int)(ceil_div(ceil_div(C, (int64_t)8 * chunks), (int64_t)64) * 64);
 }
@@ -479,9 +487,9 @@ void launch(const NormFwd& a, hipStream_t stream) {
   hipLaunchKernelGGL((k_residual_norm<TX, NCH, GATE_ROW, EXACT, NT>), dim3((unsigned)norm_blocks(a.M, lanes, 2048)),
                      dim3((unsigned)lanes), 0, stream, a);
 }
-template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT>
+template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT, bool HOLD>
 void launch(const NormBwd& a, hipStream_t stream) {
-  hipLaunchKernelGGL((k_residual_norm_backward<TX, NCH, GATE_ROW, EXACT, NT>),
+  hipLaunchKernelGGL((k_residual_norm_backward<TX, NCH, GATE_ROW, EXACT, NT, HOLD>),
                      dim3((unsigned)norm_backward_blocks(a.M, a.C)), dim3((unsigned)norm_lanes(a.C, NCH)), 0, stream,
                      a);
 }
@@ -494,11 +502,9 @@ void launch_chunks(const NormFwd& a, hipStream_t stream) {
 }
 template <typename TX, bool GATE_ROW, bool EXACT, bool NT>
 void launch_chunks(const NormBwd& a, hipStream_t stream) {
-  switch (backward_chunks(a.C)) {
-    case 1: return launch<TX, 1, GATE_ROW, EXACT, NT>(a, stream);
-    case 2: return launch<TX, 2, GATE_ROW, EXACT, NT>(a, stream);
-    default: return launch<TX, 4, GATE_ROW, EXACT, NT>(a, stream);
-  }
+  if (!backward_holds(a.C, a.flags)) launch<TX, 2, GATE_ROW, EXACT, NT, false>(a, stream);
+  else if (backward_chunks(a.C) == 1) launch<TX, 1, GATE_ROW, EXACT, NT, true>(a, stream);
+  else launch<TX, 2, GATE_ROW, EXACT, NT, true>(a, stream);
 }
 template <typename TX, bool GATE_ROW, typename A>
 void launch_exact(const A& a, bool nt, hipStream_t stream) {
