@@ -305,12 +305,10 @@ __global__ __launch_bounds__(256) void k_moe_combine(const TR* __restrict__ rows
 // Gradient of the combine: a workgroup takes one token, reads dy once, and for
 // eight experts at a time reads their rows, adds up the eight dot products
 // (FP32, lane by lane over the channels, then across lanes) and writes the
-// eight scaled copies of dy.  Up to 1024 lanes, so that each part of a row is
-// read and written in one piece (8192 tokens, 8 rows of 7168: 390 us, 396 with
-// 256 lanes).
+// eight scaled copies of dy.
 // ---------------------------------------------------------------------------
 template <typename TY, typename TR, typename TD, bool EXACT, bool NT>
-__global__ __launch_bounds__(1024) void k_moe_combine_backward(const TY* __restrict__ dy, int64_t lddy,
+__global__ __launch_bounds__(512) void k_moe_combine_backward(const TY* __restrict__ dy, int64_t lddy,
                                                                const TR* __restrict__ rows, int64_t ldr, int64_t T,
                                                                uint32_t K, int64_t C,
                                                                const int32_t* __restrict__ row_of,
@@ -444,13 +442,20 @@ void pick_combine(const CombineArgs& a, RowSplit sp, hipStream_t stream) {
   const bool nt = a.T * a.C * (int64_t)(a.K * sizeof(TR) + sizeof(TY)) >= kStreamBytes;
   if (a.w != nullptr) {
     if (!exact) return launch_combine<TR, TY, true, false, false>(a, sp, stream);
-    if (nt) return launch_combine<TR, TY, true, true, true>(a, sp, stream);
-    return launch_combine<TR, TY, true, true, false>(a, sp, stream);
+    return nt ? launch_combine<TR, TY, true, true, true>(a, sp, stream)
+              : launch_combine<TR, TY, true, true, false>(a, sp, stream);
   }
   if (!exact) return launch_combine<TR, TY, false, false, false>(a, sp, stream);
-  if (nt) return launch_combine<TR, TY, false, true, true>(a, sp, stream);
-  return launch_combine<TR, TY, false, true, false>(a, sp, stream);
+  return nt ? launch_combine<TR, TY, false, true, true>(a, sp, stream)
+            : launch_combine<TR, TY, false, true, false>(a, sp, stream);
 }
+
+// Lanes of a token's workgroup, at most.  Few rows a token leave a large
+// workgroup waiting on its own start and reduction: 32768 tokens of one row of
+// 7168 took 272 us with 256 lanes, 328 with 512 and 682 with 896, 16384 tokens
+// of two rows of 4096 107 / 138 / 137; with 8 rows of 7168, 64 tokens took 9.4 /
+// 8.2 / 8.6 and 8192 tokens 369 / 369 / 366.
+inline int64_t combine_grad_lanes(uint32_t K) { return K < 4 ? 256 : 512; }
 
 struct CombineGradArgs {
   const void* dy;
@@ -469,7 +474,7 @@ template <typename TY, typename TR, typename TD, bool EXACT, bool NT>
 void launch_combine_backward(const CombineGradArgs& a, hipStream_t stream) {
   const int64_t V = sizeof(TY) == 2 && sizeof(TR) == 2 && sizeof(TD) == 2 ? 8 : 4;
   hipLaunchKernelGGL((k_moe_combine_backward<TY, TR, TD, EXACT, NT>), dim3((unsigned)a.T),
-                     dim3(split_row(ceil_div(a.C, V), 1024).lanes), 0, stream, reinterpret_cast<const TY*>(a.dy), a.lddy,
+                     dim3(split_row(ceil_div(a.C, V), combine_grad_lanes(a.K)).lanes), 0, stream, reinterpret_cast<const TY*>(a.dy), a.lddy,
                      reinterpret_cast<const TR*>(a.rows), a.ldr, a.T, a.K, a.C, a.row_of, a.w,
                      reinterpret_cast<TD*>(a.drows), a.lddr, a.dw);
 }
@@ -584,7 +589,7 @@ extern "C" fp8blk_status_t fp8blk_moe_combine_backward(const void* dy, int64_t l
       !matrix_ok(drows, T * K, C, lddr, df ? 4 : 2) || !vec_ok(row_of, T * K) || !vec_ok(weights, T * K) ||
       !vec_ok(dweights, T * K))
     return FP8BLK_ERR_INVALID_ARG;
-  if (!grid_ok(T, 1024)) return FP8BLK_ERR_UNSUPPORTED;
+  if (!grid_ok(T, 512)) return FP8BLK_ERR_UNSUPPORTED;
   using U = uint16_t;
   using F = float;
   const CombineGradArgs a{dy, lddy, rows, ldr, T, (uint32_t)K, C, row_of, weights, drows, lddr, dweights};
