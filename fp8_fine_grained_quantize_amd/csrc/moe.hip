@@ -261,16 +261,20 @@ __global__ __launch_bounds__(256) void k_moe_dispatch(const uint8_t* __restrict_
 // ---------------------------------------------------------------------------
 // Combine: a workgroup takes one token and a segment of the row; a lane sums V
 // channels over the token's rows in FP32, k ascending, loads of eight rows in
-// flight.  V fills 16 bytes of the rows' type, so that a wave reads one
-// contiguous kilobyte of each row: FP32 rows in two loads 32 bytes apart from
-// lane to lane took 387 us instead of 347 (8192 tokens, 8 rows of 7168 each).
+// flight.  V fills 16 bytes of the wider type, so that a wave's loads and
+// stores are contiguous: FP32 in two accesses 32 bytes apart from lane to lane
+// took 387 us instead of 347 for the rows (8192 tokens, 8 rows of 7168 each)
+// and 348 instead of 252 for the sums (32768 tokens, one BF16 row of 7168 each).
 // ---------------------------------------------------------------------------
+template <typename TR, typename TY>
+constexpr int combine_width() { return sizeof(TR) == 2 && sizeof(TY) == 2 ? 8 : 4; }
+
 template <typename TR, typename TY, bool WEIGHTED, bool EXACT, bool NT>
 __global__ __launch_bounds__(256) void k_moe_combine(const TR* __restrict__ rows, int64_t ldr, int64_t C, int64_t T,
                                                       uint32_t K, const int32_t* __restrict__ row_of,
                                                       const float* __restrict__ w, TY* __restrict__ y, int64_t ldy,
                                                       uint32_t segs) {
-  constexpr int V = 16 / sizeof(TR);
+  constexpr int V = combine_width<TR, TY>();
   const int64_t P = T * K;
   const int64_t t = blockIdx.x / segs;
   const int64_t col = ((int64_t)(blockIdx.x % segs) * blockDim.x + threadIdx.x) * V;
@@ -438,7 +442,7 @@ void launch_combine(const CombineArgs& a, RowSplit sp, hipStream_t stream) {
 }
 template <typename TR, typename TY>
 void pick_combine(const CombineArgs& a, RowSplit sp, hipStream_t stream) {
-  const bool exact = a.C % (int64_t)(16 / sizeof(TR)) == 0;
+  const bool exact = a.C % combine_width<TR, TY>() == 0;
   const bool nt = a.T * a.C * (int64_t)(a.K * sizeof(TR) + sizeof(TY)) >= kStreamBytes;
   if (a.w != nullptr) {
     if (!exact) return launch_combine<TR, TY, true, false, false>(a, sp, stream);
@@ -474,9 +478,9 @@ template <typename TY, typename TR, typename TD, bool EXACT, bool NT>
 void launch_combine_backward(const CombineGradArgs& a, hipStream_t stream) {
   const int64_t V = sizeof(TY) == 2 && sizeof(TR) == 2 && sizeof(TD) == 2 ? 8 : 4;
   hipLaunchKernelGGL((k_moe_combine_backward<TY, TR, TD, EXACT, NT>), dim3((unsigned)a.T),
-                     dim3(split_row(ceil_div(a.C, V), combine_grad_lanes(a.K)).lanes), 0, stream, reinterpret_cast<const TY*>(a.dy), a.lddy,
-                     reinterpret_cast<const TR*>(a.rows), a.ldr, a.T, a.K, a.C, a.row_of, a.w,
-                     reinterpret_cast<TD*>(a.drows), a.lddr, a.dw);
+                     dim3(split_row(ceil_div(a.C, V), combine_grad_lanes(a.K)).lanes), 0, stream,
+                     reinterpret_cast<const TY*>(a.dy), a.lddy, reinterpret_cast<const TR*>(a.rows), a.ldr, a.T, a.K,
+                     a.C, a.row_of, a.w, reinterpret_cast<TD*>(a.drows), a.lddr, a.dw);
 }
 template <typename TY, typename TR, typename TD>
 void pick_combine_backward(const CombineGradArgs& a, hipStream_t stream) {
@@ -566,7 +570,7 @@ extern "C" fp8blk_status_t fp8blk_moe_combine(const void* rows, int64_t T, int64
   if (!matrix_ok(rows, T * K, C, ldr, rf ? 4 : 2) || !matrix_ok(y, T, C, ldy, yf ? 4 : 2) || !vec_ok(row_of, T * K) ||
       (weights != nullptr && !aligned(weights, 4)))
     return FP8BLK_ERR_INVALID_ARG;
-  const RowSplit sp = split_row(ceil_div(C, (int64_t)(rf ? 4 : 8)));
+  const RowSplit sp = split_row(ceil_div(C, (int64_t)(rf || yf ? 4 : 8)));
   if (!grid_ok(T * sp.segs, sp.lanes)) return FP8BLK_ERR_UNSUPPORTED;
   const CombineArgs a{rows, ldr, C, T, (uint32_t)K, row_of, weights, y, ldy};
   auto* go = rf ? (yf ? pick_combine<float, float> : pick_combine<float, uint16_t>)
