@@ -477,7 +477,8 @@ inline int norm_lanes(int64_t C, int chunks) {
 }
 
 // Workgroups of either kernel: `per_cu` lanes on a compute unit, as many as the
-// registers allow at a time.
+// registers allow at a time (half or twice as many were 1-2 % slower in the
+// forward, twice as many 7 % in the gradient, 8192 x 7168).
 inline int64_t norm_blocks(int64_t M, int lanes, int64_t per_cu) {
   int64_t n = per_cu / lanes;
   n = (n < 1 ? 1 : n) * device_cus();

@@ -441,6 +441,16 @@ def _as_rows(shape, stride):
     return (rows, cols, ld) if len(merged) == 2 and ld >= cols else None
 
 
+def _overlaps(t: torch.Tensor) -> bool:
+    """Whether two elements may share memory (expanded tensors, sliding windows)."""
+    reach = 0
+    for st, n in sorted((st, n) for n, st in zip(t.shape, t.stride()) if n > 1):
+        if st <= reach:
+            return True
+        reach += (n - 1) * st
+    return False
+
+
 def _row_major(t: torch.Tensor) -> bool:
     st = [st for n, st in zip(t.shape, t.stride()) if n != 1]
     return st == sorted(st, reverse=True)
@@ -469,9 +479,10 @@ def _grad_entries(t: torch.Tensor, o: torch.Tensor, flags: int, out: list) -> No
 
 class GradTable:
     """A list of gradients (and, where clipped values go elsewhere, their
-    outputs) laid out on the device for grad_norm and clip_grad_norm.  It holds
-    the tensors and stays valid as long as they are not resized: a training
-    loop that keeps its gradient buffers builds it once."""
+    outputs) laid out on the device for grad_norm and clip_grad_norm.  It names
+    the tensors' memory and holds the tensors: a training loop that keeps its
+    gradient buffers builds it once (and before a graph is captured), one whose
+    gradients are new tensors every step passes the list instead."""
 
     def __init__(self, tensors: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
         self.tensors = list(tensors)
@@ -488,8 +499,8 @@ class GradTable:
             o = t if self.outs is None else self.outs[i]
             if o.shape != t.shape:
                 raise ValueError(f"output {i} has shape {tuple(o.shape)}, its gradient {tuple(t.shape)}")
-            if any(st == 0 and n > 1 for v in (t, o) for n, st in zip(v.shape, v.stride())):
-                raise ValueError(f"gradient {i} or its output is an expanded tensor")
+            if _overlaps(t) or (o is not t and _overlaps(o)):
+                raise ValueError(f"elements of gradient {i} or of its output share memory")
             flags = (_GRAD_F32 if _is_f32(t, f"gradient {i}") else 0) | (_GRAD_OUT_F32 if _is_f32(o, f"output {i}") else 0)
             _grad_entries(t, o, flags, entries)
         L = _fb.lib()

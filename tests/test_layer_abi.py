@@ -211,6 +211,15 @@ def test_rows_of_gradients():
     assert [(e.rows, e.cols, e.ld, e.ldo) for e in entries] == [(4, 1, 6, 1)] * 6
 
 
+def test_shared_memory_is_found():
+    t = torch.empty(6, 10, 8)
+    for ok in (t, t.permute(1, 2, 0), t[:, 2:7, ::3], t[0, 0, 0], torch.empty(1, 5).expand(1, 5), torch.empty(0, 3)):
+        assert not layer._overlaps(ok)
+    for bad in (torch.empty(5, 1).expand(5, 4), torch.empty(20).as_strided((5, 4), (2, 1)),
+                torch.empty(40).as_strided((3, 3, 3), (9, 2, 1))):
+        assert layer._overlaps(bad)
+
+
 def test_binding_refuses():
     """Shapes, types and devices are checked before the library is called."""
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
