@@ -107,12 +107,19 @@ def _ld(t: Optional[torch.Tensor]) -> int:
     return ld if ld >= cols else cols
 
 
+def _mat(t: torch.Tensor, dtype, shape, what: str) -> int:
+    """Row pitch of a matrix argument, checked."""
+    if t.dtype != dtype or t.shape != shape:
+        _need(t, dtype, what)
+        _shape(t, shape, what)
+    ld, step = t.stride()
+    return ld if step == 1 and ld >= shape[1] else _ld(t)
+
+
 def _out(t: Optional[torch.Tensor], rows: int, cols: int, dtype, like: torch.Tensor, what: str):
     """(t, its pitch): the given output, checked, or a new one beside `like`."""
     if t is not None:
-        _need(t, dtype, what)
-        _shape(t, (rows, cols), what)
-        return t, _ld(t)
+        return t, _mat(t, dtype, (rows, cols), what)
     per = 16 // dtype.itemsize
     if cols % per == 0:
         if like.dtype == dtype and like.shape == (rows, cols) and like.is_contiguous():
@@ -295,9 +302,7 @@ def _gate(gate, M: int, C: int):
     """(gate per channel or None, flag, pitch)."""
     if gate is None or gate.dim() == 1:
         return gate, 0, 0
-    _need(gate, torch.bfloat16, "a gate per token")
-    _shape(gate, (M, C), "gate")
-    return None, _NORM_GATE_ROW, _ld(gate)
+    return None, _NORM_GATE_ROW, _mat(gate, torch.bfloat16, (M, C), "a gate per token")
 
 
 def residual_norm(x: torch.Tensor, w_pre=None, f=None, w_post=None, gate=None, alpha: float = 1.0, eps: float = 1e-6,
@@ -326,9 +331,7 @@ def residual_norm(x: torch.Tensor, w_pre=None, f=None, w_post=None, gate=None, a
     rstd_post = rstd_pre = None
     ldf = ldxo = ldn = ldq = 0
     if f is not None:
-        _need(f, torch.bfloat16, "f")
-        _shape(f, (M, C), "f")
-        ldf = _ld(f)
+        ldf = _mat(f, torch.bfloat16, (M, C), "f")
         x_out, ldxo = _out(x_out, M, C, x.dtype, x, "x_out")
         if w_post is not None:
             rstd_post = torch.empty(M, dtype=torch.float32, device=dev)
@@ -372,9 +375,10 @@ def residual_norm_backward(x_out: torch.Tensor, dx_out=None, dn=None, rstd_pre=N
         raise ValueError("neither dx_out nor dn is given")
     if (w_post is not None or gate is not None) and f is None:
         raise ValueError("w_post and gate need f")
+    mat = (M, C)
+    lddxo = lddn = lddx = ldf = lddf = lddg = 0
     if dx_out is not None:
-        _need(dx_out, x_out.dtype, "dx_out")
-        _shape(dx_out, (M, C), "dx_out")
+        lddxo = _mat(dx_out, x_out.dtype, mat, "dx_out")
     if (dn is None) != (w_pre is None) or (rstd_pre is None) != (w_pre is None):
         raise ValueError("dn, rstd_pre and w_pre go together")
     if (rstd_post is None) != (w_post is None):
@@ -382,16 +386,13 @@ def residual_norm_backward(x_out: torch.Tensor, dx_out=None, dn=None, rstd_pre=N
     dw_pre = dw_post = dgate = None
     new = torch.empty
     if w_pre is not None:
-        _need(dn, torch.bfloat16, "dn")
-        _shape(dn, (M, C), "dn")
+        lddn = _mat(dn, torch.bfloat16, mat, "dn")
         _dense(rstd_pre, torch.float32, (M,), "rstd_pre")
         dw_pre = new(C, dtype=torch.float32, device=dev)
-    lddx = lddf = lddg = 0
     if w_pre is not None or dx is not None:
         dx, lddx = _out(dx, M, C, x_out.dtype, x_out, "dx")
     if f is not None:
-        _need(f, torch.bfloat16, "f")
-        _shape(f, (M, C), "f")
+        ldf = _mat(f, torch.bfloat16, mat, "f")
         df, lddf = _out(df, M, C, torch.bfloat16, f, "df")
         if w_post is not None:
             _dense(rstd_post, torch.float32, (M,), "rstd_post")
@@ -409,8 +410,8 @@ def residual_norm_backward(x_out: torch.Tensor, dx_out=None, dn=None, rstd_pre=N
         workspace = new((ws_bytes + 3) // 4, dtype=torch.float32, device=dev)
     if dx is not None or f is not None:
         _fb._check(L.fp8blk_residual_norm_backward(
-            M, C, x_out.data_ptr(), _ld(x_out), _addr(dx_out), _ld(dx_out), _addr(dn), _ld(dn), _addr(rstd_pre),
-            _addr(w_pre), _addr(f), _ld(f), _addr(rstd_post), _addr(w_post), _addr(gate), ldg, alpha, _addr(dx), lddx,
+            M, C, x_out.data_ptr(), _ld(x_out), _addr(dx_out), lddxo, _addr(dn), lddn, _addr(rstd_pre),
+            _addr(w_pre), _addr(f), ldf, _addr(rstd_post), _addr(w_post), _addr(gate), ldg, alpha, _addr(dx), lddx,
             _addr(df), lddf, _addr(dw_pre), _addr(dw_post), _addr(dgate), lddg, _addr(workspace), ws_bytes, flags,
             stream), "residual_norm_backward")
     return ResidualNormGrad(dx_out if dx is None else dx, df, dw_pre, dw_post, dgate)
