@@ -237,6 +237,33 @@ def test_binding_refuses():
     with pytest.raises(ValueError):
         fb.grad_norm([x])
     for bad in (x[:1].expand(4, 64), x.t(), x[:, ::2]):  # rows on top of each other, columns apart
-        with pytest.raises(ValueError):
-            layer._ld(bad)
-    assert layer._ld(x[:1].expand(1, 64)) == 64 and layer._ld(x[:, :40]) == 64 and layer._ld(None) == 0
+        with pytest.raises(ValueError, match="row-major|shape|T ="):
+            fb.moe_dispatch(bad, ids)
+    with pytest.raises(TypeError):
+        fb.moe_combine(torch.zeros(8, 64, dtype=torch.bfloat16), ids, weights=3)
+    with pytest.raises(TypeError):
+        fb.moe_combine(torch.zeros(8, 64, dtype=torch.float16), ids)
+    with pytest.raises(ValueError):
+        fb.residual_norm(x, w_pre=torch.ones(63))
+    with pytest.raises(TypeError):
+        fb.residual_norm(x, w_pre=torch.ones(64), f=x, w_post=torch.ones(64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        fb.residual_norm(x)
+    with pytest.raises(ValueError):
+        fb.residual_norm_backward(x, dx_out=x, dn=x)
+    with pytest.raises(ValueError):
+        fb.residual_norm_backward(x)
+    lent = torch.zeros(1, dtype=torch.int32).expand(1 << 20)  # four bytes, however long
+    with pytest.raises(ValueError, match="contiguous"):
+        fb.moe_sort(ids, 8, workspace=lent)
+    with pytest.raises(ValueError, match="contiguous"):
+        fb.residual_norm_backward(x, dx_out=x, workspace=lent)
+
+
+def test_binding_fails_loudly_without_its_extension(monkeypatch):
+    import sys
+    monkeypatch.setattr(layer, "_EXT", None)
+    monkeypatch.delattr(fb, "_layer_ext", raising=False)
+    monkeypatch.setitem(sys.modules, "fp8_fine_grained_quantize_amd._layer_ext", None)  # as if it were missing
+    with pytest.raises(fb.Fp8BlkError, match="build"):
+        layer._ext()
