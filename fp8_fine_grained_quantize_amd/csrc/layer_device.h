@@ -115,10 +115,11 @@ __device__ __forceinline__ void unpack_end(const RawV<T, V>& r, int64_t col, int
   unpack_v<T, V>(r, v);
   if (EXACT || (!LONG && C < V)) return;
   const int64_t d = col + V - C;  // elements that precede column col in r
-  if (d <= 0) return;
+  if (__ballot(d > 0) == 0) return;  // every wave but the row's last one
+  asm volatile("");                  // keeps the branch: the moves are as much work as all else
 #pragma unroll
   for (int k = 1; k < V; k *= 2) {
-    const bool move = (d & k) != 0;
+    const bool move = d > 0 && (d & k) != 0;
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = move ? (j + k < V ? v[j + k] : 0.0f) : v[j];
   }
@@ -171,12 +172,25 @@ __device__ __forceinline__ float row16_sum(float v) {
   v += dpp_f32<0x140>(v);  // row_mirror
   return v;
 }
-__device__ __forceinline__ float wave_sum(float v) {
-  v = row16_sum(v);
+__device__ __forceinline__ float add_row16(float v) {  // of a pair of rows
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float add_row32(float v) {  // of the wave's halves
   const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(h[0]) + __uint_as_float(h[1]);
+}
+__device__ __forceinline__ float wave_sum(float v) { return add_row32(add_row16(row16_sum(v))); }
+// The same over groups of 16, 32 or 64 lanes (`lanes`, uniform): groups that
+// have left the loop around it are not read.
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], int lanes) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = row16_sum(v[i]);
+    if (lanes > 16) v[i] = add_row16(v[i]);
+    if (lanes > 32) v[i] = add_row32(v[i]);
+  }
 }
 template <int CTRL>
 __device__ __forceinline__ double dpp_f64(double v) {
@@ -194,6 +208,13 @@ __device__ __forceinline__ double wave_sum(double v) {
   v += __shfl_xor(v, 32);
   return v;
 }
+
+// Waits for this wave's loads.  Before a row's successor is loaded in a loop:
+// where the loads that follow may be skipped, the compiler can wait for a value
+// only by waiting for every load, the successor's too, so the present row's
+// values have to be there first (gradient of the norm, 32768 x 4096 with a gate
+// per token: 346 us without, 261 with).
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
 
 // A barrier that orders LDS accesses only: global loads and stores in flight
 // stay in flight across it.

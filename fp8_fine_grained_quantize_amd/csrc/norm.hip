@@ -20,6 +20,8 @@
 namespace fp8blk {
 
 constexpr int64_t kNormMaxC = 16384;
+constexpr int64_t kPackMaxC = 512;  // rows up to here: several to a workgroup, each held by one wave or part of it
+constexpr int kPackLanes = 512;     // most lanes of such a workgroup
 
 struct NormFwd {
   const void* x;
@@ -36,6 +38,7 @@ struct NormFwd {
   int64_t M, C, ldx, ldf, ldg, ldxo, ldn, ldq;
   float alpha, eps;
   uint32_t flags;
+  int group;  // lanes of a row where a workgroup takes several
 };
 
 // Eight parameters of either type from an element-aligned vector.
@@ -86,6 +89,28 @@ __device__ __forceinline__ void store_codes8(uint8_t* p, int64_t avail, uint2 c)
 // The statistic of a row: (sum / C + eps)^(-1/2).
 __device__ __forceinline__ float rstd_of(float sum, float inv_c, float eps) { return 1.0f / sqrtf(sum * inv_c + eps); }
 
+// Which rows a lane works on.  A workgroup has one row at a time, or (PACK,
+// rows of at most 512 channels) one for each group of 16, 32 or 64 lanes.
+template <bool PACK>
+struct Rows {
+  int lane, lanes;      // of the row's
+  int64_t first, step;  // the lane's rows
+  __device__ __forceinline__ explicit Rows(int group) {
+    lanes = PACK ? group : (int)blockDim.x;
+    lane = PACK ? (int)threadIdx.x & (group - 1) : (int)threadIdx.x;
+    const int per = PACK ? (int)blockDim.x / group : 1;
+    first = PACK ? (int64_t)blockIdx.x * per + threadIdx.x / group : blockIdx.x;
+    step = (int64_t)gridDim.x * per;
+  }
+  __device__ __forceinline__ int64_t col(int c) const { return ((int64_t)lane + (int64_t)c * lanes) * 8; }
+  // Sums over the row's lanes (block_sum's LDS array where it is a workgroup's).
+  template <int N>
+  __device__ __forceinline__ void sum(float (&v)[N], float* red) const {
+    if (PACK) group_sum<N>(v, lanes);
+    else block_sum<N>(v, red, lanes >> 6);
+  }
+};
+
 // What a lane reads of one row, before it is unpacked.
 template <typename TX, int NCH, bool GATE_ROW, bool EXACT>
 struct NormRow {
@@ -93,35 +118,39 @@ struct NormRow {
   RawV<uint16_t, 8> f[NCH], gate[GATE_ROW ? NCH : 1];
 };
 
-template <bool NT, typename TX, int NCH, bool GATE_ROW, bool EXACT>
-__device__ __forceinline__ void load_row(NormRow<TX, NCH, GATE_ROW, EXACT>& r, const NormFwd& a, int64_t row) {
+template <bool NT, typename TX, int NCH, bool GATE_ROW, bool EXACT, bool PACK>
+__device__ __forceinline__ void load_row(NormRow<TX, NCH, GATE_ROW, EXACT>& r, const NormFwd& a, const Rows<PACK>& rows,
+                                         int64_t row) {
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * blockDim.x) * 8;
-    r.x[c] = load_end<8, EXACT, NT, (NCH > 1)>(reinterpret_cast<const TX*>(a.x) + row * a.ldx, col, a.C);
-    if (a.f != nullptr) r.f[c] = load_end<8, EXACT, NT, (NCH > 1)>(a.f + row * a.ldf, col, a.C);
-    if (GATE_ROW) r.gate[c] = load_end<8, EXACT, NT, (NCH > 1)>(reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg, col, a.C);
+    const int64_t col = rows.col(c);
+    r.x[c] = load_end<8, EXACT, NT, !PACK>(reinterpret_cast<const TX*>(a.x) + row * a.ldx, col, a.C);
+    if (a.f != nullptr) r.f[c] = load_end<8, EXACT, NT, !PACK>(a.f + row * a.ldf, col, a.C);
+    if (GATE_ROW)
+      r.gate[c] = load_end<8, EXACT, NT, !PACK>(reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg, col, a.C);
   }
 }
 
 // A workgroup takes the rows blockIdx.x, blockIdx.x + gridDim.x, ...; lane t
 // holds the chunks of eight channels t, t + NT, ... (NCH of them), so that a
-// 1x128 tile is one row of 16 lanes, and the parameters of its channels.  The
-// next row is loaded before the present one is worked on: the reductions and
-// stores of one row cover the other's way from HBM, which bounds it.  8192 x 7168
-// (BF16, n and E4M3 out) takes 96 us, 530 MB at 5.5 TB/s; without the next row
-// in flight and with the parameters read again for every row it took 162.  A
-// decode step of 16 rows takes 5.5 us: launch, one load, two reductions.
-template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT>
-__global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
+// 1x128 tile is one row of 16 lanes, and the parameters of its channels.  Rows
+// of at most 512 channels lie several to a workgroup and need no barrier (PACK;
+// 1048576 x 128, norm only: 100 us, 211 with a workgroup each).  The next row is
+// loaded before the present one is worked on: the reductions and stores of one
+// row cover the other's way from HBM, which bounds it.  8192 x 7168 (BF16, n and
+// E4M3 out) takes 96 us, 530 MB at 5.5 TB/s; without the next row in flight and
+// with the parameters read again for every row it took 162.  A decode step of 16
+// rows takes 5.5 us: launch, one load, two reductions.
+template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT, bool PACK>
+__global__ __launch_bounds__(PACK ? kPackLanes : 1024) void k_residual_norm(const NormFwd a) {
   __shared__ float red[2][2][16];
-  const int nt = blockDim.x, nw = nt >> 6;
+  const Rows<PACK> rows(a.group);
   const float inv_c = 1.0f / (float)a.C;
   const bool pf32 = (a.flags & FP8BLK_NORM_PARAM_F32) != 0;
   float pc[NCH][8], wn[NCH][8];  // alpha * w_post * (gate per channel); w_pre
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
+    const int64_t col = rows.col(c);
 #pragma unroll
     for (int i = 0; i < 8; ++i) pc[c][i] = a.alpha;
     float w[8];
@@ -138,15 +167,15 @@ __global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
     if (a.w_pre != nullptr) load_param8<EXACT>(a.w_pre, pf32, col, a.C, wn[c]);
   }
   NormRow<TX, NCH, GATE_ROW, EXACT> next;
-  load_row<NT>(next, a, blockIdx.x);
+  if (!PACK || rows.first < a.M) load_row<NT>(next, a, rows, rows.first);
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
+  for (int64_t row = rows.first; row < a.M; row += rows.step, turn ^= 1) {
     const NormRow<TX, NCH, GATE_ROW, EXACT> cur = next;
-    if (row + gridDim.x < a.M) load_row<NT>(next, a, row + gridDim.x);
+    if (row + rows.step < a.M) load_row<NT>(next, a, rows, row + rows.step);
     float z[NCH][8];
 #pragma unroll
     for (int c = 0; c < NCH; ++c)
-      unpack_end<TX, 8, EXACT, (NCH > 1)>(cur.x[c], ((int64_t)threadIdx.x + (int64_t)c * nt) * 8, a.C, z[c]);
+      unpack_end<TX, 8, EXACT, !PACK>(cur.x[c], rows.col(c), a.C, z[c]);
     if (a.f != nullptr) {
       float r = 1.0f;
       if (a.w_post != nullptr) {
@@ -154,22 +183,22 @@ __global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
           float f[8];
-          unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.f[c], ((int64_t)threadIdx.x + (int64_t)c * nt) * 8, a.C, f);
+          unpack_end<uint16_t, 8, EXACT, !PACK>(cur.f[c], rows.col(c), a.C, f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(f[i], f[i], sum[0]);
         }
-        block_sum<1>(sum, red[turn][0], nw);
+        rows.sum(sum, red[turn][0]);
         r = rstd_of(sum[0], inv_c, a.eps);
-        if (a.rstd_post != nullptr && threadIdx.x == 0) a.rstd_post[row] = r;
+        if (a.rstd_post != nullptr && rows.lane == 0) a.rstd_post[row] = r;
       }
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
-        const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
+        const int64_t col = rows.col(c);
         float f[8];
-        unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.f[c], col, a.C, f);
+        unpack_end<uint16_t, 8, EXACT, !PACK>(cur.f[c], col, a.C, f);
         if (GATE_ROW) {
           float g[8];
-          unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.gate[c], col, a.C, g);
+          unpack_end<uint16_t, 8, EXACT, !PACK>(cur.gate[c], col, a.C, g);
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] *= g[i];
         }
@@ -184,12 +213,12 @@ __global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(z[c][i], z[c][i], sum[0]);
-    block_sum<1>(sum, red[turn][1], nw);
+    rows.sum(sum, red[turn][1]);
     const float r = rstd_of(sum[0], inv_c, a.eps);
-    if (a.rstd_pre != nullptr && threadIdx.x == 0) a.rstd_pre[row] = r;
+    if (a.rstd_pre != nullptr && rows.lane == 0) a.rstd_pre[row] = r;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      const int64_t chunk = (int64_t)threadIdx.x + (int64_t)c * nt, col = chunk * 8, avail = a.C - col;
+      const int64_t col = rows.col(c), avail = a.C - col;
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[c][i] = z[c][i] * r * wn[c][i];
       if (a.n != nullptr) store_end<8, EXACT, NT>(a.n + row * a.ldn, col, a.C, z[c]);
@@ -198,7 +227,7 @@ __global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
         const uint2 codes = a.flags & FP8BLK_SCALE_POW2 ? quantize_tile<true>(z[c], s) : quantize_tile<false>(z[c], s);
         if (avail > 0) {
           store_codes8<EXACT, NT>(a.q + row * a.ldq + col, avail, codes);
-          if ((threadIdx.x & 15) == 0) a.s[(chunk >> 4) * a.M + row] = s;
+          if ((rows.lane & 15) == 0) a.s[(col >> 7) * a.M + row] = s;
         }
       }
     }
@@ -218,9 +247,11 @@ __global__ __launch_bounds__(1024) void k_residual_norm(const NormFwd a) {
 // A workgroup takes the rows blockIdx.x, blockIdx.x + gridDim.x, ... with the
 // next row's loads in flight, keeps the accumulators in registers and writes
 // them as one row of partials, which k_norm_sums adds up in order.  HBM bounds
-// it: 8192 x 7168 takes 120 us, 705 MB at 5.9 TB/s, and the sums 5; with two
+// it: 8192 x 7168 takes 122 us, 705 MB at 5.8 TB/s, and the sums 5; with two
 // reductions a row, three accumulators per channel and no row ahead it was 222
-// + 16.
+// + 16.  The norm's gradient alone (POST: there is an f) keeps half the
+// registers, so twice the lanes are at work: 131072 x 1024 takes 142 us, 182
+// by the other kernel; 1048576 x 128 135, 204.
 // ---------------------------------------------------------------------------
 struct NormBwd {
   const void* x;
@@ -240,6 +271,7 @@ struct NormBwd {
   int64_t M, C, ldx, lddxo, lddn, ldf, ldg, lddx, lddf, lddg;
   float alpha;
   uint32_t flags;
+  int group;  // lanes of a row where a workgroup takes several
 };
 
 // What a lane reads of one chunk of one row, before it is unpacked.
@@ -249,16 +281,18 @@ struct NormBwdChunk {
   RawV<uint16_t, 8> dn, f, gate;
 };
 
-template <bool EXACT, bool NT, bool LONG, typename TX, bool GATE_ROW>
+template <bool EXACT, bool NT, bool LONG, bool POST, typename TX, bool GATE_ROW>
 __device__ __forceinline__ void load_chunk(NormBwdChunk<TX, GATE_ROW>& r, const NormBwd& a, int64_t row, int64_t col) {
   r = {};
   if (a.w_pre != nullptr) {
     r.x = load_end<8, EXACT, NT, LONG>(reinterpret_cast<const TX*>(a.x) + row * a.ldx, col, a.C);
     r.dn = load_end<8, EXACT, NT, LONG>(a.dn + row * a.lddn, col, a.C);
   }
-  if (a.dxo != nullptr) r.dxo = load_end<8, EXACT, NT, LONG>(reinterpret_cast<const TX*>(a.dxo) + row * a.lddxo, col, a.C);
-  if (a.f != nullptr) r.f = load_end<8, EXACT, NT, LONG>(a.f + row * a.ldf, col, a.C);
-  if (GATE_ROW) r.gate = load_end<8, EXACT, NT, LONG>(reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg, col, a.C);
+  if (a.dxo != nullptr)
+    r.dxo = load_end<8, EXACT, NT, LONG>(reinterpret_cast<const TX*>(a.dxo) + row * a.lddxo, col, a.C);
+  if (POST) r.f = load_end<8, EXACT, NT, LONG>(a.f + row * a.ldf, col, a.C);
+  if (GATE_ROW)
+    r.gate = load_end<8, EXACT, NT, LONG>(reinterpret_cast<const uint16_t*>(a.gate) + row * a.ldg, col, a.C);
 }
 
 // The parameters of a chunk: alpha * w_post * (gate per channel), and w_pre.
@@ -289,59 +323,86 @@ __device__ __forceinline__ void load_factors(const NormBwd& a, int64_t col, floa
 // x with a gate per token above 4096) 1024 lanes read factors and rows chunk
 // by chunk, and once more (from L2) after the reduction, with the accumulators
 // in LDS.
-template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT, bool HOLD>
-__global__ __launch_bounds__(HOLD ? 512 : 1024) void k_residual_norm_backward(const NormBwd a) {
+template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT, bool HOLD, bool PACK, bool POST>
+__global__ __launch_bounds__(PACK || (HOLD && POST) ? 512 : 1024) void k_residual_norm_backward(const NormBwd a) {
   constexpr int NH = HOLD ? NCH : 1, UNROLL = NH;  // without HOLD one chunk after the other
+  // Rows that end inside a chunk: the last lane takes the row's last eight
+  // channels, of which the lane before holds some too.  Both compute and store
+  // the same for them; sums over the row leave out the last lane's share.  No
+  // values are moved and no pieces stored while the row's other waves wait
+  // (65536 x 2051: 318 us, 580 with the end's values moved to their places).
+  constexpr int SUMS = POST ? 3 : 1;
+  constexpr bool OVER = HOLD && !EXACT && !PACK, FULL = EXACT || OVER;
   __shared__ float red[2][3 * 16];
-  const int nt = blockDim.x, nw = nt >> 6;
+  const Rows<PACK> rows(a.group);
   const float inv_c = 1.0f / (float)a.C;
-  __shared__ float acc[HOLD ? 1 : 2 * NCH * 8 * 1024];
+  auto col_of = [&](int c) { return OVER && rows.col(c) > a.C - 8 ? a.C - 8 : rows.col(c); };
+  auto twice = [&](int c) { return (int)(rows.col(c) - col_of(c)); };  // channels of the chunk that a lane before holds
+  auto store_col = [&](int c) { return OVER && twice(c) >= 8 ? a.C : col_of(c); };
+  __shared__ float acc[HOLD ? PACK ? 8 * kPackLanes : 1 : 2 * NCH * 8 * 1024];
   float s_pre[NH][8], s_post[NH][8], pc_[NH][8], wn_[NH][8];
   // this lane's accumulator `vec` (0: dn h, 1: g h') of channel i of chunk c in LDS
   auto slot = [&](int vec, int c, int i) -> float& { return acc[((vec * NCH + c) * 8 + i) * 1024 + threadIdx.x]; };
   NormBwdChunk<TX, GATE_ROW> next[NH], cur_[NH];
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
+    const int64_t col = col_of(c);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (HOLD) s_pre[c][i] = s_post[c][i] = 0.0f;
       else slot(0, c, i) = slot(1, c, i) = 0.0f;
     }
     if (HOLD) {
-      load_factors<GATE_ROW, EXACT>(a, col, pc_[c], wn_[c]);
-      load_chunk<EXACT, NT, (NCH > 1)>(next[c], a, blockIdx.x, col);
+      load_factors<GATE_ROW, FULL>(a, col, pc_[c], wn_[c]);
+      if (!PACK || rows.first < a.M) load_chunk<FULL, NT, !PACK, POST>(next[c], a, rows.first, col);
     }
   }
+  const bool pre = a.w_pre != nullptr, post = POST && a.w_post != nullptr;
+  float next_pre = 0.0f, next_post = 1.0f;  // the statistics of the next row
+  if (HOLD && rows.first < a.M) {
+    if (pre) next_pre = a.rstd_pre[rows.first];
+    if (post) next_post = a.rstd_post[rows.first];
+  }
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
-    const float r_pre = a.w_pre != nullptr ? a.rstd_pre[row] : 0.0f;
-    const float r_post = a.w_post != nullptr ? a.rstd_post[row] : 1.0f;
-    if (HOLD) {
+  for (int64_t row = rows.first; row < a.M; row += rows.step, turn ^= 1) {
+    float r_pre = next_pre, r_post = next_post;
+    if (!HOLD) {
+      if (pre) r_pre = a.rstd_pre[row];
+      if (post) r_post = a.rstd_post[row];
+    } else {
+      wait_loads();
+      if (row + rows.step < a.M) {
+        if (pre) next_pre = a.rstd_pre[row + rows.step];
+        if (post) next_post = a.rstd_post[row + rows.step];
+      }
 #pragma unroll
       for (int c = 0; c < NH; ++c) {
         cur_[c] = next[c];
-        if (row + gridDim.x < a.M)
-          load_chunk<EXACT, NT, (NCH > 1)>(next[c], a, row + gridDim.x, ((int64_t)threadIdx.x + (int64_t)c * nt) * 8);
+        if (row + rows.step < a.M)
+          load_chunk<FULL, NT, !PACK, POST>(next[c], a, row + rows.step, col_of(c));
       }
     }
-    float sum[3] = {0.0f, 0.0f, 0.0f};
+    float sum[SUMS] = {}, before[SUMS];  // before the present chunk
 #pragma unroll UNROLL
     for (int c = 0; c < NCH; ++c) {
       float(&pc)[8] = pc_[HOLD ? c : 0];
       float(&wn)[8] = wn_[HOLD ? c : 0];
       NormBwdChunk<TX, GATE_ROW>& cur = cur_[HOLD ? c : 0];
-      const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
+      const int64_t col = col_of(c);
       if (!HOLD) {
-        load_factors<GATE_ROW, EXACT>(a, col, pc, wn);
-        load_chunk<EXACT, NT && HOLD, (NCH > 1)>(cur, a, row, col);
+        load_factors<GATE_ROW, FULL>(a, col, pc, wn);
+        load_chunk<FULL, NT && HOLD, !PACK, POST>(cur, a, row, col);
+      }
+      if (OVER) {
+#pragma unroll
+        for (int i = 0; i < SUMS; ++i) before[i] = sum[i];
       }
       float h[8], v[8], g[8], hf[8], gt[8];
-      unpack_end<TX, 8, EXACT, (NCH > 1)>(cur.x, col, a.C, h);
-      unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.dn, col, a.C, v);
-      unpack_end<TX, 8, EXACT, (NCH > 1)>(cur.dxo, col, a.C, g);
-      unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.f, col, a.C, hf);
-      if (GATE_ROW) unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.gate, col, a.C, gt);
+      unpack_end<TX, 8, FULL, !PACK>(cur.x, col, a.C, h);
+      unpack_end<uint16_t, 8, FULL, !PACK>(cur.dn, col, a.C, v);
+      unpack_end<TX, 8, FULL, !PACK>(cur.dxo, col, a.C, g);
+      if (POST) unpack_end<uint16_t, 8, FULL, !PACK>(cur.f, col, a.C, hf);
+      if (GATE_ROW) unpack_end<uint16_t, 8, FULL, !PACK>(cur.gate, col, a.C, gt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         h[i] *= r_pre;
@@ -349,37 +410,53 @@ __global__ __launch_bounds__(HOLD ? 512 : 1024) void k_residual_norm_backward(co
         sp = __builtin_fmaf(v[i], h[i], sp);
         v[i] *= wn[i];
         sum[0] = __builtin_fmaf(v[i], h[i], sum[0]);
+        if (!POST) continue;
         float p = pc[i] * (hf[i] * r_post);
         if (GATE_ROW) p *= gt[i];
-        sum[1] = __builtin_fmaf(p, __builtin_fmaf(r_pre, v[i], g[i]), sum[1]);
-        sum[2] = __builtin_fmaf(p, h[i], sum[2]);
+        sum[POST ? 1 : 0] = __builtin_fmaf(p, __builtin_fmaf(r_pre, v[i], g[i]), sum[POST ? 1 : 0]);
+        sum[POST ? 2 : 0] = __builtin_fmaf(p, h[i], sum[POST ? 2 : 0]);
+      }
+      if (OVER && __ballot(twice(c) > 0) != 0) {  // the row's last wave: once more, without them
+        asm volatile("");
+#pragma unroll
+        for (int i = 0; i < SUMS; ++i) sum[i] = twice(c) > 0 ? before[i] : sum[i];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+          if (twice(c) == 0 || i < twice(c)) continue;
+          sum[0] = __builtin_fmaf(v[i], h[i], sum[0]);
+          if (!POST) continue;
+          float p = pc[i] * (hf[i] * r_post);
+          if (GATE_ROW) p *= gt[i];
+          sum[POST ? 1 : 0] = __builtin_fmaf(p, __builtin_fmaf(r_pre, v[i], g[i]), sum[POST ? 1 : 0]);
+          sum[POST ? 2 : 0] = __builtin_fmaf(p, h[i], sum[POST ? 2 : 0]);
+        }
       }
     }
-    block_sum<3>(sum, red[turn], nw);
+    rows.sum(sum, red[turn]);
     const float m = sum[0] * inv_c;
-    const float m_post = a.w_post != nullptr ? (sum[1] - r_pre * m * sum[2]) * inv_c : 0.0f;
+    const float m_post = post ? (sum[POST ? 1 : 0] - r_pre * m * sum[POST ? 2 : 0]) * inv_c : 0.0f;
 #pragma unroll UNROLL
     for (int c = 0; c < NCH; ++c) {
-      const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
+      const int64_t col = col_of(c);
       float(&pc)[8] = pc_[HOLD ? c : 0];
       float(&wn)[8] = wn_[HOLD ? c : 0];
       NormBwdChunk<TX, GATE_ROW>& cur = cur_[HOLD ? c : 0];
       if (!HOLD) {
-        load_factors<GATE_ROW, EXACT>(a, col, pc, wn);
-        load_chunk<EXACT, NT && HOLD, (NCH > 1)>(cur, a, row, col);
+        load_factors<GATE_ROW, FULL>(a, col, pc, wn);
+        load_chunk<FULL, NT && HOLD, !PACK, POST>(cur, a, row, col);
       }
       float h[8], v[8], g[8];
-      unpack_end<TX, 8, EXACT, (NCH > 1)>(cur.x, col, a.C, h);
-      unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.dn, col, a.C, v);
-      unpack_end<TX, 8, EXACT, (NCH > 1)>(cur.dxo, col, a.C, g);
+      unpack_end<TX, 8, FULL, !PACK>(cur.x, col, a.C, h);
+      unpack_end<uint16_t, 8, FULL, !PACK>(cur.dn, col, a.C, v);
+      unpack_end<TX, 8, FULL, !PACK>(cur.dxo, col, a.C, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         g[i] = __builtin_fmaf(r_pre, __builtin_fmaf(-(h[i] * r_pre), m, v[i] * wn[i]), g[i]);
-      if (a.dx != nullptr) store_end<8, EXACT, NT>(reinterpret_cast<TX*>(a.dx) + row * a.lddx, col, a.C, g);
-      if (a.f == nullptr) continue;
-      unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.f, col, a.C, h);
+      if (a.dx != nullptr) store_end<8, FULL, NT>(reinterpret_cast<TX*>(a.dx) + row * a.lddx, store_col(c), a.C, g);
+      if (!POST) continue;
+      unpack_end<uint16_t, 8, FULL, !PACK>(cur.f, col, a.C, h);
       float gt[8];
-      if (GATE_ROW) unpack_end<uint16_t, 8, EXACT, (NCH > 1)>(cur.gate, col, a.C, gt);
+      if (GATE_ROW) unpack_end<uint16_t, 8, FULL, !PACK>(cur.gate, col, a.C, gt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         h[i] *= r_post;
@@ -393,14 +470,30 @@ __global__ __launch_bounds__(HOLD ? 512 : 1024) void k_residual_norm_backward(co
       if (GATE_ROW) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= pc[i];
-        store_end<8, EXACT, NT>(a.dgate_row + row * a.lddg, col, a.C, v);
+        store_end<8, FULL, NT>(a.dgate_row + row * a.lddg, store_col(c), a.C, v);
       }
-      store_end<8, EXACT, NT>(a.df + row * a.lddf, col, a.C, g);
+      store_end<8, FULL, NT>(a.df + row * a.lddf, store_col(c), a.C, g);
     }
+  }
+  if (PACK) {  // the groups' accumulators are added in order: one row of partials
+#pragma unroll
+    for (int vec = 0; vec < 2; ++vec) {
+      float* part = vec == 0 ? a.part_pre : a.part_post;
+      if (part == nullptr) continue;
+      if (vec == 1) __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[threadIdx.x * 8 + i] = vec == 0 ? s_pre[0][i] : s_post[0][i];
+      __syncthreads();
+      for (int col = threadIdx.x; col < a.C; col += blockDim.x) {
+        float t = 0.0f;
+        for (int g = 0; g < (int)blockDim.x; g += rows.lanes) t += acc[g * 8 + col];
+        part[(int64_t)blockIdx.x * a.C + col] = t;
+      }
+    }
+    return;
   }
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int64_t col = ((int64_t)threadIdx.x + (int64_t)c * nt) * 8;
     if (!HOLD) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -408,14 +501,17 @@ __global__ __launch_bounds__(HOLD ? 512 : 1024) void k_residual_norm_backward(co
         s_post[0][i] = slot(1, c, i);
       }
     }
-    if (a.part_pre != nullptr) store_end<8, EXACT, false>(a.part_pre + (int64_t)blockIdx.x * a.C, col, a.C, s_pre[HOLD ? c : 0]);
-    if (a.part_post != nullptr) store_end<8, EXACT, false>(a.part_post + (int64_t)blockIdx.x * a.C, col, a.C, s_post[HOLD ? c : 0]);
+    const int64_t part = (int64_t)blockIdx.x * a.C, at = store_col(c);
+    if (a.part_pre != nullptr) store_end<8, FULL, false>(a.part_pre + part, at, a.C, s_pre[HOLD ? c : 0]);
+    if (a.part_post != nullptr) store_end<8, FULL, false>(a.part_post + part, at, a.C, s_post[HOLD ? c : 0]);
   }
 }
 
-// Sums over the nb rows of partials in a fixed order: 64 columns per
-// workgroup, sixteen row classes, then the sixteen sums in order; blockIdx.y
-// picks the vector.  Of the second, both dw_post and dgate are made.
+// Sums over the nb rows of partials in a fixed order: kSumCols columns per
+// workgroup, 1024 / kSumCols row classes, then their sums in order; blockIdx.y
+// picks the vector.  Of the second, both dw_post and dgate are made.  Dependent
+// loads bound it (8192 x 1024, gradient and sums: 18.8 us, 22.7 with 64 columns).
+constexpr int kSumCols = 32;
 struct NormSums {
   const float* part[2];
   float* dw_pre;
@@ -430,17 +526,18 @@ __device__ __forceinline__ float param_at(const void* p, bool f32, int64_t i) {
   return f32 ? reinterpret_cast<const float*>(p)[i] : to_f32(reinterpret_cast<const uint16_t*>(p)[i]);
 }
 __global__ __launch_bounds__(1024) void k_norm_sums(const NormSums a, int first, int64_t nb, int64_t C) {
-  __shared__ float acc[16][64];
+  constexpr int CLASSES = 1024 / kSumCols;
+  __shared__ float acc[CLASSES][kSumCols];
   const int vec = first + blockIdx.y;
   const float* part = a.part[vec];
-  const int lane = threadIdx.x & 63, cls = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 64 + lane;
+  const int lane = threadIdx.x % kSumCols, cls = threadIdx.x / kSumCols;
+  const int64_t col = (int64_t)blockIdx.x * kSumCols + lane;
   float sum = 0.0f;
   if (col < C) {
-    for (int64_t b = cls; b < nb; b += 16 * 8) {
+    for (int64_t b = cls; b < nb; b += CLASSES * 8) {
       float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = b + 16 * i < nb ? part[(b + 16 * i) * C + col] : 0.0f;
+      for (int i = 0; i < 8; ++i) v[i] = b + CLASSES * i < nb ? part[(b + CLASSES * i) * C + col] : 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum += v[i];
     }
@@ -450,7 +547,7 @@ __global__ __launch_bounds__(1024) void k_norm_sums(const NormSums a, int first,
   if (cls == 0 && col < C) {
     float t = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t += acc[i][lane];
+    for (int i = 0; i < CLASSES; ++i) t += acc[i][lane];
     if (vec == 0) {
       a.dw_pre[col] = t;
     } else {
@@ -463,59 +560,89 @@ __global__ __launch_bounds__(1024) void k_norm_sums(const NormSums a, int first,
 
 // Chunks of eight channels per lane, and lanes of a row's workgroup (a multiple
 // of 64).  Forward: one chunk up to 1024 lanes, then two (8192 x 7168 took 97 us
-// with 896 lanes of one chunk, 99 with 448 of two).  Gradient: at most 512
-// lanes where they hold a row ahead, so that each may have 256 registers (123
-// us with 448 lanes of two chunks, 128 with 896 of one).
+// with 896 lanes of one chunk, 99 with 448 of two).  Gradient with an f: at most
+// 512 lanes where they hold a row ahead, so that each may have 256 registers
+// (123 us with 448 lanes of two chunks, 128 with 896 of one); without one, as
+// the forward.
 inline int forward_chunks(int64_t C) { return C > 8192 ? 2 : 1; }
 inline bool backward_holds(int64_t C, uint32_t flags) {
-  return C <= 4096 || (C <= 8192 && (flags & (FP8BLK_NORM_RES_F32 | FP8BLK_NORM_GATE_ROW)) !=
-                                        (FP8BLK_NORM_RES_F32 | FP8BLK_NORM_GATE_ROW));
+  constexpr uint32_t wide = FP8BLK_NORM_RES_F32 | FP8BLK_NORM_GATE_ROW;
+  return C <= 4096 || (C <= 8192 && (flags & wide) != wide);
 }
-inline int backward_chunks(int64_t C) { return C > 4096 ? 2 : 1; }
+inline int backward_chunks(int64_t C, bool post) { return C > (post ? 4096 : 8192) ? 2 : 1; }
 inline int norm_lanes(int64_t C, int chunks) {
   return (int)(ceil_div(ceil_div(C, (int64_t)8 * chunks), (int64_t)64) * 64);
 }
 
 // Workgroups of either kernel: `per_cu` lanes on a compute unit, as many as the
 // registers allow at a time (half or twice as many were 1-2 % slower in the
-// forward, twice as many 7 % in the gradient, 8192 x 7168).
+// forward, twice as many 7 % in the gradient, 8192 x 7168; 768 lanes instead of
+// 512 in the gradient, 65536 x 2048: 216 us, 204).
 inline int64_t norm_blocks(int64_t M, int lanes, int64_t per_cu) {
   int64_t n = per_cu / lanes;
   n = (n < 1 ? 1 : n) * device_cus();
   return M < n ? M : n;
 }
-inline int64_t norm_backward_blocks(int64_t M, int64_t C) {
-  return norm_blocks(M, norm_lanes(C, backward_chunks(C)), 512);
+// Rows of at most kPackMaxC channels: lanes of a row, and of a workgroup, the
+// fewest that reach every compute unit once (gradient of 512 x 128: 7.6 us in
+// workgroups of 64 lanes, 9.5 in 512; 1048576 x 128, norm only: 106 in 64, 100
+// in 512).
+inline int norm_group(int64_t C) { return C <= 128 ? 16 : C <= 256 ? 32 : 64; }
+inline int packed_lanes(int64_t M, int64_t C) {
+  int lanes = 64;
+  while (lanes < kPackLanes && M > (int64_t)(lanes / norm_group(C)) * device_cus()) lanes *= 2;
+  return lanes;
+}
+inline int64_t packed_blocks(int64_t M, int64_t C, int64_t per_cu) {
+  const int lanes = packed_lanes(M, C);
+  return norm_blocks(ceil_div(M, (int64_t)(lanes / norm_group(C))), lanes, per_cu);
+}
+inline int64_t norm_backward_blocks(int64_t M, int64_t C, bool post) {
+  const int64_t per_cu = post ? 512 : 1024;
+  return C <= kPackMaxC ? packed_blocks(M, C, per_cu) : norm_blocks(M, norm_lanes(C, backward_chunks(C, post)), per_cu);
 }
 
-template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT>
+template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT, bool PACK>
 void launch(const NormFwd& a, hipStream_t stream) {
-  const int lanes = norm_lanes(a.C, NCH);
-  hipLaunchKernelGGL((k_residual_norm<TX, NCH, GATE_ROW, EXACT, NT>), dim3((unsigned)norm_blocks(a.M, lanes, 2048)),
+  const int lanes = PACK ? packed_lanes(a.M, a.C) : norm_lanes(a.C, NCH);
+  const int64_t blocks = PACK ? packed_blocks(a.M, a.C, 2048) : norm_blocks(a.M, lanes, 2048);
+  hipLaunchKernelGGL((k_residual_norm<TX, NCH, GATE_ROW, EXACT, NT, PACK>), dim3((unsigned)blocks),
                      dim3((unsigned)lanes), 0, stream, a);
 }
-template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT, bool HOLD>
+template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT, bool HOLD, bool PACK, bool POST>
 void launch(const NormBwd& a, hipStream_t stream) {
-  hipLaunchKernelGGL((k_residual_norm_backward<TX, NCH, GATE_ROW, EXACT, NT, HOLD>),
-                     dim3((unsigned)norm_backward_blocks(a.M, a.C)), dim3((unsigned)norm_lanes(a.C, NCH)), 0, stream,
-                     a);
+  hipLaunchKernelGGL((k_residual_norm_backward<TX, NCH, GATE_ROW, EXACT, NT, HOLD, PACK, POST>),
+                     dim3((unsigned)norm_backward_blocks(a.M, a.C, POST)),
+                     dim3((unsigned)(PACK ? packed_lanes(a.M, a.C) : norm_lanes(a.C, NCH))), 0, stream, a);
 }
 
 // The kernel for the arguments' types and sizes.
 template <typename TX, bool GATE_ROW, bool EXACT, bool NT>
 void launch_chunks(const NormFwd& a, hipStream_t stream) {
-  if (forward_chunks(a.C) == 1) launch<TX, 1, GATE_ROW, EXACT, NT>(a, stream);
-  else launch<TX, 2, GATE_ROW, EXACT, NT>(a, stream);
+  if (a.C <= kPackMaxC) launch<TX, 1, GATE_ROW, EXACT, NT, true>(a, stream);
+  else if (forward_chunks(a.C) == 1) launch<TX, 1, GATE_ROW, EXACT, NT, false>(a, stream);
+  else launch<TX, 2, GATE_ROW, EXACT, NT, false>(a, stream);
+}
+template <typename TX, bool GATE_ROW, bool EXACT, bool NT, bool POST>
+void launch_held(const NormBwd& a, hipStream_t stream) {
+  if (a.C <= kPackMaxC) return launch<TX, 1, GATE_ROW, EXACT, NT, true, true, POST>(a, stream);
+  if (a.C > 8192) return launch<TX, 2, GATE_ROW, EXACT, NT, false, false, POST>(a, stream);
+  if constexpr (POST) {
+    if (!backward_holds(a.C, a.flags)) return launch<TX, 1, GATE_ROW, EXACT, NT, false, false, true>(a, stream);
+    if constexpr (!(GATE_ROW && sizeof(TX) == 4))
+      if (a.C > 4096) return launch<TX, 2, GATE_ROW, EXACT, NT, true, false, true>(a, stream);
+  }
+  launch<TX, 1, GATE_ROW, EXACT, NT, true, false, POST>(a, stream);
 }
 template <typename TX, bool GATE_ROW, bool EXACT, bool NT>
 void launch_chunks(const NormBwd& a, hipStream_t stream) {
-  if (!backward_holds(a.C, a.flags)) launch<TX, 2, GATE_ROW, EXACT, NT, false>(a, stream);
-  else if (backward_chunks(a.C) == 1) launch<TX, 1, GATE_ROW, EXACT, NT, true>(a, stream);
-  else launch<TX, 2, GATE_ROW, EXACT, NT, true>(a, stream);
+  if (GATE_ROW || a.f != nullptr) launch_held<TX, GATE_ROW, EXACT, NT, true>(a, stream);
+  else launch_held<TX, false, EXACT, NT, false>(a, stream);
 }
 template <typename TX, bool GATE_ROW, typename A>
 void launch_exact(const A& a, bool nt, hipStream_t stream) {
-  if (a.C % 8 != 0) return launch_chunks<TX, GATE_ROW, false, false>(a, stream);  // streamed 5 % slower: rows share lines
+  if (a.C % 8 != 0)  // streamed 5 % slower: rows share lines
+    return launch_chunks<TX, GATE_ROW, false, false>(a, stream);
   return nt ? launch_chunks<TX, GATE_ROW, true, true>(a, stream) : launch_chunks<TX, GATE_ROW, true, false>(a, stream);
 }
 // moved: bytes that the call reads and writes.
@@ -563,7 +690,7 @@ extern "C" fp8blk_status_t fp8blk_residual_norm(int64_t M, int64_t C, const void
     return FP8BLK_ERR_INVALID_ARG;
   if ((flags & FP8BLK_SCALE_POW2) && q == nullptr) return FP8BLK_ERR_INVALID_ARG;
   const NormFwd a{x, f, w_post, gate, w_pre, x_out, n, q, s, rstd_post, rstd_pre,
-                  M, C, ldx, ldf, ldg, ldxo, ldn, ldq, alpha, eps, flags};
+                  M, C, ldx, ldf, ldg, ldxo, ldn, ldq, alpha, eps, flags, norm_group(C)};
   const int64_t xe = xf ? 4 : 2;
   launch_norm(a, M * C * (xe + (f != nullptr ? 2 + xe : 0) + (gr ? 2 : 0) + (n != nullptr ? 2 : 0) + (q != nullptr ? 1 : 0)),
               as_stream(stream));
@@ -572,7 +699,8 @@ extern "C" fp8blk_status_t fp8blk_residual_norm(int64_t M, int64_t C, const void
 
 extern "C" size_t fp8blk_residual_norm_backward_workspace_bytes(int64_t M, int64_t C) {
   if (M <= 0 || C <= 0 || C > kNormMaxC) return 0;
-  return (size_t)(norm_backward_blocks(M, C) * C) * 2 * sizeof(float);
+  const int64_t both = 2 * norm_backward_blocks(M, C, true), one = norm_backward_blocks(M, C, false);
+  return (size_t)((both > one ? both : one) * C) * sizeof(float);
 }
 
 extern "C" fp8blk_status_t fp8blk_residual_norm_backward(
@@ -612,7 +740,7 @@ extern "C" fp8blk_status_t fp8blk_residual_norm_backward(
       return FP8BLK_ERR_INVALID_ARG;
   }
   const bool sums = pre || postw || (gated && !gr);
-  const int64_t nb = M > 0 ? norm_backward_blocks(M, C) : 0;
+  const int64_t nb = M > 0 ? norm_backward_blocks(M, C, f != nullptr) : 0;
   if (sums && nb > 0 &&
       (workspace == nullptr || !aligned(workspace, 16) ||
        workspace_bytes < fp8blk_residual_norm_backward_workspace_bytes(M, C)))
@@ -623,7 +751,7 @@ extern "C" fp8blk_status_t fp8blk_residual_norm_backward(
   if (nb > 0) {
     const NormBwd a{x_out, dx_out, dn, rstd_pre, w_pre, f, rstd_post, w_post, gate, dx, df,
                     gr ? reinterpret_cast<uint16_t*>(dgate) : nullptr, part_pre, part_post,
-                    M, C, ldx, lddxo, lddn, ldf, ldg, lddx, lddf, lddg, alpha, flags};
+                    M, C, ldx, lddxo, lddn, ldf, ldg, lddx, lddf, lddg, alpha, flags, norm_group(C)};
     launch_norm(a, M * C * ((pre ? xe + 2 : 0) + (dx_out != nullptr ? xe : 0) + (dx != nullptr ? xe : 0) +
                             (f != nullptr ? 4 : 0) + (gr ? 4 : 0)), as_stream(stream));
     const fp8blk_status_t st = launch_status();
@@ -633,8 +761,9 @@ extern "C" fp8blk_status_t fp8blk_residual_norm_backward(
     const int first = pre ? 0 : 1, last = postw || (gated && !gr) ? 1 : 0;
     const NormSums a{{part_pre, part_post}, dw_pre, dw_post, gr ? nullptr : reinterpret_cast<float*>(dgate), w_post,
                      gr ? nullptr : gate, alpha, (flags & FP8BLK_NORM_PARAM_F32) != 0};
-    hipLaunchKernelGGL(k_norm_sums, dim3((unsigned)ceil_div(C, (int64_t)64), (unsigned)(last - first + 1)), dim3(1024),
-                       0, as_stream(stream), a, first, nb, C);
+    const unsigned vecs = (unsigned)(last - first + 1);
+    hipLaunchKernelGGL(k_norm_sums, dim3((unsigned)ceil_div(C, (int64_t)kSumCols), vecs), dim3(1024), 0,
+                       as_stream(stream), a, first, nb, C);
     return launch_status();
   }
   return FP8BLK_OK;

@@ -228,6 +228,43 @@ def test_backward(M, C, post, pre, gate, res, param):
     assert np.all(np.abs(_np(g.df) - w["df"]) <= 3 * rel * d + UB * np.abs(w["df"]))
 
 
+# Rows that share a workgroup, in groups of 16, 32 and 64 lanes and more rows
+# than groups; rows that end inside a chunk, and one channel past each limit.
+ENDS = [(37, 100), (70, 129), (9001, 72), (33, 257), (41, 511), (600, 519), (5, 520), (260, 1025), (9, 4097), (9, 5001),
+        (5, 8191)]
+
+
+@pytest.mark.parametrize("post,pre,gate", [("none", True, "none"), ("norm", True, "channel"), ("norm", True, "row"),
+                                           ("add", False, "channel")])
+@pytest.mark.parametrize("M,C", ENDS)
+@pytest.mark.parametrize("res,param", TYPES)
+def test_row_ends_and_shared_workgroups(M, C, post, pre, gate, res, param):
+    test_forward(M, C, post, pre, gate, res, param)
+    if (post, gate) == ("norm", "channel"):
+        test_quantized(M, C, res == torch.float32, res == torch.bfloat16)
+    test_backward(M, C, post, pre, gate, res, param)
+
+
+@pytest.mark.parametrize("M,C", [(50, 100), (40, 300), (300, 1025), (20, 5001), (20, 7168), (6, 9001)])
+def test_backward_in_place(M, C):
+    """Gradients over their own inputs, outputs' padding untouched."""
+    xo, a = _grads(M, C, "norm", True, "channel", torch.bfloat16, torch.float32)
+    want = fb.residual_norm_backward(xo, alpha=ALPHA, **a)
+    a = {k: v if v is None or v.dim() != 2 else fb.as_pitched(v) for k, v in a.items()}
+    dx, df = a["dx_out"], a["f"]
+    got = fb.residual_norm_backward(xo, alpha=ALPHA, dx=dx, df=df, **a)
+    assert got.dx is dx and got.df is df
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("C", [64, 100, 1025, 7168])
+def test_backward_without_a_norm_copies(C):
+    d = _matrix(9, C, torch.bfloat16, 3)
+    out = _matrix(9, C, torch.bfloat16, 4)
+    g = fb.residual_norm_backward(d, dx_out=d, dx=out)
+    assert g.dx is out and torch.equal(out, d) and g.df is None and g.dw_pre is None
+
+
 def test_backward_twice_is_the_same():
     xo, a = _grads(2000, 264, "norm", True, "channel", torch.bfloat16, torch.float32)
     one, two = (fb.residual_norm_backward(xo, alpha=ALPHA, **a) for _ in range(2))
