@@ -152,11 +152,6 @@ __device__ __forceinline__ void store_end(T* row, int64_t col, int64_t C, const 
   }
 }
 
-template <bool NT>
-__device__ __forceinline__ void store_u128(void* p, const uint4& v) {
-  store_words<NT, 4>((Global<void>*)p, Words<4>::type{v.x, v.y, v.z, v.w});
-}
-
 // Sum over the wave's 64 lanes, the same bits in every lane.  FP32: four DPP
 // steps inside each row of 16 lanes, then the rows and the halves exchanged by
 // register swaps; no LDS traffic, where a lane exchange by __shfl costs an LDS

@@ -197,13 +197,21 @@ __global__ __launch_bounds__(1024) void k_moe_sort(const ID* __restrict__ ids, i
 // groups, written coalesced (the scales of all tokens stay in L2).  HBM writes
 // bound it: 8192 tokens of 7168 codes to 65536 rows take 99 us, 545 MB at 5.5
 // TB/s (109 through the caches); counters show each code and scale written once
-// and read at most once.  UNIT: bytes of an element, the granularity of a row's end.
+// and read at most once.  A row's last 16 bytes are moved whole, some of them by
+// two lanes (32768 tokens of 8 rows of 259 codes: 23 us, 41 byte by byte); UNIT,
+// the bytes of an element, is the step of rows shorter than that.
 // ---------------------------------------------------------------------------
 constexpr int kScaleGroups = 8;
 
+// Sixteen bytes at any address.
+typedef Words<4>::type Bytes16 __attribute__((aligned(1)));
+
 template <int UNIT>
 __device__ __forceinline__ uint4 load_part(const uint8_t* p, int64_t avail) {
-  if (avail >= 16) return *reinterpret_cast<const uint4*>(p);
+  if (avail >= 16) {
+    const auto v = *(const Global<const Bytes16>*)p;
+    return make_uint4(v.x, v.y, v.z, v.w);
+  }
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int j = 0; j < 16; j += UNIT)
@@ -217,7 +225,9 @@ __device__ __forceinline__ uint4 load_part(const uint8_t* p, int64_t avail) {
 template <int UNIT, bool NT>
 __device__ __forceinline__ void store_part(uint8_t* p, int64_t avail, const uint4& v) {
   if (avail >= 16) {
-    store_u128<NT>(p, v);
+    auto* q = (Global<Bytes16>*)p;
+    if (NT) __builtin_nontemporal_store(Bytes16{v.x, v.y, v.z, v.w}, q);
+    else *q = Bytes16{v.x, v.y, v.z, v.w};
     return;
   }
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -241,9 +251,10 @@ __global__ __launch_bounds__(256) void k_moe_dispatch(const uint8_t* __restrict_
   const int64_t copies = T * segs;
   if (!SCALES || (int64_t)blockIdx.x < copies) {
     const int64_t t = blockIdx.x / segs;
-    const int64_t col = ((int64_t)(blockIdx.x % segs) * blockDim.x + threadIdx.x) * 16;
+    int64_t col = ((int64_t)(blockIdx.x % segs) * blockDim.x + threadIdx.x) * 16;
+    if (col >= row_bytes) return;
+    if (row_bytes >= 16 && col > row_bytes - 16) col = row_bytes - 16;  // a row's end: some bytes twice
     const int64_t avail = row_bytes - col;
-    if (avail <= 0) return;
     const uint4 v = load_part<UNIT>(x + t * ldx + col, avail);
     for (uint32_t k = 0; k < K; ++k) {
       const int32_t r = row_of[t * K + k];
@@ -272,8 +283,11 @@ __global__ __launch_bounds__(256) void k_moe_dispatch(const uint8_t* __restrict_
 // stores are contiguous: FP32 in two accesses 32 bytes apart from lane to lane
 // took 387 us instead of 347 for the rows (8192 tokens, 8 rows of 7168 each)
 // and 348 instead of 252 for the sums (32768 tokens, one BF16 row of 7168 each).
-// HBM reads bound it: 8192 tokens of 8 FP32 rows of 7168 take 319 us, 2.0 GB at
-// 6.3 TB/s; a decode step of 16 tokens 3.6 us, its launch and two dependent loads.
+// The last V channels of a row that ends inside a lane's are summed whole, some
+// by two lanes (8192 tokens of one FP32 row of 7169: 77 us, 108 with the end
+// moved and stored in pieces).  HBM reads bound it: 8192 tokens of 8 FP32 rows of
+// 7168 take 319 us, 2.0 GB at 6.3 TB/s; a decode step of 16 tokens 3.6 us, its
+// launch and two dependent loads.
 // ---------------------------------------------------------------------------
 template <typename TR, typename TY>
 constexpr int combine_width() { return sizeof(TR) == 2 && sizeof(TY) == 2 ? 8 : 4; }
@@ -286,8 +300,9 @@ __global__ __launch_bounds__(256) void k_moe_combine(const TR* __restrict__ rows
   constexpr int V = combine_width<TR, TY>();
   const int64_t P = T * K;
   const int64_t t = blockIdx.x / segs;
-  const int64_t col = ((int64_t)(blockIdx.x % segs) * blockDim.x + threadIdx.x) * V;
+  int64_t col = ((int64_t)(blockIdx.x % segs) * blockDim.x + threadIdx.x) * V;
   if (col >= C) return;
+  if (!EXACT && C >= V && col > C - V) col = C - V;  // a row's end: some channels by two lanes, alike
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.0f;
@@ -306,7 +321,7 @@ __global__ __launch_bounds__(256) void k_moe_combine(const TR* __restrict__ rows
       if (!on[j]) continue;
       const float wk = WEIGHTED ? w[t * K + k0 + j] : 1.0f;
       float v[V];
-      unpack_end<TR, V, EXACT>(raw[j], col, C, v);
+      unpack_v<TR, V>(raw[j], v);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] = WEIGHTED ? __builtin_fmaf(wk, v[i], acc[i]) : acc[i] + v[i];
     }
@@ -349,14 +364,18 @@ __global__ __launch_bounds__(512) void k_moe_combine_backward(const TY* __restri
       wk[j] = on[j] ? w[t * K + k0 + j] : 0.0f;
       dot[j] = 0.0f;
     }
-    for (int64_t col = (int64_t)threadIdx.x * V; col < C; col += (int64_t)blockDim.x * V) {
+    for (int64_t c0 = (int64_t)threadIdx.x * V; c0 < C; c0 += (int64_t)blockDim.x * V) {
+      // a row's end: `twice` channels by two lanes, alike but for the dot products
+      const int64_t col = !EXACT && C >= V && c0 > C - V ? C - V : c0;
+      const int twice = (int)(c0 - col);
+      const bool ends = !EXACT && __ballot(twice > 0) != 0;
       float d[V];
       const RawV<TY, V> raw_dy = load_end<V, EXACT, false>(dy + t * lddy, col, C);
       RawV<TR, V> raw[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (on[j]) raw[j] = load_end<V, EXACT, NT>(rows + row[j] * ldr, col, C);
-      unpack_end<TY, V, EXACT>(raw_dy, col, C, d);
+      unpack_v<TY, V>(raw_dy, d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (row[j] < 0) continue;
@@ -365,9 +384,15 @@ __global__ __launch_bounds__(512) void k_moe_combine_backward(const TY* __restri
         for (int i = 0; i < V; ++i) o[i] = on[j] ? wk[j] * d[i] : 0.0f;
         if (on[j]) {
           float v[V];
-          unpack_end<TR, V, EXACT>(raw[j], col, C, v);
+          unpack_v<TR, V>(raw[j], v);
+          if (!ends) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) dot[j] = __builtin_fmaf(d[i], v[i], dot[j]);
+            for (int i = 0; i < V; ++i) dot[j] = __builtin_fmaf(d[i], v[i], dot[j]);
+          } else {
+            asm volatile("");  // a branch, not a choice at each channel
+#pragma unroll
+            for (int i = 0; i < V; ++i) dot[j] = i >= twice ? __builtin_fmaf(d[i], v[i], dot[j]) : dot[j];
+          }
         }
         store_end<V, EXACT, NT>(drows + row[j] * lddr, col, C, o);
       }
@@ -566,7 +591,8 @@ extern "C" fp8blk_status_t fp8blk_moe_dispatch_fp8(const uint8_t* q, int64_t T, 
   const int64_t blocks = T * sp.segs + ceil_div(P, (int64_t)256) * ceil_div(G, (int64_t)kScaleGroups);
   if (!grid_ok(blocks, sp.lanes)) return FP8BLK_ERR_UNSUPPORTED;
   hipLaunchKernelGGL(((P + T) * C >= kStreamBytes ? k_moe_dispatch<1, true, true> : k_moe_dispatch<1, true, false>),
-                     dim3((unsigned)blocks), dim3(sp.lanes), 0, as_stream(stream), q, ldq, C, T, (uint32_t)K, row_of, qr, ldqr, sp.segs, s, G, slot_of, sr);
+                     dim3((unsigned)blocks), dim3(sp.lanes), 0, as_stream(stream), q, ldq, C, T, (uint32_t)K, row_of, qr,
+                     ldqr, sp.segs, s, G, slot_of, sr);
   return launch_status();
 }
 

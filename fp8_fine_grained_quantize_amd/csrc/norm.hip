@@ -692,8 +692,8 @@ extern "C" fp8blk_status_t fp8blk_residual_norm(int64_t M, int64_t C, const void
   const NormFwd a{x, f, w_post, gate, w_pre, x_out, n, q, s, rstd_post, rstd_pre,
                   M, C, ldx, ldf, ldg, ldxo, ldn, ldq, alpha, eps, flags, norm_group(C)};
   const int64_t xe = xf ? 4 : 2;
-  launch_norm(a, M * C * (xe + (f != nullptr ? 2 + xe : 0) + (gr ? 2 : 0) + (n != nullptr ? 2 : 0) + (q != nullptr ? 1 : 0)),
-              as_stream(stream));
+  const int64_t each = xe + (f != nullptr ? 2 + xe : 0) + (gr ? 2 : 0) + (n != nullptr ? 2 : 0) + (q != nullptr ? 1 : 0);
+  launch_norm(a, M * C * each, as_stream(stream));
   return launch_status();
 }
 

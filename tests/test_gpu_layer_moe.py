@@ -162,6 +162,29 @@ def test_combine_backward(T, K, E, C, drop, dy_dt, rows_dt, drows_dt):
     assert np.all(np.abs(_np(dw) - wd) <= 2 * C * U * mag)
 
 
+@pytest.mark.parametrize("C", [3, 4, 7, 8, 9, 15, 16, 17, 31, 33, 65, 513, 1027, 2049])
+def test_row_ends(C):
+    """Rows around the widths that one lane moves or sums; the last lane's share
+    overlaps the one before."""
+    test_dispatch(37, 3, 9, C, 0.1, 1)
+    for a, b in ((torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16), (torch.bfloat16, torch.float32)):
+        test_combine(37, 3, 9, C, 0.1, a, b, True)
+        test_combine_backward(37, 3, 9, C, 0.1, a, b, a)
+
+
+def test_an_infinity_at_a_row_end_counts_once():
+    T, C = 4, 1027
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    _, row_of, _ = fb.moe_sort(ids, 1)
+    dy = fb.as_pitched(torch.ones(T, C, dtype=torch.bfloat16, device="cuda"))
+    rows, w = dy.clone(), torch.ones(T, 1, device="cuda")
+    rows = fb.as_pitched(rows)
+    rows[1, C - 5], rows[2, C - 1], dy[3, C - 2] = float("inf"), float("-inf"), float("inf")
+    drows, dw = fb.moe_combine_backward(dy, rows, row_of, w)
+    assert dw[:, 0].tolist() == [float(C), float("inf"), float("-inf"), float("inf")]
+    assert torch.equal(drows, dy)
+
+
 def test_gradients_by_differences():
     """Central differences of the 64-bit combine: exact up to rounding, as it
     is linear in the rows and in the weights."""
