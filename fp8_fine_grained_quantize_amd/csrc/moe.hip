@@ -26,18 +26,22 @@ namespace fp8blk {
 //   in its wave),
 // the last from a wave-wide match of equal keys by ballots over the key's
 // bits, so the order is the pairs' own and nothing depends on timing.  Up to
-// kSortOne pairs one workgroup does it all; above, k_moe_count first counts
-// each workgroup's segment and every workgroup of k_moe_sort then sums the
-// counts before it.  Dropped pairs form the last bucket, key E.  Latency bounds
-// it, launches, barriers and dependent loads: 128 pairs take 3.1 us, 65536
-// pairs of 256 experts 2.7 + 7.0 us, of which the sums over the workgroups' counts
-// are 2 and the scan with its four barriers 2.5.
+// kSortOne pairs one workgroup does it all; up to kSortAll every workgroup
+// counts all pairs for itself; above, k_moe_count first counts each workgroup's
+// segment and every workgroup of k_moe_sort then sums the counts before it.
+// Dropped pairs form the last bucket, key E.  Latency bounds it, launches,
+// barriers and dependent loads: 128 pairs take 3.1 us, 65536 pairs of 256 experts
+// 2.7 + 7.0 us, of which the sums over the workgroups' counts are 2 and the scan
+// with its four barriers 2.5.
 // ---------------------------------------------------------------------------
 constexpr int kMaxExperts = 960;       // 16 waves' counts, kept within 64 KB of LDS
-// Pairs that one workgroup sorts: one launch against two with 256 experts takes
-// 4.0 / 6.2 us for 1024 pairs, 5.1 / 6.8 for 2048, 7.3 / 7.3 for 4096 and 11.4 /
-// 7.7 for 8192.
-constexpr int64_t kSortOne = 4096;
+// Pairs that one workgroup sorts, and that one launch does: 256 experts take 4.1
+// us for 1024 pairs in one workgroup, 5.2 for 2048 (5.3 in two), 7.3 for 4096
+// (5.5 in four that count all pairs, 7.3 in two launches); 8192 take 5.9 in one
+// launch and 7.7 in two, 16384 7.1 and 7.8, but where all pairs have one expert,
+// whose count they add to one after the other, 8192 take 11.7 and 8.6, 16384 18.8
+// and 8.7.  With more than 512 experts LDS does not hold the counts of all pairs.
+constexpr int64_t kSortOne = 2048, kSortAll = 8192, kSortOneWide = 4096;
 constexpr int64_t kSortBlocks = 256;   // most workgroups of the two-launch sort
 constexpr int kSortWaves = 16;
 
@@ -78,7 +82,7 @@ __device__ __forceinline__ int32_t wave_scan(int32_t v) {
 
 // nb workgroups of nw waves (at most kSortWaves); each wave takes per_wave (a
 // multiple of 64) consecutive pairs.  LDS: cnt[nw][E+1], scan[2][nw] and, with
-// hist and E at most half of blockDim, 2 * blockDim partial counts.
+// several workgroups and E at most half of blockDim, 2 * blockDim partial counts.
 // blockDim > E: thread e deals with the bucket of expert e, thread E with that
 // of the dropped pairs.
 template <typename ID>
@@ -118,9 +122,23 @@ __global__ __launch_bounds__(1024) void k_moe_sort(const ID* __restrict__ ids, i
     }
   }
   for (int i = threadIdx.x; i < nw * EB; i += blockDim.x) cnt[i] = 0;
+  int32_t* part = scan + 2 * nw;  // [2][blockDim.x]
+  const bool all = hist == nullptr && gridDim.x > 1;
+  if (all) part[e] = part[blockDim.x + e] = 0;
   __syncthreads();
   for (uint32_t p = w0 + lane; p < w1; p += 64) atomicAdd(&cnt[wave * EB + sort_key(ids, ld, K, p, E)], 1);
-  int32_t* part = scan + 2 * nw;  // [2][blockDim.x]
+  if (all) {  // the other workgroups' pairs too: those before b0 apart
+    for (uint32_t p0 = threadIdx.x; p0 < P; p0 += 8 * blockDim.x) {
+      int key[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) key[i] = sort_key(ids, ld, K, min(p0 + i * blockDim.x, P - 1), E);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t p = p0 + i * blockDim.x;
+        if (p < P) atomicAdd(&part[(p < b0 ? blockDim.x : 0) + key[i]], 1);
+      }
+    }
+  }
   if (groups > 1) {
     part[e] = total;
     part[blockDim.x + e] = before;
@@ -139,6 +157,9 @@ __global__ __launch_bounds__(1024) void k_moe_sort(const ID* __restrict__ ids, i
         total += part[i * EP + e];
         before += part[blockDim.x + i * EP + e];
       }
+  } else if (all && e < E) {
+    before = part[blockDim.x + e];
+    total = part[e] + before;
   } else if (groups == 0 && e < E) {
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) total += w < nw ? c[w] : 0;
@@ -430,6 +451,10 @@ inline fp8blk_status_t pairs_ok(int64_t T, int64_t K, int64_t C) {
   return FP8BLK_OK;
 }
 
+// Most pairs of one workgroup, and of one launch.
+inline int64_t sort_one(int64_t E) { return E <= 512 ? kSortOne : kSortOneWide; }
+inline int64_t sort_launch(int64_t E) { return E <= 512 ? kSortAll : kSortOneWide; }
+
 inline int64_t sort_per_wave(int64_t P) {
   return ceil_div(ceil_div(P, kSortBlocks * kSortWaves), (int64_t)64) * 64;
 }
@@ -439,7 +464,7 @@ fp8blk_status_t launch_sort(const ID* ids, int64_t ld, uint32_t K, int64_t P, in
                             int32_t* slot_of, int32_t* hist, hipStream_t stream) {
   int nbits = 0;
   while ((E >> nbits) != 0) ++nbits;
-  if (P <= kSortOne) {
+  if (P <= sort_one(E)) {
     int64_t nw = ceil_div(P, (int64_t)64);
     if (nw > kSortWaves) nw = kSortWaves;
     if (nw < ceil_div((int64_t)E + 1, (int64_t)64)) nw = ceil_div((int64_t)E + 1, (int64_t)64);
@@ -451,10 +476,14 @@ fp8blk_status_t launch_sort(const ID* ids, int64_t ld, uint32_t K, int64_t P, in
   }
   const uint32_t per_wave = (uint32_t)sort_per_wave(P), per_block = per_wave * kSortWaves;
   const unsigned nb = (unsigned)ceil_div(P, (int64_t)per_block);
-  hipLaunchKernelGGL(k_moe_count<ID>, dim3(nb), dim3(1024), (size_t)(E + 1) * 4, stream, ids, ld, K, (uint32_t)P, E,
-                     per_block, hist);
-  const fp8blk_status_t st = launch_status();
-  if (st != FP8BLK_OK) return st;
+  if (P <= sort_launch(E)) {
+    hist = nullptr;
+  } else {
+    hipLaunchKernelGGL(k_moe_count<ID>, dim3(nb), dim3(1024), (size_t)(E + 1) * 4, stream, ids, ld, K, (uint32_t)P, E,
+                       per_block, hist);
+    const fp8blk_status_t st = launch_status();
+    if (st != FP8BLK_OK) return st;
+  }
   const size_t lds = (size_t)(kSortWaves * (E + 1) + 2 * kSortWaves + (E <= 512 ? 2 * kSortWaves * 64 : 0)) * 4;
   hipLaunchKernelGGL(k_moe_sort<ID>, dim3(nb), dim3(kSortWaves * 64), lds, stream, ids, ld, K, (uint32_t)P, E, nbits,
                      per_wave, hist, offsets, row_of, slot_of);
@@ -533,7 +562,7 @@ using namespace fp8blk;
 extern "C" int fp8blk_layer_abi_version(void) { return 1; }
 
 extern "C" size_t fp8blk_moe_sort_workspace_bytes(int64_t T, int64_t K, int64_t E) {
-  if (pairs_ok(T, K, 0) != FP8BLK_OK || E < 0 || E > kMaxExperts || T * K <= kSortOne) return 0;
+  if (pairs_ok(T, K, 0) != FP8BLK_OK || E < 0 || E > kMaxExperts || T * K <= sort_launch(E)) return 0;
   return (size_t)(ceil_div(T * K, sort_per_wave(T * K) * kSortWaves) * E) * 4;
 }
 

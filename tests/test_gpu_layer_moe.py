@@ -79,6 +79,18 @@ def test_sort_strided_ids_and_given_outputs():
     assert np.array_equal(got[1].cpu().numpy(), row_of)
 
 
+# Around the sizes where one workgroup, several that count all pairs, and two
+# launches take over; all pairs of one expert, and none kept.
+TURNS = [(2048, 1, 256, 0.0), (683, 3, 9, 0.2), (2049, 1, 512, 0.1), (1000, 8, 1, 0.0), (1024, 8, 256, 0.0),
+         (1024, 8, 500, 1.0), (2731, 3, 64, 0.1), (1025, 8, 512, 0.1), (512, 8, 600, 0.1), (513, 8, 600, 0.1)]
+
+
+@pytest.mark.parametrize("T,K,E,drop", TURNS)
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_sort_where_its_form_changes(T, K, E, drop, dtype):
+    test_sort(T, K, E, drop, dtype)
+
+
 @pytest.mark.parametrize("T,K", [(0, 8), (5, 0), (0, 0)])
 def test_sort_empty(T, K):
     off, row_of, slot_of = fb.moe_sort(torch.empty(T, K, dtype=torch.int32, device="cuda"), 17)
