@@ -465,7 +465,8 @@ __global__ __launch_bounds__(PACK || (HOLD && POST) ? 512 : 1024) void k_residua
         if (GATE_ROW) d *= gt[i];
         float& sp = HOLD ? s_post[HOLD ? c : 0][i] : slot(1, c, i);
         sp += GATE_ROW ? v[i] * gt[i] : v[i];
-        g[i] = r_post * __builtin_fmaf(-h[i], m_post, d);
+        // df = d without a norm, whatever f holds: 0 times an infinite f would be NaN
+        g[i] = post ? r_post * __builtin_fmaf(-h[i], m_post, d) : d;
       }
       if (GATE_ROW) {
 #pragma unroll
