@@ -133,6 +133,14 @@ void* stream_of(PyObject* stream, const Tensor& first, std::initializer_list<con
   return reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(stream)));
 }
 
+// Outputs and workspaces that the caller lends, before their addresses are
+// taken: one that shares its memory with a tensor until either is written (a
+// copy-on-write clone) gets its own here.  Inputs are read where they are.
+void own(std::initializer_list<const Tensor*> lent) {
+  for (const Tensor* t : lent)
+    if (t != nullptr) t->mutable_data_ptr();
+}
+
 Tensor vec(std::initializer_list<int64_t> shape, ScalarType dtype, const Tensor& like) {
   return at::empty(c10::IntArrayRef(shape), at::TensorOptions().dtype(dtype).device(like.device()));
 }
@@ -202,6 +210,7 @@ PyObject* moe_sort(PyObject* const* a) {  // ids, E, offsets, row_of, slot_of, w
   scratch(w);
   void* stream = stream_of(a[6], ids, {o, r, s, w});
   Unlocked unlocked;
+  own({o, r, s, w});
   const int64_t T = ids.size(0), K = ids.size(1);
   if ((K > 1 && ids.stride(1) != 1) || (T > 1 && ids.stride(0) < K)) ids = ids.contiguous();
   if (o != nullptr) dense(*o, at::kInt, {E + 1}, "offsets");
@@ -231,6 +240,7 @@ PyObject* moe_dispatch(PyObject* const* a) {  // x, row_of, out, stream
   const int64_t T = x.size(0), C = x.size(1), K = pairs(row_of, T), ldx = pitch(x, "x");
   void* stream = stream_of(a[3], x, {&row_of, o});
   Unlocked unlocked;
+  own({o});
   int64_t ldo;
   const Tensor out = output(o, T * K, C, at::kBFloat16, x, "out", ldo);
   ok(fp8blk_moe_dispatch(static_cast<uint16_t*>(addr(x)), T, C, ldx, K, static_cast<int32_t*>(addr(row_of)),
@@ -252,6 +262,7 @@ PyObject* moe_dispatch_fp8(PyObject* const* a) {  // q, s, row_of, slot_of, qr, 
   if (os != nullptr) dense(*os, at::kFloat, {G, T * K}, "sr");
   void* stream = stream_of(a[6], q, {&s, &row_of, &slot_of, oq, os});
   Unlocked unlocked;
+  own({oq, os});
   int64_t ldqr;
   const Tensor qr = output(oq, T * K, C, at::kByte, q, "qr", ldqr);
   const Tensor sr = os != nullptr ? *os : vec({G, T * K}, at::kFloat, q);
@@ -277,6 +288,7 @@ PyObject* moe_combine(PyObject* const* a) {  // rows, row_of, weights, out_dtype
   const ScalarType dt = o != nullptr ? o->scalar_type() : dtype_of(a[3]);
   void* stream = stream_of(a[5], rows, {&row_of, w, o});
   Unlocked unlocked;
+  own({o});
   int64_t ldo;
   const Tensor out = output(o, T, C, dt, rows, "out", ldo);
   if (out.scalar_type() == at::kFloat) flags |= FP8BLK_MOE_TOKENS_F32;
@@ -302,6 +314,7 @@ PyObject* moe_combine_backward(PyObject* const* a) {  // dy, rows, row_of, weigh
   const ScalarType dt = od != nullptr ? od->scalar_type() : a[4] == Py_None ? rows.scalar_type() : dtype_of(a[4]);
   void* stream = stream_of(a[7], dy, {&rows, &row_of, &w, od, ow});
   Unlocked unlocked;
+  own({od, ow});
   int64_t lddr;
   const Tensor drows = output(od, T * K, C, dt, dy, "drows", lddr);
   if (dt == at::kFloat) flags |= FP8BLK_MOE_DROWS_F32;
@@ -358,6 +371,7 @@ PyObject* residual_norm(PyObject* const* a) {
   if (f != nullptr) ldf = pitch(*f, at::kBFloat16, M, C, "f");
   void* stream = stream_of(a[14], x, {wn, f, wp, g, ox, on, oq, os});
   Unlocked unlocked;
+  own({ox, on, oq, os});
   Tensor xo, n, q, s, r_post, r_pre;
   if (f != nullptr) {
     xo = output(ox, M, C, x.scalar_type(), x, "x_out", ldxo);
@@ -411,6 +425,7 @@ PyObject* residual_norm_backward(PyObject* const* a) {
   scratch(w);
   void* stream = stream_of(a[13], x, {dxo, dn, r_pre, wn, f, r_post, wp, g, ox, of, w});
   Unlocked unlocked;
+  own({ox, of, w});
   Tensor dx, df, dw_pre, dw_post, dgate, ws;
   if (wn != nullptr || ox != nullptr) dx = output(ox, M, C, x.scalar_type(), x, "dx", lddx);
   if (wn != nullptr) dw_pre = vec({C}, at::kFloat, x);

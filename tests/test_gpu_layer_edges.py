@@ -1,5 +1,6 @@
 """GPU tests of what the operators around the GEMMs do with inputs and outputs
-out of the ordinary: infinities where a formula does not read them.
+out of the ordinary: infinities where a formula does not read them, lent
+outputs that share memory.
 """
 import pytest
 import torch
@@ -33,3 +34,64 @@ def test_infinities_of_an_unnormed_block_stay_out_of_its_gradient(M, C, gate, pr
     for i, j in at:
         bad[(i, j) if gate == "row" else j] = True
     assert torch.equal(~torch.isfinite(g.dgate), bad) and torch.equal(g.dgate[~bad], clean.dgate[~bad])
+
+
+def _lent(shape, dtype):
+    """A matrix to lend to a call, and a second tensor of the same values that
+    shares its memory until one of the two is written."""
+    t = torch.full(shape, 3, dtype=dtype, device="cuda")
+    return torch._lazy_clone(t), t
+
+
+def test_lent_outputs_that_share_memory_until_written():
+    T, K, E, C = 24, 2, 4, 256
+    ids = torch.randint(0, E, (T, K), generator=torch.Generator().manual_seed(1)).cuda()
+    x, f, dx = (norm._matrix(T, C, torch.bfloat16, i) for i in (1, 2, 3))
+    w, p = norm._vector(C, torch.float32, 4), torch.rand(T, K, device="cuda")
+    bf, u8, i32, f32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
+    pairs = []
+
+    def lend(shape, dtype):
+        pairs.append(_lent(shape, dtype))
+        return pairs[-1][0]
+
+    maps = fb.moe_sort(ids, E, lend((E + 1,), i32), lend((T, K), i32), lend((T * K,), i32))
+    want = [*fb.moe_sort(ids, E)]
+    row_of, slot_of = want[1:]
+    rows = fb.moe_dispatch(x, row_of)
+    got = [*maps, fb.moe_dispatch(x, row_of, out=lend((T * K, C), bf))]
+    want += [rows]
+    q, s = fb.quantize_1x128(x)
+    got += fb.moe_dispatch_fp8(q, s, row_of, slot_of, lend((T * K, C), u8), lend((C // 128, T * K), f32))
+    want += fb.moe_dispatch_fp8(q, s, row_of, slot_of)
+    got += [fb.moe_combine(rows, row_of, p, out=lend((T, C), bf))]
+    want += [fb.moe_combine(rows, row_of, p)]
+    got += fb.moe_combine_backward(dx, rows, row_of, p, drows=lend((T * K, C), bf), dweights=lend((T, K), f32))
+    want += fb.moe_combine_backward(dx, rows, row_of, p)
+    a = dict(w_pre=w, f=f, w_post=w, alpha=0.5)
+    r = fb.residual_norm(x, quantize=True, **a)
+    got += fb.residual_norm(x, quantize=True, x_out=lend((T, C), bf), n=lend((T, C), bf), q=lend((T, C), u8),
+                            s=lend((C // 128, T), f32), **a)
+    want += r
+    a.update(dx_out=dx, dn=f, rstd_pre=r.rstd_pre, rstd_post=r.rstd_post)
+    ws = lend((fb.lib().fp8blk_residual_norm_backward_workspace_bytes(T, C) // 4,), f32)
+    got += fb.residual_norm_backward(r.x, dx=lend((T, C), bf), df=lend((T, C), bf), workspace=ws, **a)
+    want += fb.residual_norm_backward(r.x, **a)
+    outs = [lend((T, C), bf), lend((T, K), f32)]
+    fb.clip_grad_norm(fb.grad_table([x, p], outs), 1.0)
+    grads = [x.clone(), p.clone()]
+    fb.clip_grad_norm(grads, 1.0)
+    for i, (g, t) in enumerate(zip(got + outs, want + grads)):
+        assert (g is None and t is None) or torch.equal(g, t), i
+    for i, (_, other) in enumerate(pairs):
+        assert (other == 3).all(), i
+
+
+def test_in_place_on_memory_shared_until_written():
+    x = norm._matrix(9, 200, torch.bfloat16, 1)
+    f = norm._matrix(9, 200, torch.bfloat16, 2)
+    want = fb.residual_norm(x, f=f, alpha=0.5).x
+    keep = x.clone()
+    mine = torch._lazy_clone(x)
+    assert fb.residual_norm(mine, f=f, alpha=0.5, x_out=mine).x is mine
+    assert torch.equal(mine, want) and torch.equal(x, keep)
