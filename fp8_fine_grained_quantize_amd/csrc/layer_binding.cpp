@@ -13,8 +13,11 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/python_headers.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <string>
+#include <utility>
+#include <vector>
 
 #include "../../include/libfp8blk_layer.h"
 
@@ -451,6 +454,91 @@ PyObject* residual_norm_backward(PyObject* const* a) {
 }
 
 // --- gradient norm and clipping ------------------------------------------------
+
+// Rows of `width` bytes, `pitch` (at least the width) apart.
+struct Span {
+  int64_t base, width, pitch, rows;
+  int64_t end() const { return base + (rows - 1) * pitch + width; }
+};
+Span span(const void* p, const fp8blk_grad_t& g, int64_t ld, bool f32) {
+  const int64_t size = f32 ? 4 : 2;
+  return {static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)), g.cols * size, ld * size, g.rows};
+}
+Span grad_span(const fp8blk_grad_t& g) { return span(g.grad, g, g.ld, g.flags & FP8BLK_GRAD_F32); }
+Span out_span(const fp8blk_grad_t& g) { return span(g.out, g, g.ldo, g.flags & FP8BLK_GRAD_OUT_F32); }
+// Clipped in place: every element is read and written by one lane.
+bool in_place(const fp8blk_grad_t& g) {
+  return g.grad == g.out && (g.rows == 1 || g.ld == g.ldo) &&
+         !(g.flags & FP8BLK_GRAD_F32) == !(g.flags & FP8BLK_GRAD_OUT_F32);
+}
+
+// Whether two spans have a byte in common, exactly: rows may lie between rows.
+bool meet(Span a, Span b) {
+  if (a.rows > b.rows) std::swap(a, b);
+  if (a.pitch == b.pitch && a.rows > 1) {  // only the distance of the rows counts: one row against all of them
+    b.base -= (a.rows - 1) * a.pitch;
+    b.rows += a.rows - 1;
+    a.rows = 1;
+  }
+  for (int64_t i = 0; i < a.rows; ++i) {
+    const int64_t lo = a.base + i * a.pitch, past = lo - b.width - b.base;  // b's rows up to `past` end before lo
+    const int64_t j = past < 0 ? 0 : past / b.pitch + 1;
+    if (j < b.rows && b.base + j * b.pitch < lo + a.width) return true;
+  }
+  return false;
+}
+
+// Two gradients of a list that clipping must not take together: an output of
+// one shares memory with the other's gradient or output, or with its own
+// gradient other than in place, so that values would be scaled twice or read
+// while they are written.  Gradients that are only read may share theirs.
+// first[t] .. first[t + 1]: the entries of tensor t.
+PyObject* grad_shared(PyObject* const* a) {  // address of the entries, of `first`, tensors
+  const auto* list = reinterpret_cast<const fp8blk_grad_t*>(static_cast<uintptr_t>(integer(a[0])));
+  const auto* first = reinterpret_cast<const int64_t*>(static_cast<uintptr_t>(integer(a[1])));
+  struct Item {  // the extent of a tensor's gradient or output
+    int64_t lo, hi, t;
+    bool out;
+  };
+  std::vector<Item> items, open;
+  const int64_t tensors = integer(a[2]);
+  for (int64_t t = 0; t < tensors; ++t) {
+    if (first[t] == first[t + 1]) continue;
+    Item g{INT64_MAX, INT64_MIN, t, false}, o{INT64_MAX, INT64_MIN, t, true};
+    bool all_in_place = true;
+    for (int64_t e = first[t]; e < first[t + 1]; ++e) {
+      const Span gs = grad_span(list[e]), os = out_span(list[e]);
+      g = {std::min(g.lo, gs.base), std::max(g.hi, gs.end()), t, false};
+      o = {std::min(o.lo, os.base), std::max(o.hi, os.end()), t, true};
+      all_in_place = all_in_place && in_place(list[e]);
+    }
+    items.push_back(o);
+    if (!all_in_place) items.push_back(g);
+  }
+  auto shared = [&](const Item& p, const Item& q) {
+    for (int64_t e = first[p.t]; e < first[p.t + 1]; ++e)
+      for (int64_t f = first[q.t]; f < first[q.t + 1]; ++f) {
+        if (e == f && in_place(list[e])) continue;
+        if (meet(p.out ? out_span(list[e]) : grad_span(list[e]), q.out ? out_span(list[f]) : grad_span(list[f])))
+          return true;
+      }
+    return false;
+  };
+  std::sort(items.begin(), items.end(), [](const Item& p, const Item& q) { return p.lo < q.lo; });
+  for (const Item& q : items) {  // against the extents that reach past its start
+    size_t kept = 0;
+    for (const Item& p : open) {
+      if (p.hi <= q.lo) continue;
+      if ((p.out || q.out) && shared(p, q))
+        return Py_BuildValue("LL", static_cast<long long>(std::min(p.t, q.t)), static_cast<long long>(std::max(p.t, q.t)));
+      open[kept++] = p;
+    }
+    open.resize(kept);
+    open.push_back(q);
+  }
+  Py_RETURN_NONE;
+}
+
 // The table tensor (undefined address for n = 0), n, chunks, ...
 
 PyObject* grad_norm(PyObject* const* a) {  // table, n, chunks, stream
@@ -527,6 +615,7 @@ PyMethodDef methods[] = {FP8BLK_METHOD(moe_sort, 7),
                          FP8BLK_METHOD(moe_combine_backward, 8),
                          FP8BLK_METHOD(residual_norm, 15),
                          FP8BLK_METHOD(residual_norm_backward, 14),
+                         FP8BLK_METHOD(grad_shared, 3),
                          FP8BLK_METHOD(grad_norm, 4),
                          FP8BLK_METHOD(grad_clip, 7),
                          FP8BLK_METHOD(clip_grad_norm, 6),

@@ -235,12 +235,23 @@ def _grad_entries(t: torch.Tensor, o: torch.Tensor, flags: int, out: list) -> No
         _grad_entries(t[i], o[i], flags, out)
 
 
+def _shared(array, first):
+    """The first two tensors of a list of entries that clipping must not take
+    together (see layer_binding.cpp), None without such; first: where each
+    tensor's entries start, and their number."""
+    starts = (_i64 * len(first))(*first)
+    return _ext().grad_shared(ctypes.addressof(array), ctypes.addressof(starts), len(first) - 1)
+
+
 class GradTable:
     """A list of gradients (and, where clipped values go elsewhere, their
     outputs) laid out on the device for grad_norm and clip_grad_norm.  It names
     the tensors' memory and holds the tensors: a training loop that keeps its
     gradient buffers builds it once (and before a graph is captured), one whose
-    gradients are new tensors every step passes the list instead."""
+    gradients are new tensors every step passes the list instead.  Gradients
+    may share memory (a tied weight listed twice) for grad_norm, which counts
+    them each time; clipping refuses outputs that share memory with another
+    tensor of the list, or with their own gradient other than in place."""
 
     def __init__(self, tensors: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
         self.tensors = list(tensors)
@@ -254,7 +265,7 @@ class GradTable:
             for t in (*self.tensors, *(self.outs or ())):
                 if t.device != self.device or _stream(t) is None:
                     raise ValueError(f"expected tensors on the current GPU, got {t.device}")
-        entries = []
+        entries, first = [], [0]
         for i, t in enumerate(self.tensors):
             o = t if self.outs is None else self.outs[i]
             if o.shape != t.shape:
@@ -263,12 +274,14 @@ class GradTable:
                 raise ValueError(f"elements of gradient {i} or of its output share memory")
             flags = (_GRAD_F32 if _is_f32(t, f"gradient {i}") else 0) | (_GRAD_OUT_F32 if _is_f32(o, f"output {i}") else 0)
             _grad_entries(t, o, flags, entries)
+            first.append(len(entries))
         L = _fb.lib()
         self.n = len(entries)
         nbytes = L.fp8blk_grad_table_bytes(self.n)
         host = torch.empty(nbytes // 8, dtype=torch.int64)
         chunks = _i64(0)
         array = (_Grad * max(self.n, 1))(*entries)
+        self.shared = _shared(array, first)
         _fb._check(L.fp8blk_grad_table_build(ctypes.cast(array, _vp), self.n, host.data_ptr(), nbytes,
                                              ctypes.cast(ctypes.pointer(chunks), _vp)), "grad_table")
         self.chunks = chunks.value
@@ -291,6 +304,14 @@ def _table(grads):
     return t, stream
 
 
+def _clippable(grads):
+    """_table of gradients that can be clipped together."""
+    t, stream = _table(grads)
+    if t.shared is not None:
+        raise ValueError("gradients {} and {}, or their outputs, share memory that clipping would write".format(*t.shared))
+    return t, stream
+
+
 def grad_norm(grads) -> torch.Tensor:
     """Global 2-norm over all gradients (a GradTable or a list of tensors): a
     float32 scalar on the device."""
@@ -302,11 +323,11 @@ def grad_clip(grads, norm: torch.Tensor, max_norm: float, eps: float = 1e-6) -> 
     """Scale every gradient by min(1, max_norm / (norm + eps)), norm a float32
     scalar on the device (e.g. reduced over ranks): in place, or into the
     table's outputs."""
-    t, stream = _table(grads)
+    t, stream = _clippable(grads)
     _ext().grad_clip(t.device_table, t.n, t.chunks, norm, max_norm, eps, stream)
 
 
 def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6) -> torch.Tensor:
     """grad_norm and grad_clip by it; returns the norm before clipping."""
-    t, stream = _table(grads)
+    t, stream = _clippable(grads)
     return _ext().clip_grad_norm(t.device_table, t.n, t.chunks, max_norm, eps, stream)

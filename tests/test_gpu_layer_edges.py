@@ -1,12 +1,13 @@
 """GPU tests of what the operators around the GEMMs do with inputs and outputs
 out of the ordinary: infinities where a formula does not read them, lent
-outputs that share memory.
+outputs and lists of gradients that share memory.
 """
 import pytest
 import torch
 
 import fp8_fine_grained_quantize_amd as fb
 from tests import test_gpu_layer_norm as norm
+from tests.layer_ref import U
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +96,19 @@ def test_in_place_on_memory_shared_until_written():
     mine = torch._lazy_clone(x)
     assert fb.residual_norm(mine, f=f, alpha=0.5, x_out=mine).x is mine
     assert torch.equal(mine, want) and torch.equal(x, keep)
+
+
+def test_clipping_refuses_gradients_that_share_memory():
+    """Which lists do is tested in test_layer_grad_lists.py."""
+    g, o = torch.randn(5000, device="cuda"), torch.zeros(5000, device="cuda")
+    before, n = g.clone(), float(g.double().square().sum())
+    for table in ([g, g], fb.grad_table([g, o, g[100:]]), fb.grad_table([g, g], [o, o]), fb.grad_table([g[1:]], [g[:-1]])):
+        with pytest.raises(ValueError, match="share memory"):
+            fb.clip_grad_norm(table, 1.0)
+        with pytest.raises(ValueError, match="share memory"):
+            fb.grad_clip(table, torch.ones((), device="cuda"), 1.0)
+    assert torch.equal(g, before) and not o.any()
+    assert abs(float(fb.grad_norm([g, g])) - (2 * n) ** 0.5) <= 2 * U * (2 * n) ** 0.5  # read only: counted twice
+    p = torch.zeros(5000, dtype=torch.bfloat16, device="cuda")
+    fb.clip_grad_norm(fb.grad_table([g, g], [o, p]), 1e9)
+    assert torch.equal(o, g) and torch.equal(p, g.to(torch.bfloat16))
