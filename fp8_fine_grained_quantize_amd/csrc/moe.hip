@@ -442,12 +442,15 @@ inline RowSplit split_row(int64_t chunks, int64_t most = 256) {
 }
 
 constexpr int64_t kMaxPairs = 0x7FFFFFFF - (1 << 20);
+// Channels: more than any memory holds, and few enough that neither a row's
+// parts (RowSplit) nor the product of sizes overflow.
+constexpr int64_t kMaxChannels = (int64_t)1 << 40;
 
 // Sizes of a token matrix with K rows per token: FP8BLK_OK where they can be
 // worked on.
 inline fp8blk_status_t pairs_ok(int64_t T, int64_t K, int64_t C) {
   if (T < 0 || K < 0 || C < 0) return FP8BLK_ERR_INVALID_ARG;
-  if (K > 0 && T > kMaxPairs / K) return FP8BLK_ERR_UNSUPPORTED;
+  if ((K > 0 && T > kMaxPairs / K) || (T > 0 && C > kMaxChannels)) return FP8BLK_ERR_UNSUPPORTED;
   return FP8BLK_OK;
 }
 

@@ -35,8 +35,8 @@ int fp8blk_layer_abi_version(void);
 
 /* ------------------------------------------------------------------------
  * Tokens by expert.  T tokens, K expert choices ("pairs") each, E experts;
- * pair p = t*K + k.  T*K at most 2^31 - 1 - 2^20, E at most 960 and
- * T * C / 8 below 2^32, the lanes of a launch (FP8BLK_ERR_UNSUPPORTED
+ * pair p = t*K + k.  T*K at most 2^31 - 1 - 2^20, C at most 2^40, E at most
+ * 960 and T * C / 8 below 2^32, the lanes of a launch (FP8BLK_ERR_UNSUPPORTED
  * otherwise).
  * ------------------------------------------------------------------------ */
 
