@@ -541,12 +541,11 @@ struct CombineGradArgs {
   void* drows;
   int64_t lddr;
   float* dw;
+  uint32_t lanes;  // of a token's workgroup
 };
 template <typename TY, typename TR, typename TD, bool EXACT, bool NT>
 void launch_combine_backward(const CombineGradArgs& a, hipStream_t stream) {
-  const int64_t V = sizeof(TY) == 2 && sizeof(TR) == 2 && sizeof(TD) == 2 ? 8 : 4;
-  hipLaunchKernelGGL((k_moe_combine_backward<TY, TR, TD, EXACT, NT>), dim3((unsigned)a.T),
-                     dim3(split_row(ceil_div(a.C, V), combine_grad_lanes(a.K)).lanes), 0, stream,
+  hipLaunchKernelGGL((k_moe_combine_backward<TY, TR, TD, EXACT, NT>), dim3((unsigned)a.T), dim3(a.lanes), 0, stream,
                      reinterpret_cast<const TY*>(a.dy), a.lddy, reinterpret_cast<const TR*>(a.rows), a.ldr, a.T, a.K,
                      a.C, a.row_of, a.w, reinterpret_cast<TD*>(a.drows), a.lddr, a.dw);
 }
@@ -662,10 +661,12 @@ extern "C" fp8blk_status_t fp8blk_moe_combine_backward(const void* dy, int64_t l
       !matrix_ok(drows, T * K, C, lddr, df ? 4 : 2) || !vec_ok(row_of, T * K) || !vec_ok(weights, T * K) ||
       !vec_ok(dweights, T * K))
     return FP8BLK_ERR_INVALID_ARG;
-  if (!grid_ok(T, 512)) return FP8BLK_ERR_UNSUPPORTED;
+  // channels of a lane as in k_moe_combine_backward: 16 bytes of the widest type
+  const uint32_t lanes = split_row(ceil_div(C, (int64_t)(yf || rf || df ? 4 : 8)), combine_grad_lanes((uint32_t)K)).lanes;
+  if (!grid_ok(T, lanes)) return FP8BLK_ERR_UNSUPPORTED;
   using U = uint16_t;
   using F = float;
-  const CombineGradArgs a{dy, lddy, rows, ldr, T, (uint32_t)K, C, row_of, weights, drows, lddr, dweights};
+  const CombineGradArgs a{dy, lddy, rows, ldr, T, (uint32_t)K, C, row_of, weights, drows, lddr, dweights, lanes};
   auto* go = yf ? (rf ? (df ? pick_combine_backward<F, F, F> : pick_combine_backward<F, F, U>)
                       : (df ? pick_combine_backward<F, U, F> : pick_combine_backward<F, U, U>))
                 : (rf ? (df ? pick_combine_backward<U, F, F> : pick_combine_backward<U, F, U>)

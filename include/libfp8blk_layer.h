@@ -36,8 +36,11 @@ int fp8blk_layer_abi_version(void);
 /* ------------------------------------------------------------------------
  * Tokens by expert.  T tokens, K expert choices ("pairs") each, E experts;
  * pair p = t*K + k.  T*K at most 2^31 - 1 - 2^20, C at most 2^40, E at most
- * 960 and T * C / 8 below 2^32, the lanes of a launch (FP8BLK_ERR_UNSUPPORTED
- * otherwise).
+ * 960, and a launch has fewer than 2^32 lanes (FP8BLK_ERR_UNSUPPORTED
+ * otherwise): a token's row takes one for 8 channels (4 where either matrix
+ * is FP32; 16 codes) in workgroups of 64 to 256, for codes always 256, of
+ * which the scales take more for every 256 rows and 8 groups; in the gradient
+ * of the combine every token has one workgroup, of 64 to 512 lanes whatever C.
  * ------------------------------------------------------------------------ */
 
 /* Flag: the expert ids are int64 (as a top-k over router scores returns

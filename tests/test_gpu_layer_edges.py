@@ -112,3 +112,18 @@ def test_clipping_refuses_gradients_that_share_memory():
     p = torch.zeros(5000, dtype=torch.bfloat16, device="cuda")
     fb.clip_grad_norm(fb.grad_table([g, g], [o, p]), 1e9)
     assert torch.equal(o, g) and torch.equal(p, g.to(torch.bfloat16))
+
+
+def test_gradient_of_the_combine_of_many_narrow_tokens():
+    """As many tokens as a launch of 64 lanes each takes, not one of 512."""
+    T, C = 2 ** 23 + 3, 8
+    print(f"[layer] combine grad T={T} C={C}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dy = torch.randn(T, C, generator=g, device="cuda").to(torch.bfloat16)
+    rows = torch.randn(T, C, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.rand(T, 1, generator=g, device="cuda")
+    row_of = torch.arange(T - 1, -1, -1, dtype=torch.int32, device="cuda").view(T, 1)
+    drows, dw = fb.moe_combine_backward(dy, rows, row_of, w)
+    assert torch.equal(drows, (w * dy.float()).to(torch.bfloat16).flip(0))
+    terms = dy.double() * rows.double().flip(0)
+    assert bool(((dw.double() - terms.sum(1, keepdim=True)).abs() <= 2 * C * U * terms.abs().sum(1, keepdim=True)).all())

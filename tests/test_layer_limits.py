@@ -31,3 +31,11 @@ def _combine_backward(T, K, C, flags=0):
 @pytest.mark.parametrize("C", [2 ** 41, 2 ** 43, 2 ** 44, 2 ** 44 + 2 ** 20, 2 ** 45, 2 ** 58, 2 ** 62])
 def test_rows_that_no_memory_holds(call, C):
     assert call(1, 1, C) == UNSUPPORTED
+
+
+def test_tokens_past_the_lanes_of_a_launch():
+    """64 lanes at least for a token's row, 256 for codes."""
+    assert _dispatch(2 ** 26, 1, 64) == _combine(2 ** 26, 1, 64) == _combine_backward(2 ** 26, 1, 64) == UNSUPPORTED
+    assert _dispatch_fp8(2 ** 24, 1, 64) == UNSUPPORTED
+    assert _combine(2 ** 20, 1, 2 ** 14, 1) == UNSUPPORTED   # FP32 rows: 4 channels a lane
+    assert _combine_backward(2 ** 23, 4, 8192) == UNSUPPORTED and _combine_backward(2 ** 24, 3, 8192) == UNSUPPORTED
