@@ -73,7 +73,10 @@ def _ext():
 def _stream(first: torch.Tensor):
     """Handle of the current stream; None unless the first tensor is on the
     current GPU (where the library works), which is then refused."""
-    i = first.get_device()
+    try:
+        i = first.get_device()
+    except AttributeError:  # no tensor: refused by its name
+        return None
     return torch._C._cuda_getCurrentRawStream(i) if i >= 0 and i == torch._C._cuda_getDevice() else None
 
 
@@ -256,6 +259,10 @@ class GradTable:
     def __init__(self, tensors: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
         self.tensors = list(tensors)
         self.outs = None if outs is None else list(outs)
+        for what, ts in (("gradient", self.tensors), ("output", self.outs or ())):
+            for i, t in enumerate(ts):
+                if not isinstance(t, torch.Tensor):
+                    raise TypeError(f"{what} {i} must be a tensor")
         if self.outs is not None and len(self.outs) != len(self.tensors):
             raise ValueError(f"{len(self.tensors)} gradients, {len(self.outs)} outputs")
         if not self.tensors:
