@@ -216,10 +216,11 @@ PyObject* moe_sort(PyObject* const* a) {  // ids, E, offsets, row_of, slot_of, w
   own({o, r, s, w});
   const int64_t T = ids.size(0), K = ids.size(1);
   if ((K > 1 && ids.stride(1) != 1) || (T > 1 && ids.stride(0) < K)) ids = ids.contiguous();
-  if (o != nullptr) dense(*o, at::kInt, {E + 1}, "offsets");
+  const int64_t bounds = std::clamp<int64_t>(E, 0, 1 << 16) + 1;  // the library refuses far fewer: no memory for those
+  if (o != nullptr) dense(*o, at::kInt, {bounds}, "offsets");
   if (r != nullptr) dense(*r, at::kInt, {T, K}, "row_of");
   if (s != nullptr) dense(*s, at::kInt, {T * K}, "slot_of");
-  const Tensor off = o != nullptr ? *o : vec({E > 0 ? E + 1 : 1}, at::kInt, ids);
+  const Tensor off = o != nullptr ? *o : vec({bounds}, at::kInt, ids);
   const Tensor row = r != nullptr ? *r : vec({T, K}, at::kInt, ids);
   const Tensor slot = s != nullptr ? *s : vec({T * K}, at::kInt, ids);
   const size_t bytes = fp8blk_moe_sort_workspace_bytes(T, K, E);

@@ -127,3 +127,13 @@ def test_gradient_of_the_combine_of_many_narrow_tokens():
     assert torch.equal(drows, (w * dy.float()).to(torch.bfloat16).flip(0))
     terms = dy.double() * rows.double().flip(0)
     assert bool(((dw.double() - terms.sum(1, keepdim=True)).abs() <= 2 * C * U * terms.abs().sum(1, keepdim=True)).all())
+
+
+@pytest.mark.parametrize("E", [-1, 961, 2 ** 31, 2 ** 40, 2 ** 63 - 1])
+def test_a_number_of_experts_out_of_range_takes_no_memory(E):
+    ids = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    torch.cuda.reset_peak_memory_stats()
+    held = torch.cuda.memory_allocated()
+    with pytest.raises(fb.Fp8BlkError, match="moe_sort"):
+        fb.moe_sort(ids, E)
+    assert torch.cuda.max_memory_allocated() - held < 1 << 20
