@@ -204,6 +204,8 @@ def _as_rows(shape, stride):
 
 def _overlaps(t: torch.Tensor) -> bool:
     """Whether two elements may share memory (expanded tensors, sliding windows)."""
+    if t.numel() == 0:
+        return False
     reach = 0
     for st, n in sorted((st, n) for n, st in zip(t.shape, t.stride()) if n > 1):
         if st <= reach:

@@ -47,6 +47,12 @@ def test_lists_that_share_memory():
     assert _shared([b[:20].view(torch.bfloat16)[:20]], [b[10:30]]) is None
 
 
+@pytest.mark.parametrize("shape,expanded", [((1, 0), (3, 0)), ((0, 1), (0, 4)), ((1, 0, 5), (4, 0, 5))])
+def test_expanded_tensors_without_elements(shape, expanded):
+    t = torch.zeros(shape).expand(expanded)
+    assert not layer._overlaps(t) and _shared([t, t]) is None
+
+
 def _elements(t):
     """The addresses of t's elements, in order."""
     at = torch.zeros(t.shape, dtype=torch.int64)
