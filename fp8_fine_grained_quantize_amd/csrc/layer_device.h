@@ -204,12 +204,16 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// Waits for this wave's loads.  Before a row's successor is loaded in a loop:
-// where the loads that follow may be skipped, the compiler can wait for a value
-// only by waiting for every load, the successor's too, so the present row's
-// values have to be there first (gradient of the norm, 32768 x 4096 with a gate
-// per token: 346 us without, 261 with).
-__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
+// Waits for this wave's loads, and its stores: one counter counts both.  Before
+// a row's successor is loaded in a loop: where the loads that follow may be
+// skipped, the compiler can wait for a value only by waiting for every load,
+// the successor's too, so the present row's values have to be there first.
+// Gradient of the norm, every tensor separate: rows that end inside a chunk
+// 65536 x 2051 325 us, 399 without, 65536 x 1025 192 / 239; rows of whole chunks
+// gain nothing by it (32768 x 4096 with a gate per token 365 / 365) and lose
+// what the stores take to leave (8192 x 7168 126 / 125, FP32 32768 x 7168 776 /
+// 760), so they do not wait.
+__device__ __forceinline__ void wait_vmem() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
 
 // A barrier that orders LDS accesses only: global loads and stores in flight
 // stay in flight across it.

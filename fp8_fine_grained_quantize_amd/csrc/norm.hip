@@ -370,7 +370,7 @@ __global__ __launch_bounds__(PACK || (HOLD && POST) ? 512 : 1024) void k_residua
       if (pre) r_pre = a.rstd_pre[row];
       if (post) r_post = a.rstd_post[row];
     } else {
-      wait_loads();
+      if (OVER) wait_vmem();
       if (row + rows.step < a.M) {
         if (pre) next_pre = a.rstd_pre[row + rows.step];
         if (post) next_post = a.rstd_post[row + rows.step];
