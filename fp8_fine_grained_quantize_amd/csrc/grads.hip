@@ -14,7 +14,10 @@
 // workgroup of the second pass for itself, which saves a launch between.
 // 3.76 GB of FP32 gradients: 535 us for the squares (7.0 TB/s read) and 1467 for
 // the scaling (5.1 TB/s read and written); 200 small tensors of 1.2 M elements
-// in all: 4.9 and 6.7 us, launch, search of the table and partial sums.
+// in all: 4.9 and 6.7 us, launch, search of the table and partial sums.  Rows that
+// do not follow each other are taken element by element, one load in flight and a
+// 64-bit division each, which bound them: 131072 rows of 7165 FP32 values at a
+// pitch of 7168, squares 2.1 ms where dense values take 0.54.
 #include "../../include/libfp8blk_layer.h"
 #include "host_common.h"
 #include "layer_device.h"

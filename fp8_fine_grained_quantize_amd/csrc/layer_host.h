@@ -15,7 +15,7 @@ namespace fp8blk {
 //   dispatch of BF16 rows, then combine: 4096 tokens (504 MB) 210 / 240,
 //   2048 (252 MB) 99 / 89, 256 (32 MB) 14 / 13.
 //   residual_norm of 8192 x 7168 to BF16 and E4M3 alone 103 / 109, its
-//   gradient 126 / 133; clipping of 3.8 GB 2021 / 2122.
+//   gradient 125 / 137; clipping of 3.8 GB 2021 / 2122.
 constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 
 // A launch counts its lanes in 32 bits.

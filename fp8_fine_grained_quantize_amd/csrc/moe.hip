@@ -40,7 +40,9 @@ constexpr int kMaxExperts = 960;       // 16 waves' counts, kept within 64 KB of
 // (5.5 in four that count all pairs, 7.3 in two launches); 8192 take 5.9 in one
 // launch and 7.7 in two, 16384 7.1 and 7.8, but where all pairs have one expert,
 // whose count they add to one after the other, 8192 take 11.7 and 8.6, 16384 18.8
-// and 8.7.  With more than 512 experts LDS does not hold the counts of all pairs.
+// and 8.7.  With more than 512 experts one workgroup sorts twice as many: the
+// counts of all pairs beside those of 16 waves are kept within 64 KB of LDS, which
+// 960 experts would pass (70 KB).
 constexpr int64_t kSortOne = 2048, kSortAll = 8192, kSortOneWide = 4096;
 constexpr int64_t kSortBlocks = 256;   // most workgroups of the two-launch sort
 constexpr int kSortWaves = 16;
@@ -217,10 +219,13 @@ __global__ __launch_bounds__(1024) void k_moe_sort(const ID* __restrict__ ids, i
 // of their own at the end of the grid: 256 consecutive rows x kScaleGroups
 // groups, written coalesced (the scales of all tokens stay in L2).  HBM writes
 // bound it: 8192 tokens of 7168 codes to 65536 rows take 99 us, 545 MB at 5.5
-// TB/s (109 through the caches); counters show each code and scale written once
-// and read at most once.  A row's last 16 bytes are moved whole, some of them by
-// two lanes (32768 tokens of 8 rows of 259 codes: 23 us, 41 byte by byte); UNIT,
-// the bytes of an element, is the step of rows shorter than that.
+// TB/s (109 through the caches); counters show each code and scale written once,
+// the codes read once and the scales once by each of the eight L2s (76 MB read for
+// 61).  A row's last 16 bytes are moved whole, some of them by two lanes (32768
+// tokens of 8 rows of 259 codes: 23 us, 41 byte by byte); UNIT, the bytes of an
+// element, is the step of rows shorter than that.  Narrow rows leave most lanes
+// of their token's workgroup idle, with codes 252 of 256 at 64 channels: 32768
+// tokens of 8 rows of 64 take 21 us, of which moving the bytes would be 4.
 // ---------------------------------------------------------------------------
 constexpr int kScaleGroups = 8;
 
@@ -356,7 +361,8 @@ __global__ __launch_bounds__(256) void k_moe_combine(const TR* __restrict__ rows
 // (FP32, lane by lane over the channels, then across lanes) and writes the
 // eight scaled copies of dy: rows and their gradients pass once.  HBM bounds
 // it, reads and writes of scattered rows in equal parts: 8192 tokens of 8 BF16
-// rows of 7168 take 395 us, 2.0 GB at 5.1 TB/s.
+// rows of 7168 take 395 us, 2.0 GB at 5.1 TB/s.  The eight rows' addresses do not
+// fit the scalar registers: 47 to 98 of them are kept in lanes of vector ones.
 // ---------------------------------------------------------------------------
 template <typename TY, typename TR, typename TD, bool EXACT, bool NT>
 __global__ __launch_bounds__(512) void k_moe_combine_backward(const TY* __restrict__ dy, int64_t lddy,

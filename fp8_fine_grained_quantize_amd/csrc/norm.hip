@@ -140,7 +140,11 @@ __device__ __forceinline__ void load_row(NormRow<TX, NCH, GATE_ROW, EXACT>& r, c
 // row cover the other's way from HBM, which bounds it.  8192 x 7168 (BF16, n and
 // E4M3 out) takes 96 us, 530 MB at 5.5 TB/s; without the next row in flight and
 // with the parameters read again for every row it took 162.  A decode step of 16
-// rows takes 5.5 us: launch, one load, two reductions.
+// rows takes 5.5 us: launch, four loads one after the other (w_post, gate and
+// w_pre, each behind a branch on its type, then the row) and two reductions.
+// Above 8192 channels two chunks a lane and 1024 lanes leave 128 registers: FP32 x
+// with a gate per token or ragged rows, and BF16 x with both, keep 16 to 88 bytes
+// a lane in scratch.
 template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT, bool PACK>
 __global__ __launch_bounds__(PACK ? kPackLanes : 1024) void k_residual_norm(const NormFwd a) {
   __shared__ float red[2][2][16];
@@ -247,11 +251,12 @@ __global__ __launch_bounds__(PACK ? kPackLanes : 1024) void k_residual_norm(cons
 // A workgroup takes the rows blockIdx.x, blockIdx.x + gridDim.x, ... with the
 // next row's loads in flight, keeps the accumulators in registers and writes
 // them as one row of partials, which k_norm_sums adds up in order.  HBM bounds
-// it: 8192 x 7168 takes 122 us, 705 MB at 5.8 TB/s, and the sums 5; with two
+// it: 8192 x 7168 takes 120 us, 705 MB at 5.9 TB/s, and the sums 5; with two
 // reductions a row, three accumulators per channel and no row ahead it was 222
 // + 16.  The norm's gradient alone (POST: there is an f) keeps half the
-// registers, so twice the lanes are at work: 131072 x 1024 takes 142 us, 182
-// by the other kernel; 1048576 x 128 135, 204.
+// registers, so twice the lanes are at work: 32768 x 2880 takes 127 us, 149 by
+// the other kernel with no f, 65536 x 1025 113 / 236, 16384 x 7168 151 / 152; but
+// 131072 x 1024 194 / 185, 32768 x 4096 185 / 177 and FP32 16384 x 7168 297 / 276.
 // ---------------------------------------------------------------------------
 struct NormBwd {
   const void* x;
@@ -319,10 +324,12 @@ __device__ __forceinline__ void load_factors(const NormBwd& a, int64_t col, floa
 }
 
 // HOLD: the factors and the next row are held in registers, up to 256 of 512
-// lanes.  Where they would not fit beside the accumulators (C above 8192; FP32
-// x with a gate per token above 4096) 1024 lanes read factors and rows chunk
-// by chunk, and once more (from L2) after the reduction, with the accumulators
-// in LDS.
+// lanes (ragged rows of 4097 to 8192 channels with FP32 x or a gate per token keep
+// 16 and 32 bytes a lane in scratch).  Where they would not fit beside the
+// accumulators (C above 8192; FP32 x with a gate per token above 4096) 1024 lanes
+// read factors and rows chunk by chunk, and once more (from L2) after the
+// reduction, with the accumulators in LDS and no row ahead: 4096 x 16384 takes 231
+// us, 805 MB at 3.5 TB/s.
 template <typename TX, int NCH, bool GATE_ROW, bool EXACT, bool NT, bool HOLD, bool PACK, bool POST>
 __global__ __launch_bounds__(PACK || (HOLD && POST) ? 512 : 1024) void k_residual_norm_backward(const NormBwd a) {
   constexpr int NH = HOLD ? NCH : 1, UNROLL = NH;  // without HOLD one chunk after the other
@@ -330,7 +337,7 @@ __global__ __launch_bounds__(PACK || (HOLD && POST) ? 512 : 1024) void k_residua
   // channels, of which the lane before holds some too.  Both compute and store
   // the same for them; sums over the row leave out the last lane's share.  No
   // values are moved and no pieces stored while the row's other waves wait
-  // (65536 x 2051: 318 us, 580 with the end's values moved to their places).
+  // (65536 x 2051: 327 us, 608 with the end's values moved to their places).
   constexpr int SUMS = POST ? 3 : 1;
   constexpr bool OVER = HOLD && !EXACT && !PACK, FULL = EXACT || OVER;
   __shared__ float red[2][3 * 16];
@@ -511,7 +518,7 @@ __global__ __launch_bounds__(PACK || (HOLD && POST) ? 512 : 1024) void k_residua
 // Sums over the nb rows of partials in a fixed order: kSumCols columns per
 // workgroup, 1024 / kSumCols row classes, then their sums in order; blockIdx.y
 // picks the vector.  Of the second, both dw_post and dgate are made.  Dependent
-// loads bound it (8192 x 1024, gradient and sums: 18.8 us, 22.7 with 64 columns).
+// loads bound it (8192 x 1024, gradient and sums: 30 us, 32 with 64 columns).
 constexpr int kSumCols = 32;
 struct NormSums {
   const float* part[2];
@@ -563,7 +570,7 @@ __global__ __launch_bounds__(1024) void k_norm_sums(const NormSums a, int first,
 // of 64).  Forward: one chunk up to 1024 lanes, then two (8192 x 7168 took 97 us
 // with 896 lanes of one chunk, 99 with 448 of two).  Gradient with an f: at most
 // 512 lanes where they hold a row ahead, so that each may have 256 registers
-// (123 us with 448 lanes of two chunks, 128 with 896 of one); without one, as
+// (125 us with 448 lanes of two chunks, 127 with 896 of one); without one, as
 // the forward.
 inline int forward_chunks(int64_t C) { return C > 8192 ? 2 : 1; }
 inline bool backward_holds(int64_t C, uint32_t flags) {
@@ -577,8 +584,11 @@ inline int norm_lanes(int64_t C, int chunks) {
 
 // Workgroups of either kernel: `per_cu` lanes on a compute unit, as many as the
 // registers allow at a time (half or twice as many were 1-2 % slower in the
-// forward, twice as many 7 % in the gradient, 8192 x 7168; 768 lanes instead of
-// 512 in the gradient, 65536 x 2048: 216 us, 204).
+// forward to E4M3, half 2 % faster without the codes, twice as many 8 % slower in
+// the gradient, 8192 x 7168; 768 lanes instead of 512 in the gradient, 65536 x
+// 2048: 298 us, 272).  The gradient of the norm alone has 1024: with 512, 32768 x
+// 2880 takes 140 us, not 127, and 65536 x 1025 140, not 113, but 131072 x 1024
+// 173, not 193.
 inline int64_t norm_blocks(int64_t M, int lanes, int64_t per_cu) {
   int64_t n = per_cu / lanes;
   n = (n < 1 ? 1 : n) * device_cus();
@@ -586,8 +596,8 @@ inline int64_t norm_blocks(int64_t M, int lanes, int64_t per_cu) {
 }
 // Rows of at most kPackMaxC channels: lanes of a row, and of a workgroup, the
 // fewest that reach every compute unit once (gradient of 512 x 128: 7.6 us in
-// workgroups of 64 lanes, 9.5 in 512; 1048576 x 128, norm only: 106 in 64, 100
-// in 512).
+// workgroups of 64 lanes, 9.5 in 512; 1048576 x 128, norm only: 105 in 64, 99 in
+// 512, gradient 204 / 189).
 inline int norm_group(int64_t C) { return C <= 128 ? 16 : C <= 256 ? 32 : 64; }
 inline int packed_lanes(int64_t M, int64_t C) {
   int lanes = 64;

@@ -19,7 +19,8 @@
  * sizes of zero are valid.  Matrix pointers are 16-byte aligned and row
  * pitches multiples of 16 bytes; unlike the GEMMs, these operators neither
  * read nor write the padding between a row's length and its pitch.
- * Results do not depend on the run: no sum is formed by atomics.
+ * Results do not depend on the run: no floating-point sum is formed by atomics
+ * (the sort counts pairs with them, in whole numbers).
  */
 #ifndef LIBFP8BLK_LAYER_H
 #define LIBFP8BLK_LAYER_H
