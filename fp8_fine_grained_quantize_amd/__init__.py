@@ -27,6 +27,8 @@ __all__ = [
     "layer_abi_version", "LAYER_SYMBOLS", "moe_sort", "moe_dispatch", "moe_dispatch_fp8", "moe_combine",
     "moe_combine_backward", "ResidualNorm", "ResidualNormGrad", "residual_norm", "residual_norm_backward",
     "GradTable", "grad_table", "grad_norm", "grad_clip", "clip_grad_norm",
+    # the optimizer step (train.py)
+    "train_abi_version", "TRAIN_SYMBOLS", "AdamWState", "AdamWTable", "adamw_table", "adamw_step",
 ]
 
 OP_N, OP_T = 0, 1
@@ -82,7 +84,7 @@ def lib() -> ctypes.CDLL:
             raise Fp8BlkError(f"{library_path} is missing: build it with "
                               "`python -m fp8_fine_grained_quantize_amd.build`")
         L = ctypes.CDLL(library_path)
-        for name, (res, args) in (*_SIGNATURES.items(), *layer.SIGNATURES.items()):
+        for name, (res, args) in (*_SIGNATURES.items(), *layer.SIGNATURES.items(), *train.SIGNATURES.items()):
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
@@ -382,3 +384,5 @@ from .layer import (  # noqa: E402
     LAYER_SYMBOLS, GradTable, ResidualNorm, ResidualNormGrad, clip_grad_norm, grad_clip, grad_norm, grad_table,
     layer_abi_version, moe_combine, moe_combine_backward, moe_dispatch, moe_dispatch_fp8, moe_sort, residual_norm,
     residual_norm_backward)
+from . import train  # noqa: E402
+from .train import AdamWState, AdamWTable, TRAIN_SYMBOLS, adamw_step, adamw_table, train_abi_version  # noqa: E402

@@ -33,7 +33,8 @@ COMMON_FLAGS = [
     f"-I{os.path.join(ROOT, 'include')}",
 ]
 
-SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "diag.hip", "moe.hip", "norm.hip", "grads.hip"]
+SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "diag.hip", "moe.hip", "norm.hip", "grads.hip", "adamw.hip"]
+BINDING = ["layer_binding.cpp", "train_binding.cpp"]
 
 
 def _run(what: str, cmd) -> None:
@@ -53,21 +54,21 @@ def _torch_dir() -> str:
     return os.path.dirname(os.path.abspath(torch.__file__))
 
 
-def _compile_binding() -> str:
-    """The binding's C++ part, against torch's headers (host code only)."""
-    obj = os.path.join(BUILD_DIR, "layer_binding.o")
+def _compile_binding(src: str) -> str:
+    """A source of the binding's C++ part, against torch's headers (host code only)."""
+    obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
     inc = os.path.join(_torch_dir(), "include")
-    _run("layer_binding.cpp", [CXX, "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", f"-I{inc}",
+    _run(src, [CXX, "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", f"-I{inc}",
                                f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
                                f"-I{sysconfig.get_paths()['include']}", "-w", "-c",
-                               os.path.join(CSRC, "layer_binding.cpp"), "-o", obj])
+                               os.path.join(CSRC, src), "-o", obj])
     return obj
 
 
-def _link_binding(obj: str) -> None:
+def _link_binding(objs) -> None:
     lib = os.path.join(_torch_dir(), "lib")
     tmp = EXT + ".tmp"
-    _run("link of the binding", [CXX, "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libfp8blk.so", f"-L{lib}",
+    _run("link of the binding", [CXX, "-shared", "-o", tmp, *objs, f"-L{PKG}", "-l:libfp8blk.so", f"-L{lib}",
                                  "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"])
     os.replace(tmp, EXT)
 
@@ -77,10 +78,10 @@ def build(verbose: bool = False) -> str:
     C++ part; returns the library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = [s for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(_compile, srcs))
-        binding = binding.result()
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + len(BINDING))) as ex:
+        objs = ex.map(_compile, srcs)
+        binding = list(ex.map(_compile_binding, BINDING))
+        objs = list(objs)
     tmp = LIB + ".tmp"
     _run("link", [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
     os.replace(tmp, LIB)

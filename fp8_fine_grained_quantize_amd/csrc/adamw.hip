@@ -1,0 +1,432 @@
+// One AdamW step over many tensors (gfx950).
+//
+//   g = grad c,  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
+//   p = p (1 - lr decay) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps),
+// c the clipping factor of a norm in device memory, so that clipping costs no
+// pass of its own.  The pages keep the moments in low precision [p2¶4]: FP32,
+// BF16, or E4M3 codes of m and sqrt(v) with a scale for 128 values (the root
+// halves the exponents that the codes have to span).
+// Citations [pN¶k]: N-th page of the source collection, k-th paragraph
+// (p2 = inprokorea.com wr_id 735329).
+//
+// Bound by HBM: 28 bytes a value in FP32, 16.06 with E4M3 moments, against some
+// 40 operations.  A workgroup takes a contiguous run of chunks (tensor_table.h);
+// a lane holds four consecutive values, so that FP32 is one 16-byte access, and
+// 32 lanes a group of 128, whose maximum is found by lane exchanges.
+#include <cmath>
+
+#include "../../include/libfp8blk_train.h"
+#include "host_common.h"
+#include "layer_device.h"
+#include "tensor_table.h"
+
+namespace fp8blk {
+
+constexpr int kAdamBlocks = 2048;  // most workgroups
+constexpr int kAdamUnroll = 2;     // groups of four values a lane has in flight
+
+struct AdamEntry {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  uint16_t* copy;
+  int64_t n, cols, ldp, ldg, ldc;
+  int64_t chunk0;
+  float decay;
+  uint32_t flags;
+  uint32_t index;
+  uint32_t pitched;
+};
+static_assert(sizeof(AdamEntry) == 120, "table entry");
+
+struct AdamArgs {
+  double beta1, beta2;
+  double lr;
+  int64_t step;
+  const float* lr_at;
+  const int64_t* step_at;
+  const int64_t* seed_at;
+  const float* norm;
+  float b1, nb1, b2, nb2, eps;  // nb = 1 - b
+  float max_norm, clip_eps;
+  float step_size, root;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  uint32_t seed;
+};
+
+__device__ __forceinline__ uint32_t random_bits(uint32_t key, int64_t place) {
+  uint32_t h = ((uint32_t)place * 0x9E3779B1u ^ (uint32_t)((uint64_t)place >> 32)) + key;
+  h = (h ^ h >> 16) * 0x85EBCA6Bu;
+  h = (h ^ h >> 13) * 0xC2B2AE35u;
+  return h ^ h >> 16;
+}
+
+// BF16 by adding 16 random bits below the kept ones and dropping those (a NaN stays one).
+__device__ __forceinline__ float to_bf16_random(float x, uint32_t r16) {
+  return x == x ? __uint_as_float((__float_as_uint(x) + r16) & 0xFFFF0000u) : x;
+}
+
+// Codes of four values of a group of 128 that 32 lanes hold.  ROOT: the values
+// are not negative and none above zero becomes zero.
+template <bool ROOT>
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], bool random, const uint32_t (&r16)[4], float& scale) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) a = max(a, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+  a = row16_max(a);
+  const auto o = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const TileScale ts = make_scale<false, true>(max(o[0], o[1]));
+  scale = ts.s;
+  float y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = quotient_fast<false, true>(x[j], ts);
+  if (__builtin_expect(ts.slow, 0)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = quotient_slow(x[j], ts.s);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float v = fminf(__builtin_fabsf(y[j]), kE4M3Max);
+    if (random) {  // below 2^-6 the codes lie 2^-9 apart, as they do from there to 2^-5
+      const float up = v < 0x1p-6f ? 0x1p-6f : 0.0f;
+      v = __uint_as_float((__float_as_uint(v + up) + (r16[j] << 4)) & 0xFFF00000u) - up;
+    }
+    if (ROOT && x[j] > 0.0f) v = fmaxf(v, 0x1p-9f);
+    y[j] = __builtin_copysignf(v, x[j]);
+  }
+  return pack4_e4m3(y[0], y[1], y[2], y[3]);
+}
+
+__device__ __forceinline__ void decode4(uint32_t c, float s, float (&x)[4]) {
+  const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
+  x[0] = lo[0] * s;
+  x[1] = lo[1] * s;
+  x[2] = hi[0] * s;
+  x[3] = hi[1] * s;
+}
+
+// How a lane's four values lie in memory: one after another; in a row of a
+// tensor whose rows lie apart; or in two rows of one.
+enum Lie { DENSE, ROW, ROWS };
+
+// The elements i .. i + count - 1 of a tensor in rows of cols, ld apart (4 at
+// once: one access unless they lie in two rows); the others zero.
+template <bool NT, typename T>
+__device__ __forceinline__ RawV<T, 4> load4(const T* t, int64_t i, int count, Lie lie, int64_t cols, int64_t ld) {
+  if (count == 4 && lie != ROWS) return load_raw<4, NT>(global(t + (lie == ROW ? at(i, cols, ld) : i)));
+  RawV<T, 4> r{};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j >= count) continue;
+    const T x = global(t)[lie == DENSE ? i + j : at(i + j, cols, ld)];
+    if constexpr (sizeof(T) == 4) r[j] = __float_as_uint(x);
+    else r[j >> 1] |= (uint32_t)x << ((j & 1) * 16);
+  }
+  return r;
+}
+template <bool NT, typename T>
+__device__ __forceinline__ void store4(T* t, const float (&v)[4], int64_t i, int count, Lie lie, int64_t cols,
+                                       int64_t ld) {
+  if (count == 4 && lie != ROWS) return store_v<4, NT>(global(t + (lie == ROW ? at(i, cols, ld) : i)), v);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < count) global(t)[lie == DENSE ? i + j : at(i + j, cols, ld)] = from_f32<T>(v[j]);
+}
+
+// The moments' type as stored, and what a lane loads of them.
+template <int ST>
+struct Moment {
+  typedef uint16_t type;
+  typedef RawV<uint16_t, 4> raw;
+};
+template <>
+struct Moment<FP8BLK_ADAMW_F32> {
+  typedef float type;
+  typedef RawV<float, 4> raw;
+};
+template <>
+struct Moment<FP8BLK_ADAMW_E4M3> {
+  typedef uint8_t type;
+  typedef uint32_t raw;
+};
+
+template <typename TP, typename TG, int ST>
+struct Quad {  // what a lane loads of its four values
+  RawV<TP, 4> p;
+  RawV<TG, 4> g;
+  typename Moment<ST>::raw m, v;
+  float ms, vs;
+};
+
+template <typename TP, typename TG, int ST, bool NT>
+struct AdamRange {
+  typedef typename Moment<ST>::type TM;
+  const AdamEntry& e;
+  const AdamArgs& a;
+  float clip, keep, step_size, root;  // keep: 1 - lr decay
+  uint32_t key;
+  bool random;
+
+  __device__ __forceinline__ Quad<TP, TG, ST> load(int64_t i, int count, Lie lie) const {
+    Quad<TP, TG, ST> q{};
+    q.p = load4<NT>((const TP*)e.p, i, count, lie, e.cols, e.ldp);
+    q.g = load4<NT>((const TG*)e.g, i, count, lie, e.cols, e.ldg);
+    if constexpr (ST == FP8BLK_ADAMW_E4M3) {
+      const Global<const uint8_t> *m = global((const uint8_t*)e.m + i), *v = global((const uint8_t*)e.v + i);
+      if (count == 4) {
+        q.m = *(const Global<const uint32_t>*)m;
+        q.v = *(const Global<const uint32_t>*)v;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          if (j >= count) continue;
+          q.m |= (uint32_t)m[j] << (8 * j);
+          q.v |= (uint32_t)v[j] << (8 * j);
+        }
+      }
+      if (count > 0) {
+        q.ms = global(e.ms)[i >> 7];
+        q.vs = global(e.vs)[i >> 7];
+      }
+    } else {
+      q.m = load4<NT>((const TM*)e.m, i, count, DENSE, 0, 0);
+      q.v = load4<NT>((const TM*)e.v, i, count, DENSE, 0, 0);
+    }
+    return q;
+  }
+
+  // Every lane of the wave takes part (count may be 0): E4M3 scales are found across lanes.
+  __device__ __forceinline__ void finish(const Quad<TP, TG, ST>& q, int64_t i, int count, Lie lie) const {
+    float p[4], g[4], m[4], v[4], r[4];
+    unpack_v<TP, 4>(q.p, p);
+    unpack_v<TG, 4>(q.g, g);
+    if constexpr (ST == FP8BLK_ADAMW_E4M3) {
+      decode4(q.m, q.ms, m);
+      decode4(q.v, q.vs, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] *= v[j];
+    } else {
+      unpack_v<TM, 4>(q.m, m);
+      unpack_v<TM, 4>(q.v, v);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      g[j] *= clip;
+      m[j] = __builtin_fmaf(a.b1, m[j], a.nb1 * g[j]);
+      v[j] = __builtin_fmaf(a.b2, v[j], a.nb2 * g[j] * g[j]);
+      r[j] = sqrtf(v[j]);
+      p[j] = __builtin_fmaf(p[j], keep, -(step_size * m[j] / __builtin_fmaf(r[j], root, a.eps)));
+    }
+    uint32_t rm[4] = {}, rv[4] = {};
+    if (ST != FP8BLK_ADAMW_F32 && random) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t h = random_bits(key, i + j);
+        rm[j] = h & 0xFFFFu;
+        rv[j] = h >> 16;
+      }
+    }
+    if constexpr (ST == FP8BLK_ADAMW_E4M3) {
+      float ms, vs;
+      const uint32_t mc = encode4<false>(m, random, rm, ms), vc = encode4<true>(r, random, rv, vs);
+      Global<uint8_t> *md = global((uint8_t*)e.m + i), *vd = global((uint8_t*)e.v + i);
+      if (count == 4) {
+        store_words<NT, 1>((Global<void>*)md, Words<1>::type{mc});
+        store_words<NT, 1>((Global<void>*)vd, Words<1>::type{vc});
+      } else {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          if (j >= count) continue;
+          md[j] = (uint8_t)(mc >> (8 * j));
+          vd[j] = (uint8_t)(vc >> (8 * j));
+        }
+      }
+      if (count > 0 && (threadIdx.x & 31) == 0) {
+        global(e.ms)[i >> 7] = ms;
+        global(e.vs)[i >> 7] = vs;
+      }
+    } else {
+      if (ST == FP8BLK_ADAMW_BF16 && random) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          m[j] = to_bf16_random(m[j], rm[j]);
+          v[j] = to_bf16_random(v[j], rv[j]);
+        }
+      }
+      store4<NT>((TM*)e.m, m, i, count, DENSE, 0, 0);
+      store4<NT>((TM*)e.v, v, i, count, DENSE, 0, 0);
+    }
+    if (e.copy != nullptr) store4<NT>(e.copy, p, i, count, lie, e.cols, e.ldc);
+    if (sizeof(TP) == 2 && random) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] = to_bf16_random(p[j], random_bits(key ^ 0x5BD1E995u, i + j) & 0xFFFFu);
+    }
+    store4<NT>((TP*)e.p, p, i, count, lie, e.cols, e.ldp);
+  }
+
+  // The elements [lo, hi); lo is a multiple of kChunk, hi too unless the tensor ends there.
+  __device__ __forceinline__ void run(int64_t lo, int64_t hi) const {
+    const int64_t mine = (int64_t)threadIdx.x * 4;
+    int64_t base = lo;
+    if (!e.pitched) {
+      for (; base + kChunk * kAdamUnroll <= hi; base += kChunk * kAdamUnroll) {
+        Quad<TP, TG, ST> q[kAdamUnroll];
+#pragma unroll
+        for (int u = 0; u < kAdamUnroll; ++u) q[u] = load(base + u * kChunk + mine, 4, DENSE);
+#pragma unroll
+        for (int u = 0; u < kAdamUnroll; ++u) finish(q[u], base + u * kChunk + mine, 4, DENSE);
+      }
+    }
+    const Lie lie = !e.pitched ? DENSE : (e.cols & 3) == 0 ? ROW : ROWS;
+    for (; base < hi; base += kChunk) {
+      const int64_t i = base + mine;
+      const int left = (int)max((int64_t)0, min((int64_t)4, hi - i));
+      finish(load(i, left, lie), i, left, lie);
+    }
+  }
+};
+
+template <int ST, bool NT>
+__global__ __launch_bounds__(256) void k_adamw(const AdamEntry* __restrict__ tab, int64_t n, int64_t chunks,
+                                                AdamArgs a, bool random) {
+  Walk<AdamEntry> w(tab, n, chunks);
+  double lr = a.lr;
+  float step_size = a.step_size, root = a.root, clip = 1.0f;
+  if (a.lr_at != nullptr) lr = *a.lr_at;
+  if (a.step_at != nullptr) {
+    const double t = (double)*a.step_at;
+    root = (float)(1.0 / sqrt(1.0 - pow(a.beta2, t)));
+    step_size = (float)(lr / (1.0 - pow(a.beta1, t)));
+  } else if (a.lr_at != nullptr) {
+    step_size = (float)(lr / (1.0 - pow(a.beta1, (double)a.step)));
+  }
+  const uint32_t seed = a.seed_at != nullptr ? (uint32_t)*a.seed_at : a.seed;
+  if (a.norm != nullptr) {
+    clip = a.max_norm / (*a.norm + a.clip_eps);
+    clip = clip >= 1.0f ? 1.0f : clip;  // a NaN stays
+  }
+  while (w.step()) {
+    const float keep = (float)(1.0 - lr * w.e.decay);
+    const uint32_t key = seed + w.e.index * 0x27D4EB2Fu;
+    auto run = [&](auto tp, auto tg) {
+      AdamRange<decltype(tp), decltype(tg), ST, NT>{w.e, a, clip, keep, step_size, root, key, random}.run(w.lo, w.hi);
+    };
+    if (w.e.flags & FP8BLK_ADAMW_PARAM_F32) {
+      if (w.e.flags & FP8BLK_ADAMW_GRAD_F32) run(float(), float());
+      else run(float(), uint16_t());
+    } else {
+      if (w.e.flags & FP8BLK_ADAMW_GRAD_F32) run(uint16_t(), float());
+      else run(uint16_t(), uint16_t());
+    }
+  }
+}
+
+// Streamed loads and stores (see kStreamBytes in layer_host.h) from 2^23 elements on.
+inline bool adam_stream(int64_t chunks) { return chunks >= ((int64_t)1 << 23) / kChunk; }
+
+inline bool state_ok(int state) {
+  return state == FP8BLK_ADAMW_F32 || state == FP8BLK_ADAMW_BF16 || state == FP8BLK_ADAMW_E4M3;
+}
+
+}  // namespace fp8blk
+
+using namespace fp8blk;
+
+extern "C" int fp8blk_train_abi_version(void) { return 1; }
+
+extern "C" size_t fp8blk_adamw_table_bytes(int64_t n) { return n > 0 ? (size_t)n * sizeof(AdamEntry) : 0; }
+
+extern "C" fp8blk_status_t fp8blk_adamw_table_build(const fp8blk_adamw_t* list, int64_t n, int state, void* table,
+                                                    size_t table_bytes, int64_t* chunks) {
+  if (n < 0 || chunks == nullptr || !state_ok(state)) return FP8BLK_ERR_INVALID_ARG;
+  if (n > 0 && (list == nullptr || table == nullptr || !aligned(table, 8) || table_bytes < fp8blk_adamw_table_bytes(n)))
+    return FP8BLK_ERR_INVALID_ARG;
+  int64_t next = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const fp8blk_adamw_t& t = list[i];
+    const uintptr_t pe = t.flags & FP8BLK_ADAMW_PARAM_F32 ? 4 : 2, ge = t.flags & FP8BLK_ADAMW_GRAD_F32 ? 4 : 2;
+    const uintptr_t me = state == FP8BLK_ADAMW_BF16 ? 2 : 4;  // codes are read four at a time
+    if ((t.flags & ~(FP8BLK_ADAMW_PARAM_F32 | FP8BLK_ADAMW_GRAD_F32)) || t.reserved != 0) return FP8BLK_ERR_INVALID_ARG;
+    if (t.rows <= 0 || t.cols <= 0) return FP8BLK_ERR_INVALID_ARG;  // empty tensors have no place in the table
+    for (const int64_t ld : {t.ldp, t.ldg, t.copy != nullptr ? t.ldc : t.cols})
+      if (ld < t.cols || t.rows > INT64_MAX / 16 / ld) return FP8BLK_ERR_INVALID_ARG;
+    if (t.param == nullptr || t.grad == nullptr || t.m == nullptr || t.v == nullptr) return FP8BLK_ERR_INVALID_ARG;
+    if (!aligned(t.param, pe) || !aligned(t.grad, ge) || !aligned(t.m, me) || !aligned(t.v, me) || !aligned(t.copy, 2))
+      return FP8BLK_ERR_INVALID_ARG;
+    const bool scaled = state == FP8BLK_ADAMW_E4M3;
+    if (scaled != (t.m_scale != nullptr) || scaled != (t.v_scale != nullptr) || !aligned(t.m_scale, 4) ||
+        !aligned(t.v_scale, 4))
+      return FP8BLK_ERR_INVALID_ARG;
+    AdamEntry e{};
+    e.p = t.param;
+    e.g = t.grad;
+    e.m = t.m;
+    e.v = t.v;
+    e.ms = t.m_scale;
+    e.vs = t.v_scale;
+    e.copy = t.copy;
+    e.n = t.rows * t.cols;
+    e.cols = t.cols;
+    e.ldp = t.ldp;
+    e.ldg = t.ldg;
+    e.ldc = t.copy != nullptr ? t.ldc : t.cols;
+    e.chunk0 = next;
+    e.decay = t.decay;
+    e.flags = t.flags;
+    e.index = t.index;
+    e.pitched = t.rows > 1 && (t.ldp != t.cols || t.ldg != t.cols || e.ldc != t.cols);
+    next += ceil_div(e.n, kChunk);
+    reinterpret_cast<AdamEntry*>(table)[i] = e;
+  }
+  *chunks = next;
+  return FP8BLK_OK;
+}
+
+extern "C" fp8blk_status_t fp8blk_adamw_step(const void* table, int64_t n, int64_t chunks, int state,
+                                             const fp8blk_adamw_step_t* s, void* stream) {
+  if (n < 0 || chunks < n || !state_ok(state) || s == nullptr) return FP8BLK_ERR_INVALID_ARG;
+  if (n == 0 ? chunks != 0 : table == nullptr || !aligned(table, 8)) return FP8BLK_ERR_INVALID_ARG;
+  if (!(s->beta1 >= 0.0 && s->beta1 < 1.0) || !(s->beta2 >= 0.0 && s->beta2 < 1.0) || !(s->eps >= 0.0))
+    return FP8BLK_ERR_INVALID_ARG;
+  if ((s->lr_at == nullptr && !(s->lr - s->lr == 0.0)) || (s->step_at == nullptr && s->step < 1) ||
+      (s->flags & ~FP8BLK_ADAMW_RANDOM))
+    return FP8BLK_ERR_INVALID_ARG;
+  if (!aligned(s->lr_at, 4) || !aligned(s->step_at, 8) || !aligned(s->seed_at, 8) || !aligned(s->norm, 4))
+    return FP8BLK_ERR_INVALID_ARG;
+  if (s->norm != nullptr && (!(s->max_norm >= 0.0f) || !(s->clip_eps >= 0.0f))) return FP8BLK_ERR_INVALID_ARG;
+  if (n == 0) return FP8BLK_OK;
+  AdamArgs a{};
+  a.beta1 = s->beta1;
+  a.beta2 = s->beta2;
+  a.lr = s->lr;
+  a.step = s->step;
+  a.lr_at = s->lr_at;
+  a.step_at = s->step_at;
+  a.seed_at = s->seed_at;
+  a.norm = s->norm;
+  a.b1 = (float)s->beta1;
+  a.nb1 = (float)(1.0 - s->beta1);
+  a.b2 = (float)s->beta2;
+  a.nb2 = (float)(1.0 - s->beta2);
+  a.eps = (float)s->eps;
+  a.max_norm = s->max_norm;
+  a.clip_eps = s->clip_eps;
+  if (s->step_at == nullptr) {
+    a.step_size = (float)(s->lr / (1.0 - pow(s->beta1, (double)s->step)));
+    a.root = (float)(1.0 / sqrt(1.0 - pow(s->beta2, (double)s->step)));
+  }
+  a.seed = s->seed;
+  const dim3 grid((unsigned)(chunks < kAdamBlocks ? chunks : kAdamBlocks)), block(256);
+  const AdamEntry* tab = reinterpret_cast<const AdamEntry*>(table);
+  const bool random = s->flags & FP8BLK_ADAMW_RANDOM, nt = adam_stream(chunks);
+#define FP8BLK_ADAMW_LAUNCH(ST_)                                                                                    \
+  hipLaunchKernelGGL((nt ? k_adamw<ST_, true> : k_adamw<ST_, false>), grid, block, 0, as_stream(stream), tab, n, chunks, \
+                     a, random)
+  if (state == FP8BLK_ADAMW_F32) FP8BLK_ADAMW_LAUNCH(FP8BLK_ADAMW_F32);
+  else if (state == FP8BLK_ADAMW_BF16) FP8BLK_ADAMW_LAUNCH(FP8BLK_ADAMW_BF16);
+  else FP8BLK_ADAMW_LAUNCH(FP8BLK_ADAMW_E4M3);
+#undef FP8BLK_ADAMW_LAUNCH
+  return launch_status();
+}

@@ -21,10 +21,10 @@
 #include "../../include/libfp8blk_layer.h"
 #include "host_common.h"
 #include "layer_device.h"
+#include "tensor_table.h"
 
 namespace fp8blk {
 
-constexpr int64_t kChunk = 1024;
 constexpr int kGradBlocks = 1024;  // most workgroups, one partial sum each (2048: 1 % slower over 3.8 GB)
 static_assert(kGradBlocks * sizeof(double) <= FP8BLK_GRAD_WORKSPACE_BYTES, "partial sums fit the workspace");
 
@@ -38,25 +38,6 @@ struct GradEntry {
   uint32_t pitched;
 };
 static_assert(sizeof(GradEntry) == 64, "table entry");
-
-// The tensor that owns chunk c, found by the wave: 64 candidates at a time.
-// Every entry has at least one chunk, so chunk0 ascends strictly.
-__device__ __forceinline__ int64_t find_entry(const GradEntry* __restrict__ tab, int64_t n, int64_t c) {
-  const int lane = threadIdx.x & 63;
-  int64_t lo = 0, len = n;  // the owner is in [lo, lo + len), tab[lo].chunk0 <= c
-  while (len > 1) {
-    const int64_t step = (len + 63) / 64;
-    const int64_t i = lo + lane * step;
-    const uint64_t le = __ballot(lane * step < len && tab[i].chunk0 <= c);
-    const int64_t last = 63 - __builtin_clzll(le);
-    lo += last * step;
-    len = min(step, len - last * step);
-  }
-  return lo;
-}
-
-// Element offset of a flat index: rows lie ld elements apart.
-__device__ __forceinline__ int64_t at(int64_t i, int64_t cols, int64_t ld) { return i / cols * ld + i % cols; }
 
 // Calls body(v, k) for groups of V contiguous elements of [lo, hi), v from
 // element k on in FP32: kUnroll groups per lane in flight while whole ones are
@@ -122,34 +103,12 @@ __device__ __forceinline__ void scale_range(const GradEntry& e, int64_t lo, int6
   }, [&](float x, int64_t k) { dst[k] = from_f32<TD>(x * c); });
 }
 
-// The gradients of a workgroup's chunks [c, c1), one range of elements each.
-struct Walk {
-  const GradEntry* tab;
-  int64_t n, t, c, c1;
-  GradEntry e;
-  int64_t lo, hi;
-  __device__ __forceinline__ Walk(const GradEntry* tab_, int64_t n_, int64_t chunks)
-      : tab(tab_), n(n_), t(0), c(chunks * blockIdx.x / gridDim.x), c1(chunks * (blockIdx.x + 1) / gridDim.x) {
-    if (c < c1) t = find_entry(tab, n, c);
-  }
-  __device__ __forceinline__ bool step() {
-    if (c >= c1) return false;
-    e = tab[t];
-    const int64_t end = t + 1 < n ? min(tab[t + 1].chunk0, c1) : c1;
-    lo = (c - e.chunk0) * kChunk;
-    hi = min((end - e.chunk0) * kChunk, e.n);
-    c = end;
-    ++t;
-    return true;
-  }
-};
-
 template <bool NT>
 __global__ __launch_bounds__(256) void k_grad_squares(const GradEntry* __restrict__ tab, int64_t n, int64_t chunks,
                                                        double* __restrict__ partial) {
   __shared__ double red[4];
   double sum = 0.0;
-  Walk w(tab, n, chunks);
+  Walk<GradEntry> w(tab, n, chunks);
   while (w.step()) {
     if (w.e.flags & FP8BLK_GRAD_F32) add_squares<float, NT>(w.e, w.lo, w.hi, sum);
     else add_squares<uint16_t, NT>(w.e, w.lo, w.hi, sum);
@@ -184,7 +143,7 @@ __global__ __launch_bounds__(256) void k_grad_scale(const GradEntry* __restrict_
                                                      const float* given, const double* __restrict__ partial, int np,
                                                      float max_norm, float eps, float* norm) {
   __shared__ double red[4];
-  Walk w(tab, n, chunks);  // the search of the table overlaps the partial sums' way from memory
+  Walk<GradEntry> w(tab, n, chunks);  // the search of the table overlaps the partial sums' way from memory
   float total;
   if (given != nullptr) {
     total = *given;
