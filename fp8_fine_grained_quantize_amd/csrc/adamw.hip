@@ -13,6 +13,11 @@
 // 40 operations.  A workgroup takes a contiguous run of chunks (tensor_table.h);
 // a lane holds four consecutive values, so that FP32 is one 16-byte access, and
 // 32 lanes a group of 128, whose maximum is found by lane exchanges.
+//
+// Every operation is rounded by itself, none fused, in the order in which a
+// program of elementary FP32 operations takes them: a value that differs in its
+// last bit can fall to another E4M3 code, 6 to 12 % away, so that only equal
+// operations give equal codes.
 #include <cmath>
 
 #include "../../include/libfp8blk_train.h"
@@ -68,6 +73,17 @@ __device__ __forceinline__ float to_bf16_random(float x, uint32_t r16) {
   return x == x ? __uint_as_float((__float_as_uint(x) + r16) & 0xFFFF0000u) : x;
 }
 
+// The scale of a group with that maximum, and its reciprocal for the quotients
+// (within one unit in the last place, see fp8_device.h).
+__device__ __forceinline__ TileScale moment_scale(uint32_t amax_bits) {
+  TileScale t{1.0f, 1.0f, false};
+  if (amax_bits == 0) return t;
+  t.s = __uint_as_float(amax_bits) * (1.0f / kE4M3Max);
+  t.r = 1.0f / t.s;
+  t.slow = !(t.s >= 0x1p-100f && t.s <= 0x1p100f);
+  return t;
+}
+
 // Codes of four values of a group of 128 that 32 lanes hold.  ROOT: the values
 // are not negative and none above zero becomes zero.
 template <bool ROOT>
@@ -77,7 +93,7 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4], bool random, co
   for (int j = 0; j < 4; ++j) a = max(a, __float_as_uint(x[j]) & 0x7FFFFFFFu);
   a = row16_max(a);
   const auto o = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-  const TileScale ts = make_scale<false, true>(max(o[0], o[1]));
+  const TileScale ts = moment_scale(max(o[0], o[1]));
   scale = ts.s;
   float y[4];
 #pragma unroll
@@ -214,10 +230,10 @@ struct AdamRange {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       g[j] *= clip;
-      m[j] = __builtin_fmaf(a.b1, m[j], a.nb1 * g[j]);
-      v[j] = __builtin_fmaf(a.b2, v[j], a.nb2 * g[j] * g[j]);
+      m[j] = a.b1 * m[j] + a.nb1 * g[j];
+      v[j] = a.b2 * v[j] + a.nb2 * g[j] * g[j];
       r[j] = sqrtf(v[j]);
-      p[j] = __builtin_fmaf(p[j], keep, -(step_size * m[j] / __builtin_fmaf(r[j], root, a.eps)));
+      p[j] = p[j] * keep - step_size * m[j] / (r[j] * root + a.eps);
     }
     uint32_t rm[4] = {}, rv[4] = {};
     if (ST != FP8BLK_ADAMW_F32 && random) {
@@ -297,14 +313,14 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamEntry* __restrict__ tab
   if (a.lr_at != nullptr) lr = *a.lr_at;
   if (a.step_at != nullptr) {
     const double t = (double)*a.step_at;
-    root = (float)(1.0 / sqrt(1.0 - pow(a.beta2, t)));
+    root = 1.0f / (float)sqrt(1.0 - pow(a.beta2, t));
     step_size = (float)(lr / (1.0 - pow(a.beta1, t)));
   } else if (a.lr_at != nullptr) {
     step_size = (float)(lr / (1.0 - pow(a.beta1, (double)a.step)));
   }
   const uint32_t seed = a.seed_at != nullptr ? (uint32_t)*a.seed_at : a.seed;
   if (a.norm != nullptr) {
-    clip = a.max_norm / (*a.norm + a.clip_eps);
+    clip = a.max_norm * (1.0f / (*a.norm + a.clip_eps));
     clip = clip >= 1.0f ? 1.0f : clip;  // a NaN stays
   }
   while (w.step()) {
@@ -415,7 +431,7 @@ extern "C" fp8blk_status_t fp8blk_adamw_step(const void* table, int64_t n, int64
   a.clip_eps = s->clip_eps;
   if (s->step_at == nullptr) {
     a.step_size = (float)(s->lr / (1.0 - pow(s->beta1, (double)s->step)));
-    a.root = (float)(1.0 / sqrt(1.0 - pow(s->beta2, (double)s->step)));
+    a.root = 1.0f / (float)sqrt(1.0 - pow(s->beta2, (double)s->step));
   }
   a.seed = s->seed;
   const dim3 grid((unsigned)(chunks < kAdamBlocks ? chunks : kAdamBlocks)), block(256);

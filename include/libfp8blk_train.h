@@ -40,8 +40,8 @@ int fp8blk_train_abi_version(void);
 /* How the moments are stored, one for a whole table:
  *   F32, BF16  m and v as they are;
  *   E4M3       codes of m / s_m and of sqrt(v) / s_v, with one FP32 scale
- *              (amax / 448, 1 where all are zero) for every 128 consecutive
- *              elements of a tensor.  A v that is not zero keeps at least the
+ *              (amax times 1 / 448, both in FP32; 1 where all are zero) for
+ *              every 128 consecutive elements of a tensor.  A v that is not zero keeps at least the
  *              smallest code, so that no moment is divided by a rounded-off
  *              zero.  A NaN or an infinity spoils its 128 elements' moments. */
 enum { FP8BLK_ADAMW_F32 = 0, FP8BLK_ADAMW_BF16 = 1, FP8BLK_ADAMW_E4M3 = 2 };

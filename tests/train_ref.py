@@ -68,7 +68,7 @@ def code_bounds(x, e, random, floor):
     n = x.size
     top, et = group_max(x), group_max(e)
     s = np.where(top == 0, 1.0, top / 448)
-    es = np.where(top == 0, 0.0, et / 448 + 2 * U * s)
+    es = np.where(top == 0, 0.0, et / 448 + 3 * U * s)  # 1 / 448 and the product are rounded: 2 U and their product
     S = spread(s + es, n)
     k = 2 if random else 1
     # the quotient is within one unit in the last place, and what saturates at 448 is off by the scale's error
