@@ -27,7 +27,9 @@ __all__ = [
     "layer_abi_version", "LAYER_SYMBOLS", "moe_sort", "moe_dispatch", "moe_dispatch_fp8", "moe_combine",
     "moe_combine_backward", "ResidualNorm", "ResidualNormGrad", "residual_norm", "residual_norm_backward",
     "GradTable", "grad_table", "grad_norm", "grad_clip", "clip_grad_norm",
-    # the optimizer step (train.py)
+    # the gated feed-forward block and the optimizer step (train.py)
+    "GatedGemm", "GatedGemmGrad", "gated_gemm_fp8_blockscaled", "grouped_gated_gemm_fp8_blockscaled",
+    "gated_gemm_backward_fp8_blockscaled", "grouped_gated_gemm_backward_fp8_blockscaled",
     "train_abi_version", "TRAIN_SYMBOLS", "AdamWState", "AdamWTable", "adamw_table", "adamw_step",
 ]
 
@@ -385,4 +387,7 @@ from .layer import (  # noqa: E402
     layer_abi_version, moe_combine, moe_combine_backward, moe_dispatch, moe_dispatch_fp8, moe_sort, residual_norm,
     residual_norm_backward)
 from . import train  # noqa: E402
-from .train import AdamWState, AdamWTable, TRAIN_SYMBOLS, adamw_step, adamw_table, train_abi_version  # noqa: E402
+from .train import (  # noqa: E402
+    AdamWState, AdamWTable, GatedGemm, GatedGemmGrad, TRAIN_SYMBOLS, adamw_step, adamw_table,
+    gated_gemm_backward_fp8_blockscaled, gated_gemm_fp8_blockscaled, grouped_gated_gemm_backward_fp8_blockscaled,
+    grouped_gated_gemm_fp8_blockscaled, train_abi_version)

@@ -33,7 +33,8 @@ COMMON_FLAGS = [
     f"-I{os.path.join(ROOT, 'include')}",
 ]
 
-SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "diag.hip", "moe.hip", "norm.hip", "grads.hip", "adamw.hip"]
+SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "diag.hip", "moe.hip", "norm.hip", "grads.hip", "adamw.hip",
+           "gated.hip"]
 BINDING = ["layer_binding.cpp", "train_binding.cpp"]
 
 

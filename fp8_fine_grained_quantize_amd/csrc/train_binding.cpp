@@ -1,5 +1,7 @@
 // Python binding of the gated feed-forward block and of the optimizer step (see
 // binding.h; train.py passes the arguments by position, the current stream last).
+#include <ATen/ops/new_empty.h>
+
 #include <algorithm>
 #include <vector>
 
@@ -9,6 +11,156 @@
 namespace {
 
 using namespace fp8blk_py;
+
+// --- the gated feed-forward block ----------------------------------------------
+
+// Codes and scales of a product's operands, checked; G = 0: one B, otherwise one for every expert.
+struct Product {
+  const Tensor *A, *sA, *B, *sB, *offsets;
+  int64_t G = 0, M, N, K, lda, ldb, strideB = 0, stride_sB = 0, max_rows = 0;
+  int act, opB;
+};
+
+// a[0 .. 8]: offsets, A, sA, B, sB, act, opB, pow2_scales, max_group_rows
+Product product(PyObject* const* a) {
+  Product p;
+  p.offsets = maybe(a[0], "offsets");
+  p.A = &given(a[1], "A");
+  p.sA = &given(a[2], "sA");
+  p.B = &given(a[3], "B");
+  p.sB = &given(a[4], "sB");
+  p.act = static_cast<int>(integer(a[5]));
+  p.opB = static_cast<int>(integer(a[6]));
+  if (p.opB != FP8BLK_OP_N && p.opB != FP8BLK_OP_T) value_error("opB must be OP_N or OP_T");
+  need(*p.A, at::kByte, "A");
+  need(*p.B, at::kByte, "B");
+  need(*p.sB, at::kFloat, "sB");
+  two_d(*p.A, "A");
+  p.M = p.A->size(0);
+  p.K = p.A->size(1);
+  p.lda = pitch(*p.A, "A");
+  const bool grouped = p.offsets != nullptr;
+  if (p.B->dim() != (grouped ? 3 : 2)) value_error(std::string("B must have ") + (grouped ? "3" : "2") + " dimensions, got " + sizes(*p.B));
+  const Tensor one = grouped && p.B->size(0) > 0 ? p.B->select(0, 0) : grouped ? p.B->new_empty({p.B->size(1), p.B->size(2)}) : *p.B;
+  const int64_t rows = one.size(0), cols = one.size(1);
+  p.ldb = pitch(one, "B");
+  p.N = p.opB == FP8BLK_OP_N ? cols : rows;
+  if ((p.opB == FP8BLK_OP_N ? rows : cols) != p.K)
+    value_error("B must have " + std::to_string(p.K) + (p.opB == FP8BLK_OP_N ? " rows" : " columns") + ", as A has columns, got " + sizes(*p.B));
+  if (p.K % 128 != 0 || p.N % 128 != 0) value_error("sizes of B must be multiples of 128, got " + sizes(*p.B));
+  dense(*p.sA, at::kFloat, {p.K / 128, p.M}, "sA");
+  if (!grouped) {
+    dense(*p.sB, at::kFloat, {rows / 128, cols / 128}, "sB");
+  } else {
+    need(*p.offsets, at::kInt, "offsets");
+    if (p.offsets->dim() != 1 || p.offsets->size(0) != p.B->size(0) + 1 || !p.offsets->is_contiguous())
+      value_error("offsets must be a contiguous vector of one more than the experts of B, got " + sizes(*p.offsets));
+    p.G = p.B->size(0);
+    if (p.sB->dim() != 3 || p.sB->size(0) != p.G) value_error("sB has the wrong shape: " + sizes(*p.sB));
+    if (p.G > 0) dense(p.sB->select(0, 0), at::kFloat, {rows / 128, cols / 128}, "sB");
+    p.strideB = p.G > 1 ? p.B->stride(0) : rows * p.ldb;
+    p.stride_sB = p.G > 1 ? p.sB->stride(0) : rows / 128 * (cols / 128);
+    p.max_rows = a[8] == Py_None ? p.M : integer(a[8]);
+  }
+  if (truth(a[7])) p.opB |= FP8BLK_GEMM_POW2_SCALES;
+  return p;
+}
+
+uint16_t* bits(const Tensor& t) { return t.defined() ? static_cast<uint16_t*>(addr(t)) : nullptr; }
+
+// q and s of `cols` columns where they are asked for.
+void quantized(const Product& p, int64_t cols, const Tensor* oq, const Tensor* os, Tensor& q, Tensor& s, int64_t& ldq) {
+  q = output(oq, p.M, cols, at::kByte, *p.A, "q", ldq);
+  if (os != nullptr) dense(*os, at::kFloat, {cols / 128, p.M}, "s");
+  s = os != nullptr ? *os : vec({cols / 128, p.M}, at::kFloat, *p.A);
+}
+
+// The given workspace, or a new one of that size (none for 0 bytes).
+Tensor room(const Tensor* given, size_t bytes, const Tensor& like) {
+  if (given != nullptr) return *given;
+  return bytes != 0 ? vec({static_cast<int64_t>((bytes + 3) / 4)}, at::kFloat, like) : Tensor();
+}
+
+// product's arguments, then quantize, pow2, want_h, want_u, split_k, workspace, u, h, q, s, stream
+PyObject* gated_gemm(PyObject* const* a) {
+  const Product p = product(a);
+  a += 9;
+  const bool quantize = truth(a[0]), pow2 = truth(a[1]), want_h = truth(a[2]), want_u = truth(a[3]), split = truth(a[4]);
+  const Tensor *w = maybe(a[5], "workspace"), *ou = maybe(a[6], "u"), *oh = maybe(a[7], "h"), *oq = maybe(a[8], "q");
+  const Tensor* os = maybe(a[9], "s");
+  if (p.N % 256 != 0) value_error("B must have the gate's columns and as many of the up projection, got " + sizes(*p.B));
+  if (!quantize && (oq != nullptr || os != nullptr)) value_error("q and s need quantize");
+  scratch(w);
+  void* stream = stream_of(a[10], *p.A, {p.offsets, p.sA, p.B, p.sB, w, ou, oh, oq, os});
+  Unlocked unlocked;
+  own({w, ou, oh, oq, os});
+  const int64_t H = p.N / 2;
+  int64_t ldu = 0, ldh = 0, ldq = 0;
+  Tensor u, h, q, s;
+  if (ou != nullptr || want_u) u = output(ou, p.M, 2 * H, at::kBFloat16, *p.A, "u", ldu);
+  if (oh != nullptr || want_h || !quantize) h = output(oh, p.M, H, at::kBFloat16, *p.A, "h", ldh);
+  if (quantize) quantized(p, H, oq, os, q, s, ldq);
+  const uint32_t flags = pow2 ? FP8BLK_SCALE_POW2 : 0;
+  auto* qp = q.defined() ? static_cast<uint8_t*>(addr(q)) : nullptr;
+  auto* sp = s.defined() ? static_cast<float*>(addr(s)) : nullptr;
+  const auto *A = static_cast<uint8_t*>(addr(p.A)), *B = static_cast<uint8_t*>(addr(p.B));
+  const auto *sA = static_cast<float*>(addr(p.sA)), *sB = static_cast<float*>(addr(p.sB));
+  if (p.offsets != nullptr) {
+    ok(fp8blk_grouped_gated_gemm_fp8_blockscaled(p.G, static_cast<int32_t*>(addr(p.offsets)), p.M, p.max_rows, H, p.K, A,
+                                                 p.lda, sA, B, p.ldb, p.strideB, p.opB, sB, p.stride_sB, p.act, bits(u),
+                                                 ldu, bits(h), ldh, qp, ldq, sp, flags, stream),
+       "grouped_gated_gemm_fp8_blockscaled");
+  } else {
+    const Tensor ws = room(w, split ? fp8blk_gated_gemm_workspace_bytes(p.M, H, p.K) : 0, *p.A);
+    ok(fp8blk_gated_gemm_fp8_blockscaled(p.M, H, p.K, A, p.lda, sA, B, p.ldb, p.opB, sB, p.act, bits(u), ldu, bits(h),
+                                         ldh, qp, ldq, sp, flags, split && ws.defined() ? addr(ws) : nullptr,
+                                         split && ws.defined() ? ws.nbytes() : 0, stream),
+       "gated_gemm_fp8_blockscaled");
+  }
+  unlocked.end();
+  return tuple({&u, &h, &q, &s});
+}
+
+// product's arguments, then u, quantize, pow2, want_h, want_du, split_k, workspace, du, h, q, s, stream
+PyObject* gated_gemm_backward(PyObject* const* a) {
+  const Product p = product(a);
+  a += 9;
+  const Tensor& u = given(a[0], "u");
+  const bool quantize = truth(a[1]), pow2 = truth(a[2]), want_h = truth(a[3]), want_du = truth(a[4]), split = truth(a[5]);
+  const Tensor *w = maybe(a[6], "workspace"), *od = maybe(a[7], "du"), *oh = maybe(a[8], "h"), *oq = maybe(a[9], "q");
+  const Tensor* os = maybe(a[10], "s");
+  if (!quantize && (oq != nullptr || os != nullptr)) value_error("q and s need quantize");
+  const int64_t H = p.N, ldu = pitch(u, at::kBFloat16, p.M, 2 * H, "u");
+  scratch(w);
+  void* stream = stream_of(a[11], *p.A, {p.offsets, p.sA, p.B, p.sB, &u, w, od, oh, oq, os});
+  Unlocked unlocked;
+  own({w, od, oh, oq, os});
+  int64_t lddu = 0, ldh = 0, ldq = 0;
+  Tensor du, h, q, s;
+  if (od != nullptr || want_du || !quantize) du = output(od, p.M, 2 * H, at::kBFloat16, *p.A, "du", lddu);
+  if (oh != nullptr || want_h) h = output(oh, p.M, H, at::kBFloat16, *p.A, "h", ldh);
+  if (quantize) quantized(p, 2 * H, oq, os, q, s, ldq);
+  const uint32_t flags = pow2 ? FP8BLK_SCALE_POW2 : 0;
+  auto* qp = q.defined() ? static_cast<uint8_t*>(addr(q)) : nullptr;
+  auto* sp = s.defined() ? static_cast<float*>(addr(s)) : nullptr;
+  const auto *A = static_cast<uint8_t*>(addr(p.A)), *B = static_cast<uint8_t*>(addr(p.B));
+  const auto *sA = static_cast<float*>(addr(p.sA)), *sB = static_cast<float*>(addr(p.sB));
+  if (p.offsets != nullptr) {
+    ok(fp8blk_grouped_gated_gemm_backward_fp8_blockscaled(
+           p.G, static_cast<int32_t*>(addr(p.offsets)), p.M, p.max_rows, H, p.K, A, p.lda, sA, B, p.ldb, p.strideB, p.opB,
+           sB, p.stride_sB, p.act, bits(u), ldu, bits(du), lddu, bits(h), ldh, qp, ldq, sp, flags, stream),
+       "grouped_gated_gemm_backward_fp8_blockscaled");
+  } else {
+    const Tensor ws = room(w, split ? fp8blk_gated_gemm_backward_workspace_bytes(p.M, H, p.K) : 0, *p.A);
+    ok(fp8blk_gated_gemm_backward_fp8_blockscaled(p.M, H, p.K, A, p.lda, sA, B, p.ldb, p.opB, sB, p.act, bits(u), ldu,
+                                                  bits(du), lddu, bits(h), ldh, qp, ldq, sp, flags,
+                                                  split && ws.defined() ? addr(ws) : nullptr,
+                                                  split && ws.defined() ? ws.nbytes() : 0, stream),
+       "gated_gemm_backward_fp8_blockscaled");
+  }
+  unlocked.end();
+  return tuple({&du, &h, &q, &s});
+}
 
 // --- AdamW -------------------------------------------------------------------
 
@@ -108,6 +260,8 @@ PyObject* adamw_step(PyObject* const* a) {
 
 }  // namespace
 
-PyMethodDef fp8blk_train_methods[] = {FP8BLK_METHOD(adamw_shared, 3),
+PyMethodDef fp8blk_train_methods[] = {FP8BLK_METHOD(gated_gemm, 20),
+                                      FP8BLK_METHOD(gated_gemm_backward, 21),
+                                      FP8BLK_METHOD(adamw_shared, 3),
                                       FP8BLK_METHOD(adamw_step, 14),
                                       {nullptr, nullptr, 0, nullptr}};

@@ -10,7 +10,7 @@ arguments, Fp8BlkError reports a failed call.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -23,6 +23,18 @@ _i64, _u32, _vp, _sz, _int, _f32 = (ctypes.c_int64, ctypes.c_uint32, ctypes.c_vo
 
 SIGNATURES = {
     "fp8blk_train_abi_version": (_int, []),
+    "fp8blk_gated_gemm_fp8_blockscaled": (_int, [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _int, _vp, _int, _vp, _i64,
+                                                 _vp, _i64, _vp, _i64, _vp, _u32, _vp, _sz, _vp]),
+    "fp8blk_gated_gemm_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "fp8blk_grouped_gated_gemm_fp8_blockscaled": (_int, [_i64, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64,
+                                                         _int, _vp, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _u32,
+                                                         _vp]),
+    "fp8blk_gated_gemm_backward_fp8_blockscaled": (_int, [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _int, _vp, _int, _vp,
+                                                          _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _u32, _vp, _sz, _vp]),
+    "fp8blk_gated_gemm_backward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "fp8blk_grouped_gated_gemm_backward_fp8_blockscaled": (_int, [_i64, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp,
+                                                                  _i64, _i64, _int, _vp, _i64, _int, _vp, _i64, _vp, _i64,
+                                                                  _vp, _i64, _vp, _i64, _vp, _u32, _vp]),
     "fp8blk_adamw_table_bytes": (_sz, [_i64]),
     "fp8blk_adamw_table_build": (_int, [_vp, _i64, _int, _vp, _sz, _vp]),
     "fp8blk_adamw_step": (_int, [_vp, _i64, _i64, _int, _vp, _vp]),
@@ -35,6 +47,83 @@ _STATES = {torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2}
 
 def train_abi_version() -> int:
     return _fb.lib().fp8blk_train_abi_version()
+
+
+# --------------------------------------------------------------------------
+# the gated feed-forward block
+# --------------------------------------------------------------------------
+_ACTS = {"silu": 0, "gelu": 1}
+
+
+class GatedGemm(NamedTuple):
+    """u: the projections, kept for the gradient; h: act(gate) * up; (q, s): its 1x128 codes and scales."""
+    u: Optional[torch.Tensor]
+    h: Optional[torch.Tensor]
+    q: Optional[torch.Tensor]
+    s: Optional[torch.Tensor]
+
+
+class GatedGemmGrad(NamedTuple):
+    """du: gradient of u; (q, s): its 1x128 codes and scales; h: the forward's h again."""
+    du: Optional[torch.Tensor]
+    h: Optional[torch.Tensor]
+    q: Optional[torch.Tensor]
+    s: Optional[torch.Tensor]
+
+
+def _act(act: str) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)}, got {act!r}")
+    return _ACTS[act]
+
+
+def gated_gemm_fp8_blockscaled(A, sA, B, sB, act: str = "silu", opB: int = 0, pow2_scales: bool = False,
+                               quantize: bool = False, pow2: bool = False, want_h: bool = True, want_u: bool = True,
+                               split_k: bool = True, workspace=None, u=None, h=None, q=None, s=None) -> GatedGemm:
+    """Gate and up projection, activation and product in one GEMM: u = A B (A uint8 codes [M][K], B [K][2H]
+    for OP_N or [2H][K] for OP_T, its first H columns the gate's; scales, opB and pow2_scales as in
+    gemm_fp8_blockscaled), h = act(u[:, :H]) * u[:, H:] with act "silu" or "gelu" (tanh form).  Returns u
+    bf16 [M][2H] unless want_u is False, h bf16 [M][H], and with quantize (q uint8 [M][H], s float32
+    [H/128][M]) = quantize_1x128(h, pow2); want_h=False then leaves h out.  H and K are multiples of 128.
+    split_k: a product of few rows is split over the GPU, with a workspace allocated here unless given."""
+    return GatedGemm(*_ext().gated_gemm(None, A, sA, B, sB, _act(act), opB, pow2_scales, None, quantize, pow2, want_h,
+                                        want_u, split_k, workspace, u, h, q, s, _stream(A)))
+
+
+def grouped_gated_gemm_fp8_blockscaled(offsets, A, sA, B, sB, act: str = "silu", opB: int = 0,
+                                       max_group_rows: Optional[int] = None, pow2_scales: bool = False,
+                                       quantize: bool = False, pow2: bool = False, want_h: bool = True,
+                                       want_u: bool = True, u=None, h=None, q=None, s=None) -> GatedGemm:
+    """The same for the experts of a mixture: offsets int32 [G+1] on the device, B [G][K][2H] or [G][2H][K],
+    sB [G][...], as in grouped_gemm_fp8_blockscaled.  Rows past the last expert's are not written."""
+    if not isinstance(offsets, torch.Tensor):
+        raise TypeError("offsets must be a tensor")
+    return GatedGemm(*_ext().gated_gemm(offsets, A, sA, B, sB, _act(act), opB, pow2_scales, max_group_rows, quantize, pow2,
+                                        want_h, want_u, False, None, u, h, q, s, _stream(A)))
+
+
+def gated_gemm_backward_fp8_blockscaled(A, sA, B, sB, u, act: str = "silu", opB: int = 1, pow2_scales: bool = False,
+                                        quantize: bool = False, pow2: bool = False, want_h: bool = True,
+                                        want_du: bool = True, split_k: bool = True, workspace=None, du=None, h=None,
+                                        q=None, s=None) -> GatedGemmGrad:
+    """Gradient of h = act(u[:, :H]) * u[:, H:] and of the down projection that reads it, in one GEMM: dh = A B
+    with A the codes of the gradient of the projection's output [M][K] and B its weights, [H][K] as the
+    forward stored them (OP_T) or [K][H] (OP_N).  Returns du bf16 [M][2H] (du may be u, which it replaces), h
+    bf16 [M][H] again for the weights' gradient unless want_h is False, and with quantize (q uint8 [M][2H], s
+    float32 [2H/128][M]) = quantize_1x128(du, pow2); want_du=False then leaves du out."""
+    return GatedGemmGrad(*_ext().gated_gemm_backward(None, A, sA, B, sB, _act(act), opB, pow2_scales, None, u, quantize, pow2,
+                                                     want_h, want_du, split_k, workspace, du, h, q, s, _stream(A)))
+
+
+def grouped_gated_gemm_backward_fp8_blockscaled(offsets, A, sA, B, sB, u, act: str = "silu", opB: int = 1,
+                                                max_group_rows: Optional[int] = None, pow2_scales: bool = False,
+                                                quantize: bool = False, pow2: bool = False, want_h: bool = True,
+                                                want_du: bool = True, du=None, h=None, q=None, s=None) -> GatedGemmGrad:
+    """The same for the experts of a mixture (see grouped_gated_gemm_fp8_blockscaled)."""
+    if not isinstance(offsets, torch.Tensor):
+        raise TypeError("offsets must be a tensor")
+    return GatedGemmGrad(*_ext().gated_gemm_backward(offsets, A, sA, B, sB, _act(act), opB, pow2_scales, max_group_rows, u,
+                                                     quantize, pow2, want_h, want_du, False, None, du, h, q, s, _stream(A)))
 
 
 # --------------------------------------------------------------------------

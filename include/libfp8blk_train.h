@@ -30,6 +30,83 @@ extern "C" {
 int fp8blk_train_abi_version(void);
 
 /* ------------------------------------------------------------------------
+ * The gated feed-forward block: u = X W_up with the gate projection in W_up's
+ * first H columns and the up projection in its last H, h = act(u_g) * u_u, and
+ * what follows is a plain product of h with the down projection.
+ * H and K multiples of 128, M arbitrary.
+ *
+ * Definitions, from the FP32 products u and dh that fp8blk_gemm_fp8_blockscaled
+ * defines, all in FP32 and rounded for storage only:
+ *   act(g) = g p,  p = 1 / (1 + e^-z),
+ *     z = g (SILU) or (8/pi)^(1/2) (g + 0.044715 g^3) (GELU, its tanh form)
+ *   h = act(u_g) u_u
+ *   du_u = dh act(u_g),  du_g = dh u_u (p + g p (1 - p) dz/dg)
+ * and (q, s) = fp8blk_quantize_1x128 of h, or of du, as stored in BF16, with
+ * flags qflags, whether or not h or du itself is asked for.
+ *
+ * A product of few rows is split along K over the GPU and joined in a second
+ * launch if `workspace` (DEVICE, 16-byte aligned, contents irrelevant, not used
+ * by other work during the call) has the bytes that the call's _workspace_bytes
+ * gives; without it, one launch computes it all.  Either form gives the same
+ * bits on every run.
+ * ------------------------------------------------------------------------ */
+enum { FP8BLK_ACT_SILU = 0, FP8BLK_ACT_GELU = 1 };
+
+/*
+ * Both projections, the activation and the product.
+ *   A  [M][K] codes, sA [K/128][M]; B [K][2H] (FP8BLK_OP_N) or [2H][K]
+ *   (FP8BLK_OP_T), block scales; FP8BLK_GEMM_POW2_SCALES allowed in opB: as in
+ *   fp8blk_gemm_fp8_blockscaled with N = 2H.
+ *   u  [M][2H] BF16, pitch ldu, kept for the gradient, or NULL.
+ *   h  [M][H] BF16, pitch ldh, or NULL; q [M][H] codes, pitch ldq, with
+ *   s [H/128][M] FP32, or both NULL.  At least one of h and q is given.
+ *   FP8BLK_ERR_UNSUPPORTED for FP8BLK_OP_T where (H + 128) * ldb reaches 2^31.
+ */
+fp8blk_status_t fp8blk_gated_gemm_fp8_blockscaled(int64_t M, int64_t H, int64_t K, const uint8_t* A, int64_t lda,
+                                                  const float* sA, const uint8_t* B, int64_t ldb, int opB,
+                                                  const float* sB, int act, uint16_t* u, int64_t ldu, uint16_t* h,
+                                                  int64_t ldh, uint8_t* q, int64_t ldq, float* s, uint32_t qflags,
+                                                  void* workspace, size_t workspace_bytes, void* stream);
+size_t fp8blk_gated_gemm_workspace_bytes(int64_t M, int64_t H, int64_t K);
+
+/*
+ * The same for every expert's rows: group_offsets, M_total, max_group_rows,
+ * strideB and stride_sB as in fp8blk_grouped_gemm_fp8_blockscaled; s
+ * [H/128][M_total].  Rows from group_offsets[G] on are not written.
+ */
+fp8blk_status_t fp8blk_grouped_gated_gemm_fp8_blockscaled(
+    int64_t G, const int32_t* group_offsets, int64_t M_total, int64_t max_group_rows, int64_t H, int64_t K,
+    const uint8_t* A, int64_t lda, const float* sA, const uint8_t* B, int64_t ldb, int64_t strideB, int opB,
+    const float* sB, int64_t stride_sB, int act, uint16_t* u, int64_t ldu, uint16_t* h, int64_t ldh, uint8_t* q,
+    int64_t ldq, float* s, uint32_t qflags, void* stream);
+
+/*
+ * The gradient: the down projection's input gradient dh = dO W_down^T, and the
+ * activation's from it.
+ *   A  [M][K] codes of dO, sA [K/128][M].
+ *   B  W_down, [H][K] (FP8BLK_OP_T: as the forward's product h W_down reads it
+ *      with FP8BLK_OP_N) or [K][H] (FP8BLK_OP_N), block scales.
+ *   u  [M][2H] BF16 that the forward kept.
+ *   du [M][2H] BF16, pitch lddu, or NULL; it may be u itself (same pitch).
+ *   h  [M][H] BF16, h again for the down projection's weight gradient, or NULL.
+ *   q  [M][2H] codes of du, what the up projection's gradients read, with
+ *      s [2H/128][M], or both NULL.  At least one of du and q is given.
+ */
+fp8blk_status_t fp8blk_gated_gemm_backward_fp8_blockscaled(
+    int64_t M, int64_t H, int64_t K, const uint8_t* A, int64_t lda, const float* sA, const uint8_t* B, int64_t ldb,
+    int opB, const float* sB, int act, const uint16_t* u, int64_t ldu, uint16_t* du, int64_t lddu, uint16_t* h,
+    int64_t ldh, uint8_t* q, int64_t ldq, float* s, uint32_t qflags, void* workspace, size_t workspace_bytes,
+    void* stream);
+size_t fp8blk_gated_gemm_backward_workspace_bytes(int64_t M, int64_t H, int64_t K);
+
+/* The same for every expert's rows; rows from group_offsets[G] on are neither read nor written. */
+fp8blk_status_t fp8blk_grouped_gated_gemm_backward_fp8_blockscaled(
+    int64_t G, const int32_t* group_offsets, int64_t M_total, int64_t max_group_rows, int64_t H, int64_t K,
+    const uint8_t* A, int64_t lda, const float* sA, const uint8_t* B, int64_t ldb, int64_t strideB, int opB,
+    const float* sB, int64_t stride_sB, int act, const uint16_t* u, int64_t ldu, uint16_t* du, int64_t lddu,
+    uint16_t* h, int64_t ldh, uint8_t* q, int64_t ldq, float* s, uint32_t qflags, void* stream);
+
+/* ------------------------------------------------------------------------
  * AdamW over many tensors.  For every element, t steps taken with this one:
  *   g = grad * c,  c = min(1, max_norm / (*norm + clip_eps))   (c = 1 without norm)
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2

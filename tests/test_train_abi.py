@@ -182,3 +182,83 @@ def test_lists_that_share_memory():
     g2 = [_t(128), _t(128)]
     assert _shared(p, g2, **kw, m_scales=[sc[:1], sc[1:2]], v_scales=[sc[2:3], sc[3:]]) is None
     assert "scales" in _shared(p, g2, **kw, m_scales=[sc[:1], sc[1:2]], v_scales=[sc[1:2], sc[3:]])
+
+
+# --- the gated feed-forward block --------------------------------------------
+
+def _gated(M=4, H=256, K=384, A=FAKE, lda=384, sA=FAKE, B=FAKE, ldb=512, opB=0, sB=FAKE, act=0, u=FAKE, ldu=512, h=FAKE,
+           ldh=256, q=NULL, ldq=0, s=NULL, qflags=0):
+    return fb.lib().fp8blk_gated_gemm_fp8_blockscaled(M, H, K, A, lda, sA, B, ldb, opB, sB, act, u, ldu, h, ldh, q, ldq, s,
+                                                      qflags, NULL, 0, NULL)
+
+
+def _gated_grad(M=4, H=256, K=384, A=FAKE, lda=384, sA=FAKE, B=FAKE, ldb=384, opB=1, sB=FAKE, act=0, u=FAKE, ldu=512,
+                du=P(0x200000), lddu=512, h=FAKE, ldh=256, q=NULL, ldq=0, s=NULL, qflags=0):
+    return fb.lib().fp8blk_gated_gemm_backward_fp8_blockscaled(M, H, K, A, lda, sA, B, ldb, opB, sB, act, u, ldu, du, lddu, h,
+                                                               ldh, q, ldq, s, qflags, NULL, 0, NULL)
+
+
+COMMON = [dict(M=-1), dict(H=-128), dict(K=-128), dict(H=100), dict(K=100), dict(K=0), dict(A=NULL), dict(A=MIS), dict(lda=368),
+          dict(lda=392), dict(sA=NULL), dict(sA=MIS), dict(B=NULL), dict(B=MIS), dict(ldb=368), dict(opB=2), dict(opB=0x200),
+          dict(sB=NULL), dict(sB=MIS), dict(act=2), dict(act=-1), dict(u=MIS), dict(ldu=504), dict(h=MIS), dict(ldh=248),
+          dict(ldh=260), dict(q=FAKE, ldq=512), dict(s=FAKE), dict(q=MIS, ldq=512, s=FAKE), dict(q=FAKE, ldq=504, s=FAKE),
+          dict(q=FAKE, ldq=512, s=MIS), dict(qflags=2)]
+
+
+def test_gated_refuses():
+    for bad in COMMON + [dict(h=NULL), dict(q=FAKE, ldq=240, s=FAKE)]:
+        assert _gated(**bad) == INVALID, bad
+    assert _gated(lda=2 ** 23) == UNSUPPORTED and _gated(ldb=2 ** 23) == UNSUPPORTED and _gated(M=2 ** 32) == UNSUPPORTED
+    assert _gated(H=2 ** 20, opB=1, ldb=2 ** 12, ldu=2 ** 21, ldh=2 ** 20) == UNSUPPORTED  # up rows past 2^31 bytes
+    assert _gated(M=0, A=NULL, sA=NULL) == OK and _gated(H=0, B=NULL, sB=NULL) == OK
+    w = fb.lib().fp8blk_gated_gemm_workspace_bytes
+    assert w(0, 256, 384) == 0 and w(16, 100, 384) == 0 and w(16, 256, 100) == 0 and w(-1, 256, 384) == 0
+    assert w(8192, 2048, 7168) == 0 and w(2 ** 62, 2 ** 62 - 2 ** 62 % 128, 128) == 0
+    assert w(16, 256, 384) >= 16 * 512 * 4 and w(16, 256, 384) % (16 * 512 * 4) == 0
+
+
+def test_gated_gradient_refuses():
+    for bad in COMMON + [dict(u=NULL), dict(du=NULL), dict(du=MIS), dict(lddu=504), dict(du=FAKE, lddu=520),
+                         dict(q=FAKE, ldq=496, s=FAKE)]:
+        assert _gated_grad(**bad) == INVALID, bad
+    assert _gated_grad(lda=2 ** 23) == UNSUPPORTED and _gated_grad(ldb=2 ** 23) == UNSUPPORTED
+    assert _gated_grad(M=0, A=NULL, sA=NULL, u=NULL) == OK and _gated_grad(H=0, B=NULL, sB=NULL) == OK
+    w = fb.lib().fp8blk_gated_gemm_backward_workspace_bytes
+    assert w(0, 256, 384) == 0 and w(8192, 4096, 7168) == 0 and w(16, 256, 384) % (16 * 256 * 4) == 0
+
+
+def test_grouped_gated_refuses():
+    def call(G=3, off=FAKE, M=4, most=0, strideB=384 * 512, opB=0, stride_sB=12, K=384, h=FAKE):
+        return fb.lib().fp8blk_grouped_gated_gemm_fp8_blockscaled(G, off, M, most, 256, K, FAKE, 384, FAKE, FAKE, 512, strideB,
+                                                                  opB, FAKE, stride_sB, 0, FAKE, 512, h, 256, NULL, 0, NULL,
+                                                                  0, NULL)
+
+    def grad(G=3, off=FAKE, M=4, most=0, strideB=384 * 256, opB=1, stride_sB=6, du=P(0x200000)):
+        return fb.lib().fp8blk_grouped_gated_gemm_backward_fp8_blockscaled(
+            G, off, M, most, 256, 384, FAKE, 384, FAKE, FAKE, 384, strideB, opB, FAKE, stride_sB, 0, FAKE, 512, du, 512, NULL,
+            0, NULL, 0, NULL, 0, NULL)
+
+    for f in (call, grad):
+        for bad in (dict(G=-1), dict(off=NULL), dict(off=MIS), dict(M=-1), dict(most=-1), dict(strideB=100), dict(stride_sB=5),
+                    dict(opB=7)):
+            assert f(**bad) == INVALID, (f, bad)
+        assert f(G=0) == OK and f(M=0) == OK
+        assert f(G=2 ** 40) == UNSUPPORTED
+    assert call(strideB=384 * 512 + 8) == INVALID and call(h=NULL) == INVALID and call(K=128 * 4) == INVALID
+    assert grad(du=NULL) == INVALID
+
+
+X = torch.zeros(4, 128, dtype=torch.uint8)
+S = torch.zeros(1, 4)
+
+
+@pytest.mark.parametrize("name,call", [
+    ("A", lambda v: fb.gated_gemm_fp8_blockscaled(v, S, X, S)), ("sA", lambda v: fb.gated_gemm_fp8_blockscaled(X, v, X, S)),
+    ("B", lambda v: fb.gated_gemm_fp8_blockscaled(X, S, v, S)), ("sB", lambda v: fb.gated_gemm_fp8_blockscaled(X, S, X, v)),
+    ("offsets", lambda v: fb.grouped_gated_gemm_fp8_blockscaled(v, X, S, X, S)),
+    ("offsets", lambda v: fb.grouped_gated_gemm_backward_fp8_blockscaled(v, X, S, X, S, X)),
+    ("u", lambda v: fb.gated_gemm_backward_fp8_blockscaled(X, S, torch.zeros(128, 128, dtype=torch.uint8), torch.zeros(1, 1), v))])
+@pytest.mark.parametrize("value", [None, 3, [[1.0]], X.numpy()])
+def test_no_tensor(name, call, value):
+    with pytest.raises(TypeError, match=f"^{name} must be a tensor"):
+        call(value)

@@ -99,3 +99,54 @@ def drop(x, bits, r):
     w = np.asarray(x, np.float32).view(np.uint32).astype(np.int64)
     w = ((w + r) >> bits) << bits
     return (w & M32).astype(np.uint32).view(np.float32)
+
+
+# --- the gated feed-forward block ------------------------------------------
+
+def _sigmoid(z):
+    e = np.exp(-np.abs(z))
+    return np.where(z >= 0, 1 / (1 + e), e / (1 + e))
+
+
+def act(g, kind):
+    """(z, dz/dg) of act(g) = g sigmoid(z)."""
+    if kind == "silu":
+        return g, np.ones_like(g)
+    k = np.sqrt(8 / np.pi)
+    return k * (g + 0.044715 * g ** 3), k * (1 + 3 * 0.044715 * g ** 2)
+
+
+def _sigmoid_bound(z, p):
+    """FP32 error of p: z is off by at most 6 U of itself (GELU: five operations and a constant), its product with
+    log2 e and that constant by 2 U more, each of which e^-z multiplies by |z|; 2^x one unit in the last place (2 U),
+    the sum U, the reciprocal 2 U.  Below 2^-126 it may be zero."""
+    return p * U * ((1 - p) * (8 * np.abs(z) + 2) + 4) + 2.0 ** -125
+
+
+def gated(g, v, kind):
+    """(h, FP32 error bound) in FP64."""
+    z, _ = act(g, kind)
+    p = _sigmoid(z)
+    h = g * p * v
+    return h, np.abs(g * v) * _sigmoid_bound(z, p) + 3 * U * np.abs(h) + 2.0 ** -140
+
+
+def gated_slope(g, v, kind, eg, ev):
+    """How far h moves when g and v are off by eg and ev: |act'| <= 1.13, |act| <= |g|."""
+    return 1.13 * np.abs(v) * eg + np.abs(g) * ev + 1.13 * eg * ev
+
+
+def gated_grad(dh, g, v, kind):
+    """{name: (value, FP32 error bound)} for dg, dv and h in FP64."""
+    z, dz = act(g, kind)
+    p = _sigmoid(z)
+    ep = _sigmoid_bound(z, p)
+    a, q = g * p, 1 - p
+    ea = np.abs(g) * ep + U * np.abs(a)
+    t = a * q
+    et = ea * q + np.abs(a) * (ep + U * q) + U * np.abs(t)
+    slope = t * dz + p
+    es = et * np.abs(dz) + 5 * U * np.abs(t * dz) + ep + U * np.abs(slope)
+    h, eh = gated(g, v, kind)
+    return {"dg": (dh * v * slope, np.abs(dh * v) * es + 3 * U * np.abs(dh * v * slope) + 2.0 ** -140),
+            "dv": (dh * a, np.abs(dh) * ea + 2 * U * np.abs(dh * a) + 2.0 ** -140), "h": (h, eh)}
