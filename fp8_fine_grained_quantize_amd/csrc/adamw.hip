@@ -18,6 +18,7 @@
 // program of elementary FP32 operations takes them: a value that differs in its
 // last bit can fall to another E4M3 code, 6 to 12 % away, so that only equal
 // operations give equal codes.
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/libfp8blk_train.h"
@@ -26,9 +27,6 @@
 #include "tensor_table.h"
 
 namespace fp8blk {
-
-constexpr int kAdamBlocks = 2048;  // most workgroups
-constexpr int kAdamUnroll = 2;     // groups of four values a lane has in flight
 
 struct AdamEntry {
   void* p;
@@ -186,9 +184,16 @@ struct AdamRange {
   bool random;
 
   __device__ __forceinline__ Quad<TP, TG, ST> load(int64_t i, int count, Lie lie) const {
+    // FP32 moments of large tables: a wave reads one tensor after another.  Four
+    // reads and four writes at the same place of as many tensors, from every
+    // wave at once, is what memory does worst: 0.94e9 values 4.83 ms at once, 4.54
+    // in turn.  With E4M3 moments the waits cost more than that: 3.12 / 3.50.
+    constexpr bool TURNS = NT && ST == FP8BLK_ADAMW_F32;
     Quad<TP, TG, ST> q{};
     q.p = load4<NT>((const TP*)e.p, i, count, lie, e.cols, e.ldp);
+    if (TURNS) wait_vmem();
     q.g = load4<NT>((const TG*)e.g, i, count, lie, e.cols, e.ldg);
+    if (TURNS) wait_vmem();
     if constexpr (ST == FP8BLK_ADAMW_E4M3) {
       const Global<const uint8_t> *m = global((const uint8_t*)e.m + i), *v = global((const uint8_t*)e.v + i);
       if (count == 4) {
@@ -208,6 +213,7 @@ struct AdamRange {
       }
     } else {
       q.m = load4<NT>((const TM*)e.m, i, count, DENSE, 0, 0);
+      if (TURNS) wait_vmem();
       q.v = load4<NT>((const TM*)e.v, i, count, DENSE, 0, 0);
     }
     return q;
@@ -282,18 +288,21 @@ struct AdamRange {
     store4<NT>((TP*)e.p, p, i, count, lie, e.cols, e.ldp);
   }
 
-  // The elements [lo, hi); lo is a multiple of kChunk, hi too unless the tensor ends there.
+  // The elements [lo, hi); lo is a multiple of kChunk, hi too unless the tensor
+  // ends there.  A chunk's loads go out before the stores of the one before: one
+  // counter counts both, so that loads behind stores would wait for them.
   __device__ __forceinline__ void run(int64_t lo, int64_t hi) const {
     const int64_t mine = (int64_t)threadIdx.x * 4;
     int64_t base = lo;
-    if (!e.pitched) {
-      for (; base + kChunk * kAdamUnroll <= hi; base += kChunk * kAdamUnroll) {
-        Quad<TP, TG, ST> q[kAdamUnroll];
-#pragma unroll
-        for (int u = 0; u < kAdamUnroll; ++u) q[u] = load(base + u * kChunk + mine, 4, DENSE);
-#pragma unroll
-        for (int u = 0; u < kAdamUnroll; ++u) finish(q[u], base + u * kChunk + mine, 4, DENSE);
+    if (!e.pitched && base + kChunk <= hi) {
+      Quad<TP, TG, ST> q = load(base + mine, 4, DENSE);
+      for (; base + 2 * kChunk <= hi; base += kChunk) {
+        const Quad<TP, TG, ST> next = load(base + kChunk + mine, 4, DENSE);
+        finish(q, base + mine, 4, DENSE);
+        q = next;
       }
+      finish(q, base + mine, 4, DENSE);
+      base += kChunk;
     }
     const Lie lie = !e.pitched ? DENSE : (e.cols & 3) == 0 ? ROW : ROWS;
     for (; base < hi; base += kChunk) {
@@ -339,8 +348,22 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamEntry* __restrict__ tab
   }
 }
 
-// Streamed loads and stores (see kStreamBytes in layer_host.h) from 2^23 elements on.
-inline bool adam_stream(int64_t chunks) { return chunks >= ((int64_t)1 << 23) / kChunk; }
+// Streamed loads and stores (see kStreamBytes in layer_host.h) from 2^25 elements
+// on: with FP32 throughout 16e6 elements took 72 us streamed and 66 not, 0.94e9
+// 4.9 and 5.2 ms; with BF16 throughout 60e6 149 and 158 us.
+inline bool adam_stream(int64_t chunks) { return chunks >= ((int64_t)1 << 25) / kChunk; }
+
+// Chunks of a workgroup.  Short runs keep the waves' places in memory close
+// together: 0.94e9 values with FP32 moments 4.83 / 5.06 / 5.06 ms with 1 / 2 / 4
+// chunks each (persistent workgroups 5.4 and more); with E4M3 moments a chunk's
+// time no longer covers the search of the table: 4.19 / 3.28 / 3.12 (8: 3.15), and
+// 60e6 values in BF16 213 / 165 / 149 us (8: 160).
+inline int64_t adam_run(int state, int64_t chunks) {
+  return state == FP8BLK_ADAMW_F32 ? 1 : std::clamp<int64_t>(chunks / 4096, 1, 4);
+}
+// LDS that a workgroup of streamed FP32 moments asks for and does not use: five
+// of them to a compute unit instead of six took 4.55 ms, six 4.71, four 4.76.
+constexpr unsigned kAdamRoom = 32000;
 
 inline bool state_ok(int state) {
   return state == FP8BLK_ADAMW_F32 || state == FP8BLK_ADAMW_BF16 || state == FP8BLK_ADAMW_E4M3;
@@ -434,11 +457,13 @@ extern "C" fp8blk_status_t fp8blk_adamw_step(const void* table, int64_t n, int64
     a.root = 1.0f / (float)sqrt(1.0 - pow(s->beta2, (double)s->step));
   }
   a.seed = s->seed;
-  const dim3 grid((unsigned)(chunks < kAdamBlocks ? chunks : kAdamBlocks)), block(256);
+  // A launch counts its lanes in 32 bits.
+  const dim3 grid((unsigned)std::min<int64_t>(ceil_div(chunks, adam_run(state, chunks)), 0xFFFFFF)), block(256);
   const AdamEntry* tab = reinterpret_cast<const AdamEntry*>(table);
   const bool random = s->flags & FP8BLK_ADAMW_RANDOM, nt = adam_stream(chunks);
+  const unsigned room = nt && state == FP8BLK_ADAMW_F32 ? kAdamRoom : 0;
 #define FP8BLK_ADAMW_LAUNCH(ST_)                                                                                    \
-  hipLaunchKernelGGL((nt ? k_adamw<ST_, true> : k_adamw<ST_, false>), grid, block, 0, as_stream(stream), tab, n, chunks, \
+  hipLaunchKernelGGL((nt ? k_adamw<ST_, true> : k_adamw<ST_, false>), grid, block, room, as_stream(stream), tab, n, chunks, \
                      a, random)
   if (state == FP8BLK_ADAMW_F32) FP8BLK_ADAMW_LAUNCH(FP8BLK_ADAMW_F32);
   else if (state == FP8BLK_ADAMW_BF16) FP8BLK_ADAMW_LAUNCH(FP8BLK_ADAMW_BF16);

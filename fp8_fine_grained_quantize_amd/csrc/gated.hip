@@ -400,108 +400,324 @@ __global__ __launch_bounds__(CFG::NT) void k_gated_gemm_backward(GatedArgs a, Ga
                                                                    GatedGradStore<CFG>{o});
 }
 
-// --- few rows: the product split over K, joined with the activation ----------
+// --- tiles of fewer rows --------------------------------------------------------
+// With fewer than 256 rows a K group is worked on in less time than its
+// successor needs to arrive, so these tiles keep three or four LDS stages, all
+// but one of them on their way.  The matrix cores wait anyhow: power-of-two
+// scales take the same path (the scaled product is exact, and so the sum is the
+// MFMA's own).
+template <class CFG_, int STAGES_>
+struct Deep {
+  using CFG = CFG_;
+  static constexpr int STAGES = STAGES_;
+  uint8_t ops[STAGES][CFG::BUF_BYTES];
+  float sc[STAGES][CFG::SC_FLOATS];
+  static_assert(STAGES * (CFG::BUF_BYTES + CFG::SC_FLOATS * 4) <= 160 * 1024, "LDS capacity");
+};
+using MidDeep = Deep<TileCfg<2, 4, 4, 4>, 3>;  // 128 x 256, 49 KB a stage
+using LowDeep = Deep<TileCfg<2, 4, 2, 4>, 3>;  // 64 x 256, 41 KB
+using FewDeep = Deep<TileCfg<1, 8, 2, 2>, 4>;  // 32 x 256, 37 KB
+
+// All but the newest `groups` of at most MOST groups of L copies each have landed.
+template <int MOST, int L>
+__device__ __forceinline__ void wait_groups(int groups) {
+  if constexpr (MOST == 0) {
+    wait_vmcnt<0>();
+  } else {
+    if (groups >= MOST) wait_vmcnt<MOST * L>();
+    else wait_groups<MOST - 1, L>(groups);
+  }
+}
+
+template <class D, bool OPB_T, bool GATED>
+__device__ __forceinline__ void deep_loop(const TileArgs& t, D& lds, v4f (&acc)[D::CFG::TM][D::CFG::TN]) {
+  using CFG = typename D::CFG;
+  using Plan = CopyPlan<CFG, OPB_T, false, GATED>;
+  constexpr int TM = CFG::TM, TN = CFG::TN, ST = D::STAGES;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, lq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / CFG::WAVES_N, wn = wave % CFG::WAVES_N;
+  const int blk = wave < CFG::S_BLOCKS ? wave : 0;
+  // Whether this wave copies rows of A (a partial copy iteration: only where it has valid rows).
+  const bool with_a = !CFG::A_PARTIAL || (int)t.rows > wave * 8;
+  static_assert(!CFG::A_PARTIAL || CFG::A_ITERS == 1, "the copies of a wave are counted");
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  Plan plan;
+  plan.init(t);
+  const uint32_t scoff = plan.sc_offset(t);
+  GroupCursor<CFG, OPB_T, false, GATED> cur;
+  cur.init(t, t.g0, blk * 64 < CFG::BMP);
+  int into = 0;  // the stage of the next group to copy
+  auto issue = [&]() {
+    issue_copies<CFG, OPB_T, false, false, GATED>(t, plan, scoff, cur.ra(true), cur.rb(true), cur.rs(true), 0, Plan::LOADS,
+                                                  lds.ops[into], lds.sc[into], wave, blk);
+    cur.advance();
+    into = into + 1 < ST ? into + 1 : 0;
+  };
+  const int groups = t.g1 - t.g0;
+  for (int g = 0; g < groups && g < ST; ++g) issue();
+  int from = 0;
+  for (int g = 0; g < groups; ++g) {
+    // Groups g + 1 .. are still on their way: ST - 1 of them at first, then one fewer, as a
+    // stage is filled again only once every wave has left it.
+    const int newer = min(groups - 1 - g, g == 0 ? ST - 1 : ST - 2);
+    if (with_a) wait_groups<ST - 1, Plan::LOADS>(newer);
+    else wait_groups<ST - 1, Plan::LOADS - 1>(newer);
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    if (g > 0 && g + ST - 1 < groups) issue();
+    const uint8_t *As = lds.ops[from], *Bs = As + CFG::A_BYTES;
+    const float* sc = lds.sc[from];
+    from = from + 1 < ST ? from + 1 : 0;
+    auto kmaj = [&](const uint8_t* base, int r) {
+      const uint4 lo = *reinterpret_cast<const uint4*>(base + kmaj_off(r, 2 * lq));
+      const uint4 hi = *reinterpret_cast<const uint4*>(base + kmaj_off(r, 2 * lq + 1));
+      return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+    v8i bf[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int ncol = wn * CFG::WTN + 16 * j;
+      if (OPB_T) {
+        bf[j] = kmaj(Bs, ncol + l16);
+      } else {
+        v2i part[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          part[r] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (lds_v2i*)(Bs + nmaj_off<CFG::BN>(32 * lq + 8 * r + (l16 >> 1), ncol >> 4) + 8 * (l16 & 1)));
+        bf[j] = v8i{part[0][0], part[0][1], part[1][0], part[1][1], part[2][0], part[2][1], part[3][0], part[3][1]};
+      }
+    }
+    const float4 sa4 = *reinterpret_cast<const float4*>(sc + wm * CFG::WTMP + l16 * CFG::TMP);
+    static_assert(TM <= 4, "four row scales");
+    const float sa[4] = {sa4.x, sa4.y, sa4.z, sa4.w};
+    const int block = wn * CFG::WTN / 128;
+    const float sb[2] = {sc[CFG::BMP + (GATED ? 0 : block)], sc[CFG::BMP + (GATED ? 1 : block)]};
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const v8i af = kmaj(As, wm * CFG::WTM + 16 * i + l16);
+      v4f p[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        p[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af, v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 127, 0, 127);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const float f = sa[i] * sb[j < TN / 2 ? 0 : 1];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[j][r], f, acc[i][j][r]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+template <class D, bool GROUPED, bool OPB_T>
+__global__ __launch_bounds__(D::CFG::NT) void k_gated_gemm_deep(GatedArgs a, GatedOut o) {
+  __shared__ __align__(16) D lds;
+  TileArgs t;
+  if (!gated_tile<typename D::CFG, GROUPED, true>(a, t)) return;
+  v4f acc[D::CFG::TM][D::CFG::TN];
+  deep_loop<D, OPB_T, true>(t, lds, acc);
+  GatedStore<typename D::CFG>{o}(t, acc, lds.ops[0]);
+}
+
+template <class D, bool GROUPED, bool OPB_T>
+__global__ __launch_bounds__(D::CFG::NT) void k_gated_gemm_backward_deep(GatedArgs a, GatedGradOut o) {
+  __shared__ __align__(16) D lds;
+  TileArgs t;
+  if (!gated_tile<typename D::CFG, GROUPED, false>(a, t)) return;
+  v4f acc[D::CFG::TM][D::CFG::TN];
+  deep_loop<D, OPB_T, false>(t, lds, acc);
+  GatedGradStore<typename D::CFG>{o}(t, acc, lds.ops[0]);
+}
 
 // FP32 partial products [split][M][N] of K groups [split * per, ...).
-template <class CFG, bool OPB_T, bool P2>
-__global__ __launch_bounds__(CFG::NT) void k_gated_partial(GatedArgs a, float* __restrict__ partials, int per) {
-  FP8BLK_DECLARE_STAGES(CFG);
+template <class D, bool OPB_T, bool GATED>
+__global__ __launch_bounds__(D::CFG::NT) void k_gated_partial(GatedArgs a, float* __restrict__ partials, int per) {
+  using CFG = typename D::CFG;
+  __shared__ __align__(16) D lds;
   TileArgs t;
-  gated_tile<CFG, false, false>(a, t);
+  gated_tile<CFG, false, GATED>(a, t);
   t.g0 = blockIdx.y * per;
   t.g1 = min(t.g0 + per, (int)(a.K / 128));
-  t.C = partials + ((int64_t)blockIdx.y * a.M + t.m0) * a.N;
-  t.ldc = a.N;
-  gemm_tile<CFG, OPB_T, false, P2, OUT_F32>(t, s_ops0, s_ops1, s_sc0, s_sc1);
-}
-
-// Eight columns of a row: their sum over the S partial products, in order.
-__device__ __forceinline__ void join8(const float* __restrict__ p, int S, int64_t step, float (&x)[8]) {
-  float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  for (int s = 1; s < S; ++s) {
-    const float4 c = reinterpret_cast<const float4*>(p + s * step)[0], d = reinterpret_cast<const float4*>(p + s * step)[1];
-    a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
-    b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
-  }
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(bf16_pack(x[0], x[1]), bf16_pack(x[2], x[3]), bf16_pack(x[4], x[5]), bf16_pack(x[6], x[7]));
-}
-// The codes of eight values of a tile that 16 lanes hold, and its scale.
-__device__ __forceinline__ void put_codes(const uint4& w, bool pow2, uint8_t* q, float* s) {
-  const uint32_t m = row16_max(abs_max_bits(abs_max_bits(abs_max_bits(abs_max_bits(0, w.x), w.y), w.z), w.w));
-  const uint32_t p[4] = {w.x, w.y, w.z, w.w};
-  uint32_t c[2];
-  float scale;
-  if (pow2) encode_bf16<true>(p, m, c, scale);
-  else encode_bf16<false>(p, m, c, scale);
-  *reinterpret_cast<uint2*>(q) = make_uint2(c[0], c[1]);
-  if ((threadIdx.x & 15) == 0) *s = scale;
-}
-
-// A lane has eight columns of h, 16 lanes a scale group; M * H / 8 lanes, a
-// multiple of 16, in workgroups of 256.
-__global__ __launch_bounds__(256) void k_gated_join(const float* __restrict__ partials, int S, int64_t M, int64_t H,
-                                                     GatedOut o) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t m = at / (H / 8), c = at % (H / 8) * 8;
-  if (m >= M) return;
-  float g[8], v[8], x[8];
-  const float* p = partials + m * 2 * H + c;
-  join8(p, S, M * 2 * H, g);
-  join8(p + H, S, M * 2 * H, v);
-  if (o.u != nullptr) {
-    *reinterpret_cast<uint4*>(o.u + m * o.ldu + c) = pack8(g);
-    *reinterpret_cast<uint4*>(o.u + m * o.ldu + H + c) = pack8(v);
-  }
+  v4f acc[CFG::TM][CFG::TN];
+  deep_loop<D, OPB_T, GATED>(t, lds, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, lq = lane >> 4;
+  const int wm = wave / CFG::WAVES_N, wn = wave % CFG::WAVES_N;
+  float* out = partials + ((int64_t)blockIdx.y * a.M + t.m0) * a.N;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = o.gelu ? gated<true>(g[j], v[j]) : gated<false>(g[j], v[j]);
-  const uint4 w = pack8(x);
-  if (o.h != nullptr) *reinterpret_cast<uint4*>(o.h + m * o.ldh + c) = w;
+  for (int i = 0; i < CFG::TM; ++i) {
+    const int64_t row = wm * CFG::WTM + 16 * i + l16;
+    if (row >= t.rows) continue;
+#pragma unroll
+    for (int j = 0; j < CFG::TN; ++j) {
+      const int c = wn * CFG::WTN + 16 * j;
+      const int64_t col = t.n0 + (GATED ? gated_column<CFG>(c, t.H) : c) + 4 * lq;
+      if (col < t.N) *reinterpret_cast<v4f*>(out + row * t.N + col) = acc[i][j];
+    }
+  }
+}
+
+// --- the join of partial products -------------------------------------------
+// A lane has four columns of h, 32 lanes a scale group of one row, and SLICES
+// times 32 lanes share its partial products: slice k adds k, k + SLICES, ..,
+// in that order, and the first slice adds the slices' sums.  With many parts
+// each lane loads few of them (16 parts in one lane, unrolled, took 7 us for
+// 128 columns of one row, most of it fetching the instructions; 8 slices 4).
+template <int SLICES>
+struct Join {
+  int64_t m, c;  // row, first column
+  bool first;    // whether this lane holds the sums in the end
+  int slice;
+  __device__ __forceinline__ Join(int64_t H) {
+    slice = SLICES > 1 ? (int)threadIdx.x >> 5 : 0;
+    const int64_t at = SLICES > 1 ? (int64_t)blockIdx.x * 32 + (threadIdx.x & 31) : (int64_t)blockIdx.x * 64 + threadIdx.x;
+    m = (int64_t)((uint32_t)at / (uint32_t)(H / 4));  // fewer than 2^31 lanes: few rows
+    c = (int64_t)((uint32_t)at % (uint32_t)(H / 4)) * 4;
+    first = slice == 0;
+  }
+  // The sums of N columns' parts at p, p + other.
+  template <int N>
+  __device__ __forceinline__ void sum(const float* __restrict__ p, int64_t other, int S, int64_t step, v4f (&x)[N]) const {
+    __shared__ v4f part[N][SLICES][32];
+#pragma unroll
+    for (int n = 0; n < N; ++n) x[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int s = slice; s < S; s += SLICES)
+#pragma unroll
+      for (int n = 0; n < N; ++n) x[n] += *reinterpret_cast<const v4f*>(p + s * step + n * other);
+    if (SLICES == 1) return;
+#pragma unroll
+    for (int n = 0; n < N; ++n) part[n][slice][threadIdx.x & 31] = x[n];
+    __syncthreads();
+    if (!first) return;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int k = 1; k < SLICES; ++k) x[n] += part[n][k][threadIdx.x & 31];
+  }
+};
+// The codes of four values of a tile that 32 lanes hold, and its scale.
+__device__ __forceinline__ void put_codes(uint2 w, bool pow2, uint8_t* q, float* s) {
+  const uint32_t m = row16_max(abs_max_bits(abs_max_bits(0, w.x), w.y));
+  const auto o = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+  const uint32_t p[2] = {w.x, w.y};
+  uint32_t c[1];
+  float scale;
+  if (pow2) encode_bf16<true>(p, max(o[0], o[1]), c, scale);
+  else encode_bf16<false>(p, max(o[0], o[1]), c, scale);
+  *reinterpret_cast<uint32_t*>(q) = c[0];
+  if ((threadIdx.x & 31) == 0) *s = scale;
+}
+__device__ __forceinline__ uint2 pack4(const float (&x)[4]) { return make_uint2(bf16_pack(x[0], x[1]), bf16_pack(x[2], x[3])); }
+
+template <int SLICES>
+__global__ __launch_bounds__(SLICES > 1 ? 32 * SLICES : 64) void k_gated_join(const float* __restrict__ partials, int S,
+                                                                              int64_t M, int64_t H, GatedOut o) {
+  const Join<SLICES> j(H);
+  const int64_t m = j.m, c = j.c;
+  if (m >= M) return;
+  v4f u[2];
+  j.template sum<2>(partials + m * 2 * H + c, H, S, M * 2 * H, u);
+  if (!j.first) return;
+  const v4f g = u[0], v = u[1];
+  if (o.u != nullptr) {
+    *reinterpret_cast<uint2*>(o.u + m * o.ldu + c) = make_uint2(bf16_pack(g[0], g[1]), bf16_pack(g[2], g[3]));
+    *reinterpret_cast<uint2*>(o.u + m * o.ldu + H + c) = make_uint2(bf16_pack(v[0], v[1]), bf16_pack(v[2], v[3]));
+  }
+  float x[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = o.gelu ? gated<true>(g[k], v[k]) : gated<false>(g[k], v[k]);
+  const uint2 w = pack4(x);
+  if (o.h != nullptr) *reinterpret_cast<uint2*>(o.h + m * o.ldh + c) = w;
   if (o.q != nullptr) put_codes(w, o.pow2, o.q + m * o.ldq + c, o.s + (c >> 7) * o.s_ld + m);
 }
 
-__global__ __launch_bounds__(256) void k_gated_join_backward(const float* __restrict__ partials, int S, int64_t M,
-                                                              int64_t H, GatedGradOut o) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t m = at / (H / 8), c = at % (H / 8) * 8;
+template <int SLICES>
+__global__ __launch_bounds__(SLICES > 1 ? 32 * SLICES : 64) void k_gated_join_backward(const float* __restrict__ partials,
+                                                                                       int S, int64_t M, int64_t H,
+                                                                                       GatedGradOut o) {
+  const Join<SLICES> j(H);
+  const int64_t m = j.m, c = j.c;
   if (m >= M) return;
-  const uint4 ug = *reinterpret_cast<const uint4*>(o.u + m * o.ldu + c);
-  const uint4 uv = *reinterpret_cast<const uint4*>(o.u + m * o.ldu + H + c);
-  float dh[8], dg[8], dv[8], h[8];
-  join8(partials + m * H + c, S, M * H, dh);
-  const uint32_t g[4] = {ug.x, ug.y, ug.z, ug.w}, v[4] = {uv.x, uv.y, uv.z, uv.w};
+  const uint2 ug = *reinterpret_cast<const uint2*>(o.u + m * o.ldu + c);
+  const uint2 uv = *reinterpret_cast<const uint2*>(o.u + m * o.ldu + H + c);
+  v4f d[1];
+  j.template sum<1>(partials + m * H + c, 0, S, M * H, d);
+  if (!j.first) return;
+  const float g[4] = {bf16_lo(ug.x), bf16_hi(ug.x), bf16_lo(ug.y), bf16_hi(ug.y)};
+  const float v[4] = {bf16_lo(uv.x), bf16_hi(uv.x), bf16_lo(uv.y), bf16_hi(uv.y)};
+  float dg[4], dv[4], h[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float gj = j & 1 ? bf16_hi(g[j >> 1]) : bf16_lo(g[j >> 1]), vj = j & 1 ? bf16_hi(v[j >> 1]) : bf16_lo(v[j >> 1]);
-    if (o.gelu) gated_grad<true>(dh[j], gj, vj, dg[j], dv[j], h[j]);
-    else gated_grad<false>(dh[j], gj, vj, dg[j], dv[j], h[j]);
+  for (int k = 0; k < 4; ++k) {
+    if (o.gelu) gated_grad<true>(d[0][k], g[k], v[k], dg[k], dv[k], h[k]);
+    else gated_grad<false>(d[0][k], g[k], v[k], dg[k], dv[k], h[k]);
   }
-  const uint4 wg = pack8(dg), wv = pack8(dv);
+  const uint2 wg = pack4(dg), wv = pack4(dv);
   if (o.du != nullptr) {
-    *reinterpret_cast<uint4*>(o.du + m * o.lddu + c) = wg;
-    *reinterpret_cast<uint4*>(o.du + m * o.lddu + H + c) = wv;
+    *reinterpret_cast<uint2*>(o.du + m * o.lddu + c) = wg;
+    *reinterpret_cast<uint2*>(o.du + m * o.lddu + H + c) = wv;
   }
-  if (o.h != nullptr) *reinterpret_cast<uint4*>(o.h + m * o.ldh + c) = pack8(h);
+  if (o.h != nullptr) *reinterpret_cast<uint2*>(o.h + m * o.ldh + c) = pack4(h);
   if (o.q != nullptr) {
     put_codes(wg, o.pow2, o.q + m * o.ldq + c, o.s + (c >> 7) * o.s_ld + m);
     put_codes(wv, o.pow2, o.q + m * o.ldq + H + c, o.s + ((H + c) >> 7) * o.s_ld + m);
   }
 }
 
-// Splits of K for a dense product of M rows and N columns of B, 0 where the
-// fused tiles of 256 x 256 are at least half as many as the compute units and
-// it is not split at all.
-inline int64_t gated_splits(int64_t M, int64_t N, int64_t K) {
-  const int64_t big_m = (M - 1) / BigCfg::BM + 1, big_n = (N - 1) / BigCfg::BN + 1;
-  if (big_m >= 128 || big_n >= 128 || big_m * big_n >= 128) return 0;
-  const int64_t G = K / 128, tiles = ceil_div(M, SmallCfg::BM) * ceil_div(N, SmallCfg::BN);
-  int64_t S = ceil_div(2 * (int64_t)device_cus(), tiles);  // two 128 x 128 workgroups fit per CU
-  if (S > G / 4) S = G / 4;
-  if (S > 16) S = 16;
-  return S < 1 ? 1 : S;
+// Tiles of a dense product: 256, 128, 64 or 32 rows by 256 columns of B, and
+// into how many parts K is split (1: fused, more: partial products, joined).
+struct GatedForm {
+  int rows;
+  int64_t splits;
+};
+
+// The form that takes least time by what the forms take per K group and round
+// over the compute units, in ns: fitted to 252 products (1 to 4096 rows, K 512
+// to 7168, H 512 to 2048, either direction) measured in every form on one box,
+// within 0.5 % of the best form on average.  Both sides, forward of K = 7168 and
+// H = 2048 in us: 16 rows 64 fused 50, 32 in 14 parts 11.5; 128 rows 64 fused
+// 51, 64 in 8 parts 16; 1024 rows 64 fused 57, 128 70, 64 in 2 parts 67; 2048
+// rows 128 fused 74, 256 100, 64 103; 4096 rows 256 fused 102, 128 139.
+inline GatedForm gated_form(int64_t M, int64_t N, int64_t K, bool gradient, bool may_split) {
+  const int64_t n = ceil_div(N, 256), cus = device_cus(), G = K / 128;
+  GatedForm best{256, 1};
+  int64_t least = INT64_MAX;
+  auto fused = [&](int rows, int64_t group) {
+    const int64_t rounds = ceil_div(std::min<int64_t>(ceil_div(M, rows), 1 << 20) * std::min<int64_t>(n, 1 << 20), cus);
+    const int64_t ns = (gradient ? 5200 : 3300) + group * G * rounds;
+    if (ns < least) least = ns, best = {rows, 1};
+  };
+  fused(256, 1330);
+  if (ceil_div(M, 256) * n > 4 * cus) return best;  // many rounds: the largest tile
+  fused(128, 930);
+  fused(64, 580);
+  if (!may_split) return best;
+  for (const int rows : {64, 32}) {
+    const int64_t tiles = ceil_div(M, rows) * n;
+    for (int64_t s = 2; s <= 16 && s <= G; ++s) {
+      const int64_t per = ceil_div(G, s), S = ceil_div(G, per);
+      const int64_t ns = 5200 + (rows == 64 ? 470 : 420) * per * ceil_div(tiles * S, cus) + S * M * N * 3 / 2000;
+      if (ns < least) least = ns, best = {rows, S};
+    }
+  }
+  return best;
+}
+
+// Rows of the experts' tiles, by the mean number of rows: the less of a tile an
+// expert fills, the more of it is wasted.  128 experts of 7168 x 4096 (and of
+// the down projection's 2048 x 7168), skewed as a router's top 8 of them, 64 /
+// 128 / 256 rows in us: mean 2 439 / - / 528 (gradient 240 / - / 298), 32 730 /
+// 724 / 809 (376 / 364 / 432), 96 977 / 902 / 942 (558 / 504 / 563), 192 1460 /
+// 1244 / 1204 (802 / 721 / 729), 256 1833 / 1528 / 1434 (1006 / 859 / 874), 384
+// 2569 / 2045 / 1879 (1397 / 1167 / 1090).
+inline int expert_rows(int64_t G, int64_t M, bool gradient) {
+  if (M <= (gradient ? 40 : 28) * G) return 64;
+  return M <= (gradient ? 256 : 160) * G ? 128 : 256;
 }
 
 constexpr int64_t kGatedMaxPitch = int64_t(1) << 23;  // per-lane copy offsets are 32-bit
@@ -568,42 +784,139 @@ inline GatedArgs gated_args(int64_t M, int64_t H, int64_t K, int64_t N, const ui
     if (opB & FP8BLK_GEMM_POW2_SCALES) LAUNCH_(false, true); else LAUNCH_(false, false); \
   }
 
-// Grid of the grouped kernels: each expert adds at most one partial row tile;
+// Grid of the grouped kernels: each expert adds at most one partial row tile of BM;
 // a multiple of 8, as grouped_tile's shares of the XCDs need it.  0: too many.
+template <class CFG>
 inline int64_t grouped_blocks(int64_t G, int64_t M, int64_t max_group_rows, int64_t tiles_n) {
   if (G > kGatedMost) return 0;
-  int64_t tiles_m = ceil_div(M, BigCfg::BM) + G;
-  if (max_group_rows > 0) tiles_m = std::min(tiles_m, G * ceil_div(std::min(max_group_rows, M), BigCfg::BM));
+  int64_t tiles_m = ceil_div(M, CFG::BM) + G;
+  if (max_group_rows > 0) tiles_m = std::min(tiles_m, G * ceil_div(std::min(max_group_rows, M), CFG::BM));
   const int64_t blocks = ceil_div(tiles_m * tiles_n, 8) * 8;
-  return grid_ok(blocks, BigCfg::NT) ? blocks : 0;
+  return grid_ok(blocks, CFG::NT) ? blocks : 0;
+}
+
+template <class CFG>
+inline bool dense_grid(GatedArgs& a) {
+  a.tiles_m = ceil_div(a.M, CFG::BM);
+  a.tiles_n = ceil_div(a.N, CFG::BN);
+  return grid_ok(a.tiles_m * a.tiles_n, CFG::NT);
 }
 
 // The partial products of a dense product of few rows, as S slices of M x N.
+template <class D, bool GATED>
 inline fp8blk_status_t launch_partials(GatedArgs a, int opB, int64_t& S, float* partials, hipStream_t st) {
-  using CFG = SmallCfg;
-  a.tiles_m = ceil_div(a.M, CFG::BM);
-  a.tiles_n = ceil_div(a.N, CFG::BN);
   const int64_t G = a.K / 128, per = ceil_div(G, S);
   S = ceil_div(G, per);
-  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n), (unsigned)S), block(CFG::NT);
-#define FP8BLK_GATED_LAUNCH(T_, P2_) \
-  hipLaunchKernelGGL((k_gated_partial<CFG, T_, P2_>), grid, block, 0, st, a, partials, (int)per)
+  if (!dense_grid<typename D::CFG>(a)) return FP8BLK_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n), (unsigned)S), block(D::CFG::NT);
+  if (opB & FP8BLK_OP_T) hipLaunchKernelGGL((k_gated_partial<D, true, GATED>), grid, block, 0, st, a, partials, (int)per);
+  else hipLaunchKernelGGL((k_gated_partial<D, false, GATED>), grid, block, 0, st, a, partials, (int)per);
+  return launch_status();
+}
+
+// The fused kernels on tiles of CFG (BigCfg) or D, dense or grouped, over `blocks` workgroups.
+template <bool GROUPED>
+inline fp8blk_status_t launch_big(const GatedArgs& a, int opB, int64_t blocks, const GatedOut& o, hipStream_t st) {
+  const dim3 grid((unsigned)blocks), block(BigCfg::NT);
+#define FP8BLK_GATED_LAUNCH(T_, P2_) hipLaunchKernelGGL((k_gated_gemm<BigCfg, GROUPED, T_, P2_>), grid, block, 0, st, a, o)
   FP8BLK_GATED_BY_B(FP8BLK_GATED_LAUNCH)
 #undef FP8BLK_GATED_LAUNCH
   return launch_status();
+}
+template <bool GROUPED>
+inline fp8blk_status_t launch_big(const GatedArgs& a, int opB, int64_t blocks, const GatedGradOut& o, hipStream_t st) {
+  const dim3 grid((unsigned)blocks), block(BigCfg::NT);
+#define FP8BLK_GATED_LAUNCH(T_, P2_) \
+  hipLaunchKernelGGL((k_gated_gemm_backward<BigCfg, GROUPED, T_, P2_>), grid, block, 0, st, a, o)
+  FP8BLK_GATED_BY_B(FP8BLK_GATED_LAUNCH)
+#undef FP8BLK_GATED_LAUNCH
+  return launch_status();
+}
+template <class D, bool GROUPED>
+inline fp8blk_status_t launch_deep(const GatedArgs& a, int opB, int64_t blocks, const GatedOut& o, hipStream_t st) {
+  const dim3 grid((unsigned)blocks), block(D::CFG::NT);
+  if (opB & FP8BLK_OP_T) hipLaunchKernelGGL((k_gated_gemm_deep<D, GROUPED, true>), grid, block, 0, st, a, o);
+  else hipLaunchKernelGGL((k_gated_gemm_deep<D, GROUPED, false>), grid, block, 0, st, a, o);
+  return launch_status();
+}
+template <class D, bool GROUPED>
+inline fp8blk_status_t launch_deep(const GatedArgs& a, int opB, int64_t blocks, const GatedGradOut& o, hipStream_t st) {
+  const dim3 grid((unsigned)blocks), block(D::CFG::NT);
+  if (opB & FP8BLK_OP_T) hipLaunchKernelGGL((k_gated_gemm_backward_deep<D, GROUPED, true>), grid, block, 0, st, a, o);
+  else hipLaunchKernelGGL((k_gated_gemm_backward_deep<D, GROUPED, false>), grid, block, 0, st, a, o);
+  return launch_status();
+}
+constexpr int kJoinSlices = 8;  // where there are more than four parts
+inline void launch_join(const float* partials, int64_t S, const GatedArgs& a, const GatedOut& o, hipStream_t st) {
+  const int64_t groups = a.M * (a.H / 128);
+  if (S > 4)
+    hipLaunchKernelGGL(k_gated_join<kJoinSlices>, dim3((unsigned)groups), dim3(32 * kJoinSlices), 0, st, partials, (int)S, a.M,
+                       a.H, o);
+  else
+    hipLaunchKernelGGL(k_gated_join<1>, dim3((unsigned)ceil_div(groups, 2)), dim3(64), 0, st, partials, (int)S, a.M, a.H, o);
+}
+inline void launch_join(const float* partials, int64_t S, const GatedArgs& a, const GatedGradOut& o, hipStream_t st) {
+  const int64_t groups = a.M * (a.H / 128);
+  if (S > 4)
+    hipLaunchKernelGGL(k_gated_join_backward<kJoinSlices>, dim3((unsigned)groups), dim3(32 * kJoinSlices), 0, st, partials,
+                       (int)S, a.M, a.H, o);
+  else
+    hipLaunchKernelGGL(k_gated_join_backward<1>, dim3((unsigned)ceil_div(groups, 2)), dim3(64), 0, st, partials, (int)S, a.M,
+                       a.H, o);
+}
+
+inline size_t gated_bytes(int64_t M, int64_t H, int64_t K, int64_t N) {
+  if (M <= 0 || H <= 0 || K <= 0 || H % 128 != 0 || K % 128 != 0 || M > kGatedMost || H > kGatedMost) return 0;
+  const int64_t S = gated_form(M, N, K, N == H, true).splits;
+  return S > 1 ? (size_t)(S * M * N) * sizeof(float) : 0;
+}
+
+// A dense product: in parts and joined where that is faster and the workspace is there.
+template <bool GATED, class Out>
+inline fp8blk_status_t launch_dense(GatedArgs a, int opB, const Out& o, void* workspace, size_t bytes,
+                                    hipStream_t st) {
+  const size_t need = gated_bytes(a.M, a.H, a.K, a.N);
+  const bool split = need > 0 && workspace != nullptr && aligned(workspace, 16) && bytes >= need;
+  GatedForm form = gated_form(a.M, a.N, a.K, !GATED, split);
+  if (form.splits > 1) {
+    float* partials = static_cast<float*>(workspace);
+    const fp8blk_status_t got = form.rows == 32 ? launch_partials<FewDeep, GATED>(a, opB, form.splits, partials, st)
+                                                : launch_partials<LowDeep, GATED>(a, opB, form.splits, partials, st);
+    if (got != FP8BLK_OK) return got;
+    launch_join(partials, form.splits, a, o, st);
+    return launch_status();
+  }
+  const bool fits = form.rows == 256   ? dense_grid<BigCfg>(a)
+                    : form.rows == 128 ? dense_grid<MidDeep::CFG>(a)
+                                       : dense_grid<LowDeep::CFG>(a);
+  if (!fits) return FP8BLK_ERR_UNSUPPORTED;
+  const int64_t blocks = a.tiles_m * a.tiles_n;
+  if (form.rows == 256) return launch_big<false>(a, opB, blocks, o, st);
+  if (form.rows == 128) return launch_deep<MidDeep, false>(a, opB, blocks, o, st);
+  return launch_deep<LowDeep, false>(a, opB, blocks, o, st);
+}
+
+// A product for every expert.
+template <bool GATED, class Out>
+inline fp8blk_status_t launch_experts(GatedArgs a, int opB, int64_t max_group_rows, const Out& o, hipStream_t st) {
+  a.tiles_n = ceil_div(a.N, 256);
+  const int rows = expert_rows(a.G, a.M, !GATED);
+  const int64_t blocks = rows == 256   ? grouped_blocks<BigCfg>(a.G, a.M, max_group_rows, a.tiles_n)
+                         : rows == 128 ? grouped_blocks<MidDeep::CFG>(a.G, a.M, max_group_rows, a.tiles_n)
+                                       : grouped_blocks<LowDeep::CFG>(a.G, a.M, max_group_rows, a.tiles_n);
+  if (blocks == 0) return FP8BLK_ERR_UNSUPPORTED;
+  if (rows == 256) return launch_big<true>(a, opB, blocks, o, st);
+  if (rows == 128) return launch_deep<MidDeep, true>(a, opB, blocks, o, st);
+  return launch_deep<LowDeep, true>(a, opB, blocks, o, st);
 }
 
 }  // namespace fp8blk
 
 using namespace fp8blk;
 
-extern "C" size_t fp8blk_gated_gemm_workspace_bytes(int64_t M, int64_t H, int64_t K) {
-  if (M <= 0 || H <= 0 || K <= 0 || H % 128 != 0 || K % 128 != 0) return 0;
-  return (size_t)(gated_splits(M, 2 * H, K) * M * 2 * H) * sizeof(float);
-}
+extern "C" size_t fp8blk_gated_gemm_workspace_bytes(int64_t M, int64_t H, int64_t K) { return gated_bytes(M, H, K, 2 * H); }
 extern "C" size_t fp8blk_gated_gemm_backward_workspace_bytes(int64_t M, int64_t H, int64_t K) {
-  if (M <= 0 || H <= 0 || K <= 0 || H % 128 != 0 || K % 128 != 0) return 0;
-  return (size_t)(gated_splits(M, H, K) * M * H) * sizeof(float);
+  return gated_bytes(M, H, K, H);
 }
 
 extern "C" fp8blk_status_t fp8blk_gated_gemm_fp8_blockscaled(
@@ -614,27 +927,8 @@ extern "C" fp8blk_status_t fp8blk_gated_gemm_fp8_blockscaled(
   if (ok != FP8BLK_OK || M == 0 || H == 0) return ok;
   const GatedOut o{u, ldu, h, ldh, q, ldq, s, M, act == FP8BLK_ACT_GELU, (qflags & FP8BLK_SCALE_POW2) != 0};
   if (!forward_ok(M, H, o)) return FP8BLK_ERR_INVALID_ARG;
-  GatedArgs a = gated_args(M, H, K, 2 * H, A, lda, sA, B, ldb, opB, sB);
-  hipStream_t st = as_stream(stream);
-  int64_t S = gated_splits(M, 2 * H, K);
-  if (S > 0 && workspace != nullptr && aligned(workspace, 16) &&
-      workspace_bytes >= fp8blk_gated_gemm_workspace_bytes(M, H, K)) {
-    float* partials = static_cast<float*>(workspace);
-    const fp8blk_status_t got = launch_partials(a, opB, S, partials, st);
-    if (got != FP8BLK_OK) return got;
-    hipLaunchKernelGGL(k_gated_join, dim3((unsigned)ceil_div(M * (H / 8), 256)), dim3(256), 0, st, partials, (int)S, M,
-                       H, o);
-    return launch_status();
-  }
-  using CFG = BigCfg;
-  a.tiles_m = ceil_div(M, CFG::BM);
-  a.tiles_n = H / (CFG::BN / 2);
-  if (!grid_ok(a.tiles_m * a.tiles_n, CFG::NT)) return FP8BLK_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n)), block(CFG::NT);
-#define FP8BLK_GATED_LAUNCH(T_, P2_) hipLaunchKernelGGL((k_gated_gemm<CFG, false, T_, P2_>), grid, block, 0, st, a, o)
-  FP8BLK_GATED_BY_B(FP8BLK_GATED_LAUNCH)
-#undef FP8BLK_GATED_LAUNCH
-  return launch_status();
+  const GatedArgs a = gated_args(M, H, K, 2 * H, A, lda, sA, B, ldb, opB, sB);
+  return launch_dense<true>(a, opB, o, workspace, workspace_bytes, as_stream(stream));
 }
 
 extern "C" fp8blk_status_t fp8blk_grouped_gated_gemm_fp8_blockscaled(
@@ -642,7 +936,6 @@ extern "C" fp8blk_status_t fp8blk_grouped_gated_gemm_fp8_blockscaled(
     const uint8_t* A, int64_t lda, const float* sA, const uint8_t* B, int64_t ldb, int64_t strideB, int opB,
     const float* sB, int64_t stride_sB, int act, uint16_t* u, int64_t ldu, uint16_t* h, int64_t ldh, uint8_t* q,
     int64_t ldq, float* s, uint32_t qflags, void* stream) {
-  using CFG = BigCfg;
   if (G < 0 || max_group_rows < 0) return FP8BLK_ERR_INVALID_ARG;
   const fp8blk_status_t ok = gated_check(G == 0 ? 0 : M_total, H, K, 2 * H, A, lda, sA, B, ldb, opB, sB, act, qflags);
   if (ok != FP8BLK_OK || G == 0 || M_total == 0 || H == 0) return ok;
@@ -656,15 +949,7 @@ extern "C" fp8blk_status_t fp8blk_grouped_gated_gemm_fp8_blockscaled(
   a.offsets = group_offsets;
   a.strideB = strideB;
   a.stride_sB = stride_sB;
-  a.tiles_n = H / (CFG::BN / 2);
-  const int64_t blocks = grouped_blocks(G, M_total, max_group_rows, a.tiles_n);
-  if (blocks == 0) return FP8BLK_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)blocks), block(CFG::NT);
-  hipStream_t st = as_stream(stream);
-#define FP8BLK_GATED_LAUNCH(T_, P2_) hipLaunchKernelGGL((k_gated_gemm<CFG, true, T_, P2_>), grid, block, 0, st, a, o)
-  FP8BLK_GATED_BY_B(FP8BLK_GATED_LAUNCH)
-#undef FP8BLK_GATED_LAUNCH
-  return launch_status();
+  return launch_experts<true>(a, opB, max_group_rows, o, as_stream(stream));
 }
 
 extern "C" fp8blk_status_t fp8blk_gated_gemm_backward_fp8_blockscaled(
@@ -676,28 +961,8 @@ extern "C" fp8blk_status_t fp8blk_gated_gemm_backward_fp8_blockscaled(
   if (ok != FP8BLK_OK || M == 0 || H == 0) return ok;
   const GatedGradOut o{u, ldu, du, lddu, h, ldh, q, ldq, s, M, act == FP8BLK_ACT_GELU, (qflags & FP8BLK_SCALE_POW2) != 0};
   if (!backward_ok(M, H, o)) return FP8BLK_ERR_INVALID_ARG;
-  GatedArgs a = gated_args(M, H, K, H, A, lda, sA, B, ldb, opB, sB);
-  hipStream_t st = as_stream(stream);
-  int64_t S = gated_splits(M, H, K);
-  if (S > 0 && workspace != nullptr && aligned(workspace, 16) &&
-      workspace_bytes >= fp8blk_gated_gemm_backward_workspace_bytes(M, H, K)) {
-    float* partials = static_cast<float*>(workspace);
-    const fp8blk_status_t got = launch_partials(a, opB, S, partials, st);
-    if (got != FP8BLK_OK) return got;
-    hipLaunchKernelGGL(k_gated_join_backward, dim3((unsigned)ceil_div(M * (H / 8), 256)), dim3(256), 0, st, partials,
-                       (int)S, M, H, o);
-    return launch_status();
-  }
-  using CFG = BigCfg;
-  a.tiles_m = ceil_div(M, CFG::BM);
-  a.tiles_n = ceil_div(H, CFG::BN);
-  if (!grid_ok(a.tiles_m * a.tiles_n, CFG::NT)) return FP8BLK_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n)), block(CFG::NT);
-#define FP8BLK_GATED_LAUNCH(T_, P2_) \
-  hipLaunchKernelGGL((k_gated_gemm_backward<CFG, false, T_, P2_>), grid, block, 0, st, a, o)
-  FP8BLK_GATED_BY_B(FP8BLK_GATED_LAUNCH)
-#undef FP8BLK_GATED_LAUNCH
-  return launch_status();
+  const GatedArgs a = gated_args(M, H, K, H, A, lda, sA, B, ldb, opB, sB);
+  return launch_dense<false>(a, opB, o, workspace, workspace_bytes, as_stream(stream));
 }
 
 extern "C" fp8blk_status_t fp8blk_grouped_gated_gemm_backward_fp8_blockscaled(
@@ -705,7 +970,6 @@ extern "C" fp8blk_status_t fp8blk_grouped_gated_gemm_backward_fp8_blockscaled(
     const uint8_t* A, int64_t lda, const float* sA, const uint8_t* B, int64_t ldb, int64_t strideB, int opB,
     const float* sB, int64_t stride_sB, int act, const uint16_t* u, int64_t ldu, uint16_t* du, int64_t lddu,
     uint16_t* h, int64_t ldh, uint8_t* q, int64_t ldq, float* s, uint32_t qflags, void* stream) {
-  using CFG = BigCfg;
   if (G < 0 || max_group_rows < 0) return FP8BLK_ERR_INVALID_ARG;
   const fp8blk_status_t ok = gated_check(G == 0 ? 0 : M_total, H, K, H, A, lda, sA, B, ldb, opB, sB, act, qflags);
   if (ok != FP8BLK_OK || G == 0 || M_total == 0 || H == 0) return ok;
@@ -720,14 +984,5 @@ extern "C" fp8blk_status_t fp8blk_grouped_gated_gemm_backward_fp8_blockscaled(
   a.offsets = group_offsets;
   a.strideB = strideB;
   a.stride_sB = stride_sB;
-  a.tiles_n = ceil_div(H, CFG::BN);
-  const int64_t blocks = grouped_blocks(G, M_total, max_group_rows, a.tiles_n);
-  if (blocks == 0) return FP8BLK_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)blocks), block(CFG::NT);
-  hipStream_t st = as_stream(stream);
-#define FP8BLK_GATED_LAUNCH(T_, P2_) \
-  hipLaunchKernelGGL((k_gated_gemm_backward<CFG, true, T_, P2_>), grid, block, 0, st, a, o)
-  FP8BLK_GATED_BY_B(FP8BLK_GATED_LAUNCH)
-#undef FP8BLK_GATED_LAUNCH
-  return launch_status();
+  return launch_experts<false>(a, opB, max_group_rows, o, as_stream(stream));
 }

@@ -252,9 +252,9 @@ struct CopyPlan {
   // cover both.
   static constexpr int KSTEP = NW * 64 / (BN / 16);
   static_assert(KSTEP % 32 == 0, "[K][N] copies: bit 5 of k per lane or alternating per iteration");
-  static_assert(!GATED || (BN == 256 && !ROW128 && 8 * NW == CFG::WTN), "a gated tile's copies");
+  static_assert(!GATED || (BN == 256 && !ROW128 && 8 * NW % CFG::WTN == 0), "a gated tile's copies");
   // [N][K] B: rows from one copy iteration to the next
-  static constexpr int BSTEP = GATED ? CFG::WTN / 2 : 8 * NW;
+  static constexpr int BSTEP = GATED ? 4 * NW : 8 * NW;
   uint32_t a, b, b2;
 
   __device__ __forceinline__ void init(const TileArgs& t) {
@@ -366,7 +366,8 @@ struct CopyPlan {
 // with ROWPIPE_MIN_TM or more row tiles per wave (the 256x256 and 224x256
 // tiles).  The
 // 128x128 tiles (two workgroups per CU) keep the loop that issues a group's
-// copies at its start (compute_group below).
+// copies at its start (compute_group below).  Tiles with a store of their own
+// (OUT_OWN) always run it.
 #ifndef FP8BLK_ROWPIPE_MIN_TM
 #define FP8BLK_ROWPIPE_MIN_TM 7
 #endif
@@ -658,7 +659,7 @@ __device__ __forceinline__ void compute_group_rows(const uint8_t* ops, const flo
                                                    uint32_t scoff, const v4i& ra, const v4i& rb, const v4i& rs,
                                                    uint8_t* nops, float* nsc, int wave, int blk) {
   constexpr int BN = CFG::BN, TM = CFG::TM, TN = CFG::TN, R = FP8BLK_FOLD_RING;
-  constexpr int LOADS = CopyPlan<CFG, OPB_T, ROW128, GATED>::LOADS, CR = FP8BLK_COPY_ROWS;
+  constexpr int LOADS = CopyPlan<CFG, OPB_T, ROW128, GATED>::LOADS, CR = FP8BLK_COPY_ROWS < TM ? FP8BLK_COPY_ROWS : TM;
   static_assert(CR >= 1 && CR <= TM, "copy rows");
   const int lane = threadIdx.x & 63;
   const int wm = wave / CFG::WAVES_N, wn = wave % CFG::WAVES_N;
@@ -860,10 +861,9 @@ __device__ __forceinline__ void gemm_tile(const TileArgs& t, uint8_t* ops0, uint
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-  if constexpr (row_pipelined<CFG, ROW128>()) {
+  if constexpr (OM == OUT_OWN || row_pipelined<CFG, ROW128>()) {
     gemm_loop_rows<CFG, OPB_T, ROW128, P2, SKIP, GATED>(t, ops0, ops1, sc0, sc1, acc);
   } else {
-    static_assert(!GATED, "gated tiles run the row-pipelined loop");
     CopyPlan<CFG, OPB_T, ROW128> plan;
     plan.init(t);
     if (g0 < G) plan.issue(t, g0, ops0, sc0);  // no groups (an expert without tokens): C = 0

@@ -127,24 +127,54 @@ def test_gradient(M, K, H, act, opB, pow2):
         assert torch.equal(got.q, want.q)
 
 
+@pytest.mark.parametrize("M", [70, 300, 800, 2100, 4101])
+@pytest.mark.parametrize("opB,pow2", [(0, False), (1, True)])
+def test_tile_sizes(M, opB, pow2):
+    """Rows for every tile height, fused and in parts that are joined."""
+    K, H = 384, 1024
+    x, sx = fb.quantize_1x128(_bf16((M, K), 1), pow2=pow2)
+    w, sw = _weights(*((2 * H, K) if opB else (K, 2 * H)), 2, pow2)
+    C = fb.gemm_fp8_blockscaled(x, sx, w, sw, opB=opB, split_k=False, pow2_scales=pow2)
+    kw = dict(opB=opB, pow2_scales=pow2, quantize=True, pow2=pow2)
+    fused = fb.gated_gemm_fp8_blockscaled(x, sx, w, sw, split_k=False, **kw)
+    r = fb.gated_gemm_fp8_blockscaled(x, sx, w, sw, **kw)
+    assert torch.equal(fused.u, C.to(BF))
+    e = _split_error(x, sx, w, sw, opB, M, 2 * H)
+    assert np.all(np.abs(_np(r.u) - _np(C)) <= _half(_np(C), e))
+    for o in (fused, r):
+        _check_h(o.h, _np(C), H, "silu", e)
+        q, s = fb.quantize_1x128(o.h, pow2=pow2)
+        assert torch.equal(o.q, q) and torch.equal(o.s, s)
+    d, sd = _weights(*((2 * H, K) if opB else (K, 2 * H)), 3, pow2)
+    dh = fb.gemm_fp8_blockscaled(x, sx, d, sd, opB=opB, split_k=False, pow2_scales=pow2)
+    u = _bf16((M, 4 * H), 4)
+    e = _split_error(x, sx, d, sd, opB, M, 2 * H)
+    for split in (False, True):
+        g = fb.gated_gemm_backward_fp8_blockscaled(x, sx, d, sd, u, split_k=split, **kw)
+        _check_grad(g, _np(dh), u, "silu", e if split else 0.0)
+        q, s = fb.quantize_1x128(g.du, pow2=pow2)
+        assert torch.equal(g.q, q) and torch.equal(g.s, s)
+
+
 def _offsets(counts):
     return torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
 
 
-def _counts(G, seed):
+def _counts(G, seed, most):
     rng = np.random.RandomState(seed)
-    c = rng.randint(0, 60, G) * (rng.rand(G) < 0.7)
-    c[G // 2] = 300
+    c = rng.randint(0, most, G) * (rng.rand(G) < 0.7)
+    c[G // 2] = 300 if most > 20 else 70
+    c[0] += most > 200  # odd row counts throughout
     return c
 
 
-@pytest.mark.parametrize("G", [1, 7, 70, 300])
-@pytest.mark.parametrize("act,t,pow2", [("silu", False, False), ("gelu", True, True)])
-def test_experts(G, act, t, pow2):
-    """Every expert's rows as the grouped GEMM makes them; rows no expert owns stay as they were."""
-    print(f"[train] experts {G} {act} {t} {pow2}", flush=True)
-    K, H, past = 256, 128 if G == 300 else 256, 19
-    counts = _counts(G, G)
+@pytest.mark.parametrize("G,most", [(1, 60), (7, 60), (70, 60), (300, 60), (12, 14), (70, 14), (300, 6), (6, 400), (5, 1200)])
+@pytest.mark.parametrize("act,t,pow2", [("silu", False, False), ("gelu", True, True), ("silu", True, False)])
+def test_experts(G, most, act, t, pow2):
+    """Every expert's rows as the grouped GEMM makes them, many rows each and few; rows no expert owns stay as they were."""
+    print(f"[train] experts {G} {most} {act} {t} {pow2}", flush=True)
+    K, H, past = 256 if most > 20 else 768, 128 if G == 300 else 256, 19
+    counts = _counts(G, G, most)
     P, off = int(counts.sum()), _offsets(counts)
     M = P + past
     x, sx = fb.quantize_1x128(_bf16((M, K), 1), pow2=pow2)
