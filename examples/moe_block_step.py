@@ -1,6 +1,6 @@
-"""One training step of a mixture-of-experts block in FP8: forward, backward
-and gradient clipping, every step of it a call of this package (the router's
-product and top-k and the expert activation silu(gate) * up are torch).
+"""One training step of a mixture-of-experts block in FP8: forward, backward,
+gradient clipping and the optimizer's update, every step of it a call of this
+package (the router's product and top-k are torch).
 
     python examples/moe_block_step.py [--tokens 8192 --hidden 7168 --experts 256 --topk 8 --width 2048]
 
@@ -9,11 +9,18 @@ Forward, for the residual stream x:
     experts   = top-k of sigmoid(n Wr), weights normalized        torch
     maps      = pairs sorted by expert                            moe_sort
     rows      = codes and scales in expert order                  moe_dispatch_fp8
-    u, h, o   = up projection, silu(gate) * up, down projection   grouped_gemm_fp8_blockscaled, quantize_1x128
+    u, h      = gate and up projection, h = silu(gate) * up       grouped_gated_gemm_fp8_blockscaled
+    o         = down projection of h's codes                      grouped_gemm_fp8_blockscaled
     y         = rows back to tokens, weighted                     moe_combine
     x', n'    = norm of y, gate, residual sum, next block's norm  residual_norm
 Backward, from the gradients of x' and n', the same in reverse; quantization
-passes gradients through.
+passes gradients through.  Between the two, only u is kept of an expert's rows:
+the gradient of the down projection's input, the activation's gradient and h
+again are one call (grouped_gated_gemm_backward_fp8_blockscaled).
+
+Update: AdamW with E4M3 moments on the FP32 norms and router and on the BF16
+expert weights (rounded at random), gradients clipped by their global norm as
+they are read; then the expert weights' codes anew.
 """
 from __future__ import annotations
 
@@ -46,6 +53,9 @@ class Block:
     topk: int
 
     def __post_init__(self):
+        self.quantize()
+
+    def quantize(self):
         self.q_up, self.s_up = self._quantize(self.up)
         self.q_down, self.s_down = self._quantize(self.down)
 
@@ -65,13 +75,31 @@ class Block:
                      down=torch.stack([(n(H, C) * H ** -0.5).to(torch.bfloat16) for _ in range(E)]), topk=topk)
 
 
-def _act(u, H):
-    return torch.nn.functional.silu(u[:, :H].float()) * u[:, H:].float()
+NAMES = ("w_pre", "w_post", "gate", "w_next", "router", "up", "down")
+
+
+class Optimizer:
+    """AdamW over a block's parameters; no weight decay on norms and gate."""
+
+    def __init__(self, b: Block, lr=1e-3, max_norm=1.0):
+        self.block, self.lr, self.max_norm, self.steps = b, lr, max_norm, 0
+        self.state = fb.AdamWState([getattr(b, k) for k in NAMES], dtype=torch.float8_e4m3fn,
+                                   decay=[0.1 if k in ("router", "up", "down") else 0.0 for k in NAMES])
+
+    def update(self, grads) -> torch.Tensor:
+        """One step from gradients by name; returns their norm before clipping."""
+        self.steps += 1
+        grads = [grads[k] for k in NAMES]
+        norm = fb.grad_norm(grads)
+        fb.adamw_step(fb.adamw_table(self.state, grads), self.lr, self.steps, norm=norm, max_norm=self.max_norm,
+                      seed=self.steps)
+        self.block.quantize()
+        return norm
 
 
 def forward(b: Block, x: torch.Tensor):
     """(x', n', what the backward needs)."""
-    E, H = b.up.shape[0], b.down.shape[1]
+    E = b.up.shape[0]
     r0 = fb.residual_norm(x, w_pre=b.w_pre, quantize=True)
     n_router = r0.n.float().requires_grad_()
     router = b.router.detach().requires_grad_()
@@ -80,37 +108,32 @@ def forward(b: Block, x: torch.Tensor):
         weights = top.values / top.values.sum(1, keepdim=True)
     off, row_of, slot_of = fb.moe_sort(top.indices, E)
     qx, sx = fb.moe_dispatch_fp8(r0.q, r0.s, row_of, slot_of)
-    u = fb.grouped_gemm_fp8_blockscaled(off, qx, sx, b.q_up, b.s_up, out_dtype=torch.bfloat16)
-    h = _act(u, H).to(torch.bfloat16)
-    o = fb.grouped_gemm_fp8_blockscaled(off, *fb.quantize_1x128(h), b.q_down, b.s_down)
+    r = fb.grouped_gated_gemm_fp8_blockscaled(off, qx, sx, b.q_up, b.s_up, quantize=True, want_h=False)
+    o = fb.grouped_gemm_fp8_blockscaled(off, r.q, r.s, b.q_down, b.s_down)
     w = weights.detach()
     y = fb.moe_combine(o, row_of, w)
     r1 = fb.residual_norm(x, w_pre=b.w_next, f=y, w_post=b.w_post, gate=b.gate, alpha=ALPHA)
     return r1.x, r1.n, dict(x=x, r0=r0, n_router=n_router, router=router, weights=weights, w=w, off=off, row_of=row_of,
-                            u=u, h=h, o=o, y=y, r1=r1)
+                            u=r.u, o=o, y=y, r1=r1)
 
 
 def backward(b: Block, s: dict, dx_out: torch.Tensor, dn: torch.Tensor):
     """(dx, gradients by name) from the gradients of x' and n'."""
-    H = b.down.shape[1]
     off, row_of, r0, r1 = s["off"], s["row_of"], s["r0"], s["r1"]
     P = row_of.numel()
     g1 = fb.residual_norm_backward(r1.x, dx_out=dx_out, dn=dn, rstd_pre=r1.rstd_pre, w_pre=b.w_next, f=s["y"],
                                    rstd_post=r1.rstd_post, w_post=b.w_post, gate=b.gate, alpha=ALPHA)
     do, dweights = fb.moe_combine_backward(g1.df, s["o"], row_of, s["w"], drows_dtype=torch.bfloat16)
-    # down projection: gradient of its input (the stored weights read transposed) and of its weights
-    dh = fb.grouped_gemm_fp8_blockscaled(off, *fb.quantize_1x128(do), b.q_down, b.s_down, opB=fb.OP_T)
-    d_down = fb.grouped_wgrad_fp8_blockscaled(off, P, *fb.quantize_128x1_grouped(s["h"], off),
+    # down projection and activation: gradient of u (in its place) with its codes, and h again
+    g = fb.grouped_gated_gemm_backward_fp8_blockscaled(off, *fb.quantize_1x128(do), b.q_down, b.s_down, s["u"],
+                                                       quantize=True, du=s["u"])
+    d_down = fb.grouped_wgrad_fp8_blockscaled(off, P, *fb.quantize_128x1_grouped(g.h, off),
                                               *fb.quantize_128x1_grouped(do, off))
-    with torch.enable_grad():
-        u = s["u"].float().requires_grad_()
-        _act(u, H).backward(dh)
-    du = u.grad.to(torch.bfloat16)
-    dxr = fb.grouped_gemm_fp8_blockscaled(off, *fb.quantize_1x128(du), b.q_up, b.s_up, opB=fb.OP_T,
-                                          out_dtype=torch.bfloat16)
+    # up projection
+    dxr = fb.grouped_gemm_fp8_blockscaled(off, g.q, g.s, b.q_up, b.s_up, opB=fb.OP_T, out_dtype=torch.bfloat16)
     rows = fb.moe_dispatch(r0.n, row_of)
     d_up = fb.grouped_wgrad_fp8_blockscaled(off, P, *fb.quantize_128x1_grouped(rows, off),
-                                            *fb.quantize_128x1_grouped(du, off))
+                                            *fb.quantize_128x1_grouped(g.du, off))
     # the router, and the norm before the block
     s["weights"].backward(dweights)
     dn0 = fb.moe_combine(dxr, row_of, out_dtype=torch.float32).add_(s["n_router"].grad).to(torch.bfloat16)
@@ -127,6 +150,13 @@ def step(b: Block, x, dx_out, dn, max_norm=1.0):
     return xo, n, dx, grads, norm
 
 
+def train_step(b: Block, opt: Optimizer, x, dx_out, dn):
+    """Forward, backward and update: (x', n', dx, the gradients' norm before clipping)."""
+    xo, n, saved = forward(b, x)
+    dx, grads = backward(b, saved, dx_out, dn)
+    return xo, n, dx, opt.update(grads)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--tokens", type=int, default=2048)
@@ -139,15 +169,16 @@ def main(argv=None):
     g = torch.Generator(device="cuda").manual_seed(1)
     x, dx, dn = (torch.randn(a.tokens, a.hidden, generator=g, device="cuda").to(torch.bfloat16) * k
                  for k in (1.0, 1e-3, 1e-3))
+    opt = Optimizer(b)
     t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     for i in range(4):
         t0.record()
-        _, _, _, grads, norm = step(b, x, dx, dn)
+        _, _, _, norm = train_step(b, opt, x, dx, dn)
         t1.record()
     torch.cuda.synchronize()
     print(f"{a.tokens} tokens, hidden {a.hidden}, {a.experts} experts of width {a.width}, top {a.topk}: "
           f"{t0.elapsed_time(t1):.2f} ms a step, gradient norm {float(norm):.4g} over "
-          f"{sum(v.numel() for v in grads.values())} values")
+          f"{sum(getattr(b, k).numel() for k in NAMES)} values")
 
 
 if __name__ == "__main__":
