@@ -47,9 +47,9 @@ QUANT_BYTES_BLOCK = 2 + 1 + 4 / (128 * 128)
 # what the L2s request beyond themselves: 178 MB is the compulsory minimum of
 # the tile order, each of the 8 XCDs (one L2 each) reading the A and B panels
 # of its 4 x 8 block of tiles once (8 x 12 x 1.84 MB); sharing across XCDs is
-# left to the Infinity Cache.  Valid only for the GEMM source it was measured
-# on (sha256 below); reported as null otherwise.
-GEMM_TRAFFIC = {"sha256": "d7ab41e494250c7fa40bd673b214cd9b1e704c79ec03b43732dabd4a11643264",
+# left to the Infinity Cache.  Valid only for the GEMM sources it was measured
+# on (sha256 of gemm.hip and gemm_tile.h below); reported as null otherwise.
+GEMM_TRAFFIC = {"sha256": "fe9bdf0bf5ff6c29a820e9dc5cb99542ace0062b100725b97c907ac18416f886",
                 "fetch_bytes": 178243156, "write_bytes": 67108864}
 
 
@@ -140,12 +140,14 @@ def warm_up(torch, fn, min_seconds):
 
 
 def gemm_traffic():
-    """Measured HBM bytes per GEMM launch if the GEMM source is unchanged."""
+    """Measured HBM bytes per GEMM launch if the GEMM sources are unchanged."""
     import hashlib
-    src = os.path.join(ROOT, "fp8_fine_grained_quantize_amd", "csrc", "gemm.hip")
-    with open(src, "rb") as f:
-        if hashlib.sha256(f.read()).hexdigest() != GEMM_TRAFFIC["sha256"]:
-            return None
+    digest = hashlib.sha256()
+    for name in ("gemm.hip", "gemm_tile.h"):
+        with open(os.path.join(ROOT, "fp8_fine_grained_quantize_amd", "csrc", name), "rb") as f:
+            digest.update(f.read())
+    if digest.hexdigest() != GEMM_TRAFFIC["sha256"]:
+        return None
     return GEMM_TRAFFIC["fetch_bytes"] + GEMM_TRAFFIC["write_bytes"]
 
 
