@@ -13,6 +13,10 @@
 // 40 operations.  A workgroup takes a contiguous run of chunks (tensor_table.h);
 // a lane holds four consecutive values, so that FP32 is one 16-byte access, and
 // 32 lanes a group of 128, whose maximum is found by lane exchanges.
+// Measured, with BF16 copies: 0.94e9 values in FP32 4.85 ms (5.8 TB/s), with E4M3
+// moments rounded at random 3.18 ms (5.3 TB/s); 60e6 values in BF16 throughout,
+// without copies, 173 us (4.9 TB/s counting 14 bytes a value); 1.2e6 values in 200
+// tensors 9 us, three dependent reads of the table and one of the data.
 //
 // Every operation is rounded by itself, none fused, in the order in which a
 // program of elementary FP32 operations takes them: a value that differs in its

@@ -20,6 +20,14 @@
 // Gradient: the plain tile of dh, whose lanes read u where their results lie.
 // Both are bound as the GEMMs are, by moving operands; the FP32 results (u or
 // dh, half a GB for 65536 rows of 2048) never reach memory.
+//
+// Measured, K = 7168 and H = 2048: forward with codes out, 8192 rows 220 us
+// (2.19 PFLOP/s, the GEMMs' rate), 65536 rows of 256 experts with u and codes 2.83
+// ms (the GEMM of the same operands alone, FP32 out, 2.84); gradient, 8192 rows
+// 134 us (1.80 PFLOP/s), 65536 rows of 256 experts with codes 1.81 ms (plain GEMM
+// 1.46).  The gradient's codes cost 24 us at 8192 rows, one round of tiles with
+// nothing to cover its end (a quantizer of its own 19 and a launch), and 90 us for
+// the experts (148).
 #include <algorithm>
 
 #include "../../include/libfp8blk_train.h"
@@ -429,7 +437,7 @@ __device__ __forceinline__ void wait_groups(int groups) {
   }
 }
 
-template <class D, bool OPB_T, bool GATED>
+template <class D, bool OPB_T, bool GATED, bool ONCE = false>
 __device__ __forceinline__ void deep_loop(const TileArgs& t, D& lds, v4f (&acc)[D::CFG::TM][D::CFG::TN]) {
   using CFG = typename D::CFG;
   using Plan = CopyPlan<CFG, OPB_T, false, GATED>;
@@ -452,8 +460,8 @@ __device__ __forceinline__ void deep_loop(const TileArgs& t, D& lds, v4f (&acc)[
   cur.init(t, t.g0, blk * 64 < CFG::BMP);
   int into = 0;  // the stage of the next group to copy
   auto issue = [&]() {
-    issue_copies<CFG, OPB_T, false, false, GATED>(t, plan, scoff, cur.ra(true), cur.rb(true), cur.rs(true), 0, Plan::LOADS,
-                                                  lds.ops[into], lds.sc[into], wave, blk);
+    issue_copies<CFG, OPB_T, false, false, GATED, ONCE>(t, plan, scoff, cur.ra(true), cur.rb(true), cur.rs(true), 0,
+                                                        Plan::LOADS, lds.ops[into], lds.sc[into], wave, blk);
     cur.advance();
     into = into + 1 < ST ? into + 1 : 0;
   };
@@ -515,27 +523,33 @@ __device__ __forceinline__ void deep_loop(const TileArgs& t, D& lds, v4f (&acc)[
   }
 }
 
-template <class D, bool GROUPED, bool OPB_T>
+// Few rows, or experts of few rows: bound by the weights' way from memory.  128
+// rows for 79 of 256 experts of 7168 x 4096 take 367 us for 2.3 GB (6.3 TB/s;
+// reads alone reach 7.0); 777 rows of 2048 x 2816 16 us, a launch and 16 K groups
+// of one tile after the other.
+template <class D, bool GROUPED, bool OPB_T, bool ONCE>
 __global__ __launch_bounds__(D::CFG::NT) void k_gated_gemm_deep(GatedArgs a, GatedOut o) {
   __shared__ __align__(16) D lds;
   TileArgs t;
   if (!gated_tile<typename D::CFG, GROUPED, true>(a, t)) return;
   v4f acc[D::CFG::TM][D::CFG::TN];
-  deep_loop<D, OPB_T, true>(t, lds, acc);
+  deep_loop<D, OPB_T, true, ONCE>(t, lds, acc);
   GatedStore<typename D::CFG>{o}(t, acc, lds.ops[0]);
 }
 
-template <class D, bool GROUPED, bool OPB_T>
+template <class D, bool GROUPED, bool OPB_T, bool ONCE>
 __global__ __launch_bounds__(D::CFG::NT) void k_gated_gemm_backward_deep(GatedArgs a, GatedGradOut o) {
   __shared__ __align__(16) D lds;
   TileArgs t;
   if (!gated_tile<typename D::CFG, GROUPED, false>(a, t)) return;
   v4f acc[D::CFG::TM][D::CFG::TN];
-  deep_loop<D, OPB_T, false>(t, lds, acc);
+  deep_loop<D, OPB_T, false, ONCE>(t, lds, acc);
   GatedGradStore<typename D::CFG>{o}(t, acc, lds.ops[0]);
 }
 
-// FP32 partial products [split][M][N] of K groups [split * per, ...).
+// FP32 partial products [split][M][N] of K groups [split * per, ...): 16 rows of
+// 7168 x 4096 in 14 parts take 7.6 us for 29 MB of weights (and the join 2.0, see
+// below), of which the launch and the first copies' way are half.
 template <class D, bool OPB_T, bool GATED>
 __global__ __launch_bounds__(D::CFG::NT) void k_gated_partial(GatedArgs a, float* __restrict__ partials, int per) {
   using CFG = typename D::CFG;
@@ -720,6 +734,16 @@ inline int expert_rows(int64_t G, int64_t M, bool gradient) {
   return M <= (gradient ? 256 : 160) * G ? 128 : 256;
 }
 
+// Whether the weights pass by the caches: more of them than the Infinity Cache
+// holds, and read by one tile, as almost all are with few rows an expert.  256
+// experts of 7168 x 4096 (gradient: 2048 x 7168) in us, kept / passing by: 32 rows
+// of 31 experts 178 / 162 (gradient 90 / 80), 2048 of 219 1083 / 987 (559 / 535),
+// 4096 of 240 1240 / 1156 (637 / 625), 8192 of 251 1386 / 1372 (744 / 758); where
+// they fit, called again and again, 8 of 8 53 / 66 (44 / 49).
+inline bool read_once(const GatedArgs& a) {
+  return a.M <= 20 * a.G && std::min(a.G, a.M) > kStreamBytes / a.K / a.N;
+}
+
 constexpr int64_t kGatedMaxPitch = int64_t(1) << 23;  // per-lane copy offsets are 32-bit
 constexpr int64_t kGatedMost = int64_t(1) << 31;      // of M, H and K: products of two of them fit 64 bits
 
@@ -832,18 +856,18 @@ inline fp8blk_status_t launch_big(const GatedArgs& a, int opB, int64_t blocks, c
 #undef FP8BLK_GATED_LAUNCH
   return launch_status();
 }
-template <class D, bool GROUPED>
+template <class D, bool GROUPED, bool ONCE = false>
 inline fp8blk_status_t launch_deep(const GatedArgs& a, int opB, int64_t blocks, const GatedOut& o, hipStream_t st) {
   const dim3 grid((unsigned)blocks), block(D::CFG::NT);
-  if (opB & FP8BLK_OP_T) hipLaunchKernelGGL((k_gated_gemm_deep<D, GROUPED, true>), grid, block, 0, st, a, o);
-  else hipLaunchKernelGGL((k_gated_gemm_deep<D, GROUPED, false>), grid, block, 0, st, a, o);
+  if (opB & FP8BLK_OP_T) hipLaunchKernelGGL((k_gated_gemm_deep<D, GROUPED, true, ONCE>), grid, block, 0, st, a, o);
+  else hipLaunchKernelGGL((k_gated_gemm_deep<D, GROUPED, false, ONCE>), grid, block, 0, st, a, o);
   return launch_status();
 }
-template <class D, bool GROUPED>
+template <class D, bool GROUPED, bool ONCE = false>
 inline fp8blk_status_t launch_deep(const GatedArgs& a, int opB, int64_t blocks, const GatedGradOut& o, hipStream_t st) {
   const dim3 grid((unsigned)blocks), block(D::CFG::NT);
-  if (opB & FP8BLK_OP_T) hipLaunchKernelGGL((k_gated_gemm_backward_deep<D, GROUPED, true>), grid, block, 0, st, a, o);
-  else hipLaunchKernelGGL((k_gated_gemm_backward_deep<D, GROUPED, false>), grid, block, 0, st, a, o);
+  if (opB & FP8BLK_OP_T) hipLaunchKernelGGL((k_gated_gemm_backward_deep<D, GROUPED, true, ONCE>), grid, block, 0, st, a, o);
+  else hipLaunchKernelGGL((k_gated_gemm_backward_deep<D, GROUPED, false, ONCE>), grid, block, 0, st, a, o);
   return launch_status();
 }
 constexpr int kJoinSlices = 8;  // where there are more than four parts
@@ -907,6 +931,7 @@ inline fp8blk_status_t launch_experts(GatedArgs a, int opB, int64_t max_group_ro
   if (blocks == 0) return FP8BLK_ERR_UNSUPPORTED;
   if (rows == 256) return launch_big<true>(a, opB, blocks, o, st);
   if (rows == 128) return launch_deep<MidDeep, true>(a, opB, blocks, o, st);
+  if (read_once(a)) return launch_deep<LowDeep, true, true>(a, opB, blocks, o, st);
   return launch_deep<LowDeep, true>(a, opB, blocks, o, st);
 }
 

@@ -152,6 +152,13 @@ __device__ __forceinline__ void dma16(v4i r, uint32_t voff, int32_t soff, uint8_
                : "v"(voff), "s"(r), "s"(soff), "s"(lds_addr(lds_base))
                : "memory", "m0");
 }
+// dma16 of what is read once: kept no longer than it has to be in the caches.
+__device__ __forceinline__ void dma16_once(v4i r, uint32_t voff, int32_t soff, uint8_t* lds_base) {
+  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+               :
+               : "v"(voff), "s"(r), "s"(soff), "s"(lds_addr(lds_base))
+               : "memory", "m0");
+}
 // dma16 issued only when `left` > 0 (a scalar test inside the same asm
 // block, so the compiler's schedule around it is that of a plain copy).
 __device__ __forceinline__ void dma16_if(v4i r, uint32_t voff, int32_t soff, uint8_t* lds_base, int32_t left) {
@@ -624,8 +631,8 @@ struct GroupCursor {
 // Copies n0 .. n1-1 of a group (A blocks, then B blocks, then the scale run).
 // SKIP: an A block whose 8 rows all lie past the tile's valid rows is not
 // issued (its LDS rows keep stale data, which only feeds output rows that
-// are never stored).
-template <class CFG, bool OPB_T, bool ROW128, bool SKIP, bool GATED>
+// are never stored).  ONCE: no other workgroup reads this tile of B.
+template <class CFG, bool OPB_T, bool ROW128, bool SKIP, bool GATED, bool ONCE = false>
 __device__ __forceinline__ void issue_copies(const TileArgs& t, const CopyPlan<CFG, OPB_T, ROW128, GATED>& plan,
                                              uint32_t scoff, const v4i& ra, const v4i& rb, const v4i& rs, int n0,
                                              int n1, uint8_t* buf, float* sbuf, int wave, int blk) {
@@ -644,7 +651,10 @@ __device__ __forceinline__ void issue_copies(const TileArgs& t, const CopyPlan<C
     } else if (n < CFG::A_ITERS + CFG::B_ITERS) {
       const int it = n - CFG::A_ITERS;
       const int32_t so = OPB_T ? (int32_t)(it * plan.BSTEP * t.ldb) : (int32_t)(it * KSTEP * t.ldb);
-      dma16(rb, (!OPB_T && (it & 1)) ? plan.b2 : plan.b, so, buf + CFG::A_BYTES + (it * NW + wave) * 1024);
+      const uint32_t vo = (!OPB_T && (it & 1)) ? plan.b2 : plan.b;
+      uint8_t* to = buf + CFG::A_BYTES + (it * NW + wave) * 1024;
+      if constexpr (ONCE) dma16_once(rb, vo, so, to);
+      else dma16(rb, vo, so, to);
     } else {
       dma4(rs, scoff, (uint8_t*)(sbuf + blk * 64));
     }

@@ -328,7 +328,8 @@ def adamw_step(table: AdamWTable, lr, step, beta1: float = 0.9, beta2: float = 0
     as they are read, and stay as they are.  seed: round BF16 and E4M3 values at
     random by this integer, another one every step (None: to nearest).  lr, step
     and seed may be one-element tensors on the device (float32, int64, int64),
-    which a captured step reads anew at every replay."""
+    which a captured step reads anew at every replay; the graph reads the table
+    too, which has to live as long as it is replayed."""
     if not isinstance(table, AdamWTable):
         raise TypeError("table must be an AdamWTable")
     t = table.device_table

@@ -175,7 +175,8 @@ fp8blk_status_t fp8blk_adamw_table_build(const fp8blk_adamw_t* list, int64_t n, 
 
 /* What a step depends on.  Values that change from step to step may come from
  * device memory, read when the kernel runs, so that a captured graph can be
- * replayed: lr_at, step_at, seed_at non-NULL replace lr, step and seed. */
+ * replayed: lr_at, step_at, seed_at non-NULL replace lr, step and seed.  They
+ * are not checked: below 1 step a moment's correction is not finite. */
 typedef struct {
   double lr, beta1, beta2, eps; /* FP64: 1 - 0.999 in FP32 is off by 5e-5 of itself */
   int64_t step;                 /* t, at least 1 */

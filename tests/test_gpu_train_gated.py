@@ -204,6 +204,33 @@ def test_experts(G, most, act, t, pow2):
                                                                        pow2_scales=pow2).h[:P])
 
 
+@pytest.mark.parametrize("t,pow2", [(False, False), (True, True), (True, False)])
+def test_experts_past_the_caches(t, pow2):
+    """Few rows for each of many experts, whose weights are more than the caches hold: the grouped GEMM's bits."""
+    print(f"[train] experts past the caches {t} {pow2}", flush=True)
+    G, K, H, past = 280, 1024, 1024, 3
+    counts = np.random.RandomState(7).randint(0, 4, G)
+    counts[3] = 70  # two tiles
+    P, off, opB = int(counts.sum()), _offsets(counts), int(t)
+    assert 257 < P <= 20 * G  # one MB of codes an expert in the gradient, two forward
+    x, sx = fb.quantize_1x128(_bf16((P + past, K), 1), pow2=pow2)
+    w, sw = _weights(*((2 * H, K) if t else (K, 2 * H)), 2, pow2, G)
+    r = fb.grouped_gated_gemm_fp8_blockscaled(off, x, sx, w, sw, opB=opB, pow2_scales=pow2, quantize=True, pow2=pow2,
+                                              u=torch.full((P + past, 2 * H), 7.0, dtype=BF, device="cuda"))
+    C = fb.grouped_gemm_fp8_blockscaled(off, x, sx, w, sw, opB=opB, pow2_scales=pow2)[:P]
+    assert torch.equal(r.u[:P], C.to(BF)) and (r.u[P:] == 7).all()
+    _check_h(r.h[:P], _np(C), H, "silu")
+    q, s = fb.quantize_1x128(r.h[:P].contiguous(), pow2=pow2)
+    assert torch.equal(r.q[:P], q) and torch.equal(r.s[:, :P], s)
+    d, sd = _weights(*((H, K) if t else (K, H)), 5, pow2, G)
+    dh = fb.grouped_gemm_fp8_blockscaled(off, x, sx, d, sd, opB=opB, pow2_scales=pow2)[:P]
+    g = fb.grouped_gated_gemm_backward_fp8_blockscaled(off, x, sx, d, sd, r.u, opB=opB, pow2_scales=pow2, quantize=True,
+                                                       pow2=pow2)
+    _check_grad(fb.GatedGemmGrad(g.du[:P], g.h[:P], None, None), _np(dh), r.u[:P], "silu")
+    q, s = fb.quantize_1x128(g.du[:P].contiguous(), pow2=pow2)
+    assert torch.equal(g.q[:P], q) and torch.equal(g.s[:, :P], s)
+
+
 def test_no_rows():
     w, sw = _weights(256, 512, 1, False)
     x, sx = fb.quantize_1x128(_bf16((0, 256), 1))
