@@ -49,7 +49,7 @@ QUANT_BYTES_BLOCK = 2 + 1 + 4 / (128 * 128)
 # of its 4 x 8 block of tiles once (8 x 12 x 1.84 MB); sharing across XCDs is
 # left to the Infinity Cache.  Valid only for the GEMM sources it was measured
 # on (sha256 of gemm.hip and gemm_tile.h below); reported as null otherwise.
-GEMM_TRAFFIC = {"sha256": "fe9bdf0bf5ff6c29a820e9dc5cb99542ace0062b100725b97c907ac18416f886",
+GEMM_TRAFFIC = {"sha256": "44ac9b32b1a8e9450f29fa925ed90a69a051705bd0944bb80a3ab83c8884552f",
                 "fetch_bytes": 178243156, "write_bytes": 67108864}
 
 
