@@ -13,10 +13,14 @@
 // 40 operations.  A workgroup takes a contiguous run of chunks (tensor_table.h);
 // a lane holds four consecutive values, so that FP32 is one 16-byte access, and
 // 32 lanes a group of 128, whose maximum is found by lane exchanges.
-// Measured, with BF16 copies: 0.94e9 values in FP32 4.85 ms (5.8 TB/s), with E4M3
-// moments rounded at random 3.18 ms (5.3 TB/s); 60e6 values in BF16 throughout,
-// without copies, 173 us (4.9 TB/s counting 14 bytes a value); 1.2e6 values in 200
-// tensors 9 us, three dependent reads of the table and one of the data.
+// Measured, with BF16 copies: 0.94e9 values in FP32 4.76 ms (5.9 TB/s), with E4M3
+// moments rounded at random 3.12 ms (5.5 TB/s); 60e6 values in BF16 throughout,
+// without copies, 172 us (4.9 TB/s counting 14 bytes a value); 1.2e6 values in 200
+// tensors 9 us, three dependent reads of the table and one of the data.  With E4M3
+// moments the vector instructions, some 100 a value, take nearly as long as the
+// bytes: a root by root_of, a scale's reciprocal by one Newton step, magnitudes
+// without signs, and addresses in scalar registers took 0.27e9 values without
+// copies from 829 to 752 us (BF16 parameters, to nearest: 700 to 615).
 //
 // Every operation is rounded by itself, none fused, in the order in which a
 // program of elementary FP32 operations takes them: a value that differs in its
@@ -63,8 +67,9 @@ struct AdamArgs {
   uint32_t seed;
 };
 
-__device__ __forceinline__ uint32_t random_bits(uint32_t key, int64_t place) {
-  uint32_t h = ((uint32_t)place * 0x9E3779B1u ^ (uint32_t)((uint64_t)place >> 32)) + key;
+// place: its low and its high half.
+__device__ __forceinline__ uint32_t random_bits(uint32_t key, uint32_t place, uint32_t high) {
+  uint32_t h = (place * 0x9E3779B1u ^ high) + key;
   h = (h ^ h >> 16) * 0x85EBCA6Bu;
   h = (h ^ h >> 13) * 0xC2B2AE35u;
   return h ^ h >> 16;
@@ -75,13 +80,25 @@ __device__ __forceinline__ float to_bf16_random(float x, uint32_t r16) {
   return x == x ? __uint_as_float((__float_as_uint(x) + r16) & 0xFFFF0000u) : x;
 }
 
+// sqrt(x), correctly rounded, of what is zero or at least 2^-100 (NaN and
+// infinity stay): Tuckerman's test.  s, the hardware's root, is off by one unit at
+// most, and of s and its neighbours the root lies nearest to s unless s (s - ulp)
+// >= x or s (s + ulp) < x.  Neither holds for zero.
+__device__ __forceinline__ float root_of(float x) {
+  const float s = __builtin_amdgcn_sqrtf(x);
+  const float down = __uint_as_float(__float_as_uint(s) - 1), up = __uint_as_float(__float_as_uint(s) + 1);
+  const float r = __builtin_fmaf(-down, s, x) <= 0.0f ? down : s;
+  return __builtin_fmaf(-up, s, x) > 0.0f ? up : r;
+}
+
 // The scale of a group with that maximum, and its reciprocal for the quotients
-// (within one unit in the last place, see fp8_device.h).
+// (by one Newton step, within one unit in the last place; see fp8_device.h).
 __device__ __forceinline__ TileScale moment_scale(uint32_t amax_bits) {
   TileScale t{1.0f, 1.0f, false};
   if (amax_bits == 0) return t;
   t.s = __uint_as_float(amax_bits) * (1.0f / kE4M3Max);
-  t.r = 1.0f / t.s;
+  const float r = __builtin_amdgcn_rcpf(t.s);
+  t.r = __builtin_fmaf(__builtin_fmaf(-t.s, r, 1.0f), r, r);
   t.slow = !(t.s >= 0x1p-100f && t.s <= 0x1p100f);
   return t;
 }
@@ -90,29 +107,33 @@ __device__ __forceinline__ TileScale moment_scale(uint32_t amax_bits) {
 // are not negative and none above zero becomes zero.
 template <bool ROOT>
 __device__ __forceinline__ uint32_t encode4(const float (&x)[4], bool random, const uint32_t (&r16)[4], float& scale) {
+  constexpr uint32_t magnitude = ROOT ? 0xFFFFFFFFu : 0x7FFFFFFFu;
   uint32_t a = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) a = max(a, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+  for (int j = 0; j < 4; ++j) a = max(a, __float_as_uint(x[j]) & magnitude);
   a = row16_max(a);
   const auto o = __builtin_amdgcn_permlane16_swap(a, a, false, false);
   const TileScale ts = moment_scale(max(o[0], o[1]));
   scale = ts.s;
   float y[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) y[j] = quotient_fast<false, true>(x[j], ts);
+  for (int j = 0; j < 4; ++j) {  // quotient_fast, without its sign
+    const float q = x[j] * ts.r;
+    y[j] = __builtin_fmaf(__builtin_fmaf(-ts.s, q, x[j]), ts.r, q);
+  }
   if (__builtin_expect(ts.slow, 0)) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] = quotient_slow(x[j], ts.s);
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float v = fminf(__builtin_fabsf(y[j]), kE4M3Max);
+    // 2^-9, the smallest code, stays what it is below.
+    float v = __builtin_amdgcn_fmed3f(__builtin_fabsf(y[j]), ROOT && x[j] > 0.0f ? 0x1p-9f : 0.0f, kE4M3Max);
     if (random) {  // below 2^-6 the codes lie 2^-9 apart, as they do from there to 2^-5
       const float up = v < 0x1p-6f ? 0x1p-6f : 0.0f;
       v = __uint_as_float((__float_as_uint(v + up) + (r16[j] << 4)) & 0xFFF00000u) - up;
     }
-    if (ROOT && x[j] > 0.0f) v = fmaxf(v, 0x1p-9f);
-    y[j] = __builtin_copysignf(v, x[j]);
+    y[j] = ROOT ? v : __builtin_copysignf(v, x[j]);
   }
   return pack4_e4m3(y[0], y[1], y[2], y[3]);
 }
@@ -129,28 +150,40 @@ __device__ __forceinline__ void decode4(uint32_t c, float s, float (&x)[4]) {
 // tensor whose rows lie apart; or in two rows of one.
 enum Lie { DENSE, ROW, ROWS };
 
-// The elements i .. i + count - 1 of a tensor in rows of cols, ld apart (4 at
-// once: one access unless they lie in two rows); the others zero.
+// A lane's place: element `base` of its tensor, the same for the whole
+// workgroup and a multiple of kChunk, and `mine` from there on: an address in
+// scalar registers and an offset of 32 bits in vector ones.
+struct Place {
+  int64_t base;
+  uint32_t mine;
+  int count;  // of the lane's four elements, those that exist
+  Lie lie;
+  __device__ __forceinline__ int64_t index() const { return base + mine; }
+};
+
+// The elements at a place of a tensor in rows of cols, ld apart (4 at once: one
+// access unless they lie in two rows); those that do not exist zero.
 template <bool NT, typename T>
-__device__ __forceinline__ RawV<T, 4> load4(const T* t, int64_t i, int count, Lie lie, int64_t cols, int64_t ld) {
-  if (count == 4 && lie != ROWS) return load_raw<4, NT>(global(t + (lie == ROW ? at(i, cols, ld) : i)));
+__device__ __forceinline__ RawV<T, 4> load4(const T* t, const Place& w, int64_t cols, int64_t ld) {
+  if (w.count == 4 && w.lie == DENSE) return load_raw<4, NT>(global(t + w.base) + w.mine);
+  if (w.count == 4 && w.lie == ROW) return load_raw<4, NT>(global(t + at(w.index(), cols, ld)));
   RawV<T, 4> r{};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if (j >= count) continue;
-    const T x = global(t)[lie == DENSE ? i + j : at(i + j, cols, ld)];
+    if (j >= w.count) continue;
+    const T x = global(t)[w.lie == DENSE ? w.index() + j : at(w.index() + j, cols, ld)];
     if constexpr (sizeof(T) == 4) r[j] = __float_as_uint(x);
     else r[j >> 1] |= (uint32_t)x << ((j & 1) * 16);
   }
   return r;
 }
 template <bool NT, typename T>
-__device__ __forceinline__ void store4(T* t, const float (&v)[4], int64_t i, int count, Lie lie, int64_t cols,
-                                       int64_t ld) {
-  if (count == 4 && lie != ROWS) return store_v<4, NT>(global(t + (lie == ROW ? at(i, cols, ld) : i)), v);
+__device__ __forceinline__ void store4(T* t, const float (&v)[4], const Place& w, int64_t cols, int64_t ld) {
+  if (w.count == 4 && w.lie == DENSE) return store_v<4, NT>(global(t + w.base) + w.mine, v);
+  if (w.count == 4 && w.lie == ROW) return store_v<4, NT>(global(t + at(w.index(), cols, ld)), v);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (j < count) global(t)[lie == DENSE ? i + j : at(i + j, cols, ld)] = from_f32<T>(v[j]);
+    if (j < w.count) global(t)[w.lie == DENSE ? w.index() + j : at(w.index() + j, cols, ld)] = from_f32<T>(v[j]);
 }
 
 // The moments' type as stored, and what a lane loads of them.
@@ -187,44 +220,46 @@ struct AdamRange {
   uint32_t key;
   bool random;
 
-  __device__ __forceinline__ Quad<TP, TG, ST> load(int64_t i, int count, Lie lie) const {
+  __device__ __forceinline__ Quad<TP, TG, ST> load(const Place& w) const {
     // FP32 moments of large tables: a wave reads one tensor after another.  Four
     // reads and four writes at the same place of as many tensors, from every
     // wave at once, is what memory does worst: 0.94e9 values 4.83 ms at once, 4.54
-    // in turn.  With E4M3 moments the waits cost more than that: 3.12 / 3.50.
+    // in turn.  With E4M3 moments the waits cost more than that: 3.12 / 3.50, and
+    // with BF16 ones they win as often as they lose (60e6 values 172 / 187 us).
     constexpr bool TURNS = NT && ST == FP8BLK_ADAMW_F32;
     Quad<TP, TG, ST> q{};
-    q.p = load4<NT>((const TP*)e.p, i, count, lie, e.cols, e.ldp);
+    q.p = load4<NT>((const TP*)e.p, w, e.cols, e.ldp);
     if (TURNS) wait_vmem();
-    q.g = load4<NT>((const TG*)e.g, i, count, lie, e.cols, e.ldg);
+    q.g = load4<NT>((const TG*)e.g, w, e.cols, e.ldg);
     if (TURNS) wait_vmem();
     if constexpr (ST == FP8BLK_ADAMW_E4M3) {
-      const Global<const uint8_t> *m = global((const uint8_t*)e.m + i), *v = global((const uint8_t*)e.v + i);
-      if (count == 4) {
+      const Global<const uint8_t>*m = global((const uint8_t*)e.m + w.base) + w.mine,
+                   *v = global((const uint8_t*)e.v + w.base) + w.mine;
+      if (w.count == 4) {
         q.m = *(const Global<const uint32_t>*)m;
         q.v = *(const Global<const uint32_t>*)v;
       } else {
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
-          if (j >= count) continue;
+          if (j >= w.count) continue;
           q.m |= (uint32_t)m[j] << (8 * j);
           q.v |= (uint32_t)v[j] << (8 * j);
         }
       }
-      if (count > 0) {
-        q.ms = global(e.ms)[i >> 7];
-        q.vs = global(e.vs)[i >> 7];
+      if (w.count > 0) {
+        q.ms = global(e.ms + (w.base >> 7))[w.mine >> 7];
+        q.vs = global(e.vs + (w.base >> 7))[w.mine >> 7];
       }
     } else {
-      q.m = load4<NT>((const TM*)e.m, i, count, DENSE, 0, 0);
+      q.m = load4<NT>((const TM*)e.m, dense(w), 0, 0);
       if (TURNS) wait_vmem();
-      q.v = load4<NT>((const TM*)e.v, i, count, DENSE, 0, 0);
+      q.v = load4<NT>((const TM*)e.v, dense(w), 0, 0);
     }
     return q;
   }
 
   // Every lane of the wave takes part (count may be 0): E4M3 scales are found across lanes.
-  __device__ __forceinline__ void finish(const Quad<TP, TG, ST>& q, int64_t i, int count, Lie lie) const {
+  __device__ __forceinline__ void finish(const Quad<TP, TG, ST>& q, const Place& w) const {
     float p[4], g[4], m[4], v[4], r[4];
     unpack_v<TP, 4>(q.p, p);
     unpack_v<TG, 4>(q.g, g);
@@ -242,14 +277,23 @@ struct AdamRange {
       g[j] *= clip;
       m[j] = a.b1 * m[j] + a.nb1 * g[j];
       v[j] = a.b2 * v[j] + a.nb2 * g[j] * g[j];
-      r[j] = sqrtf(v[j]);
-      p[j] = p[j] * keep - step_size * m[j] / (r[j] * root + a.eps);
+      r[j] = ST != FP8BLK_ADAMW_BF16 ? root_of(v[j]) : sqrtf(v[j]);  // BF16: sqrtf with the loop below is 4 % faster
     }
+    uint32_t least = 0xFFFFFFFFu;  // zeros become the largest
+#pragma unroll
+    for (int j = 0; j < 4; ++j) least = min(least, __float_as_uint(v[j]) - 1);
+    if (ST != FP8BLK_ADAMW_BF16 && __builtin_expect(least < 0x0D800000u, 0)) {  // 2^-100
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[j] = sqrtf(v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = p[j] * keep - step_size * m[j] / (r[j] * root + a.eps);
+    const uint32_t place = (uint32_t)w.base + w.mine, high = (uint32_t)((uint64_t)w.base >> 32);
     uint32_t rm[4] = {}, rv[4] = {};
     if (ST != FP8BLK_ADAMW_F32 && random) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t h = random_bits(key, i + j);
+        const uint32_t h = random_bits(key, place + j, high);
         rm[j] = h & 0xFFFFu;
         rv[j] = h >> 16;
       }
@@ -257,21 +301,21 @@ struct AdamRange {
     if constexpr (ST == FP8BLK_ADAMW_E4M3) {
       float ms, vs;
       const uint32_t mc = encode4<false>(m, random, rm, ms), vc = encode4<true>(r, random, rv, vs);
-      Global<uint8_t> *md = global((uint8_t*)e.m + i), *vd = global((uint8_t*)e.v + i);
-      if (count == 4) {
+      Global<uint8_t>*md = global((uint8_t*)e.m + w.base) + w.mine, *vd = global((uint8_t*)e.v + w.base) + w.mine;
+      if (w.count == 4) {
         store_words<NT, 1>((Global<void>*)md, Words<1>::type{mc});
         store_words<NT, 1>((Global<void>*)vd, Words<1>::type{vc});
       } else {
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
-          if (j >= count) continue;
+          if (j >= w.count) continue;
           md[j] = (uint8_t)(mc >> (8 * j));
           vd[j] = (uint8_t)(vc >> (8 * j));
         }
       }
-      if (count > 0 && (threadIdx.x & 31) == 0) {
-        global(e.ms)[i >> 7] = ms;
-        global(e.vs)[i >> 7] = vs;
+      if (w.count > 0 && (threadIdx.x & 31) == 0) {
+        global(e.ms + (w.base >> 7))[w.mine >> 7] = ms;
+        global(e.vs + (w.base >> 7))[w.mine >> 7] = vs;
       }
     } else {
       if (ST == FP8BLK_ADAMW_BF16 && random) {
@@ -281,40 +325,53 @@ struct AdamRange {
           v[j] = to_bf16_random(v[j], rv[j]);
         }
       }
-      store4<NT>((TM*)e.m, m, i, count, DENSE, 0, 0);
-      store4<NT>((TM*)e.v, v, i, count, DENSE, 0, 0);
+      store4<NT>((TM*)e.m, m, dense(w), 0, 0);
+      store4<NT>((TM*)e.v, v, dense(w), 0, 0);
     }
-    if (e.copy != nullptr) store4<NT>(e.copy, p, i, count, lie, e.cols, e.ldc);
+    if (e.copy != nullptr) store4<NT>(e.copy, p, w, e.cols, e.ldc);
     if (sizeof(TP) == 2 && random) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = to_bf16_random(p[j], random_bits(key ^ 0x5BD1E995u, i + j) & 0xFFFFu);
+      for (int j = 0; j < 4; ++j) p[j] = to_bf16_random(p[j], random_bits(key ^ 0x5BD1E995u, place + j, high) & 0xFFFFu);
     }
-    store4<NT>((TP*)e.p, p, i, count, lie, e.cols, e.ldp);
+    store4<NT>((TP*)e.p, p, w, e.cols, e.ldp);
   }
 
   // The elements [lo, hi); lo is a multiple of kChunk, hi too unless the tensor
   // ends there.  A chunk's loads go out before the stores of the one before: one
   // counter counts both, so that loads behind stores would wait for them.
   __device__ __forceinline__ void run(int64_t lo, int64_t hi) const {
-    const int64_t mine = (int64_t)threadIdx.x * 4;
+    const uint32_t mine = threadIdx.x * 4;
     int64_t base = lo;
     if (!e.pitched && base + kChunk <= hi) {
-      Quad<TP, TG, ST> q = load(base + mine, 4, DENSE);
-      for (; base + 2 * kChunk <= hi; base += kChunk) {
-        const Quad<TP, TG, ST> next = load(base + kChunk + mine, 4, DENSE);
-        finish(q, base + mine, 4, DENSE);
+      Quad<TP, TG, ST> q = load({base, mine, 4, DENSE});
+      auto two = [&]() {
+        const Quad<TP, TG, ST> next = load({base + kChunk, mine, 4, DENSE});
+        finish(q, {base, mine, 4, DENSE});
         q = next;
+        base += kChunk;
+      };
+      if constexpr (ST == FP8BLK_ADAMW_BF16) {
+        while (base + 2 * kChunk <= hi) two();
+      } else {  // by twos, without moving `next` to `q`: E4M3 5 % of its instructions (BF16: 4 % slower)
+        for (; base + 3 * kChunk <= hi; base += 2 * kChunk) {
+          const Quad<TP, TG, ST> next = load({base + kChunk, mine, 4, DENSE});
+          finish(q, {base, mine, 4, DENSE});
+          q = load({base + 2 * kChunk, mine, 4, DENSE});
+          finish(next, {base + kChunk, mine, 4, DENSE});
+        }
+        if (base + 2 * kChunk <= hi) two();
       }
-      finish(q, base + mine, 4, DENSE);
+      finish(q, {base, mine, 4, DENSE});
       base += kChunk;
     }
     const Lie lie = !e.pitched ? DENSE : (e.cols & 3) == 0 ? ROW : ROWS;
     for (; base < hi; base += kChunk) {
-      const int64_t i = base + mine;
-      const int left = (int)max((int64_t)0, min((int64_t)4, hi - i));
-      finish(load(i, left, lie), i, left, lie);
+      const int left = (int)max((int64_t)0, min((int64_t)4, hi - base - mine));
+      const Place w{base, mine, left, lie};
+      finish(load(w), w);
     }
   }
+  static __device__ __forceinline__ Place dense(const Place& w) { return {w.base, w.mine, w.count, DENSE}; }
 };
 
 template <int ST, bool NT>
@@ -358,16 +415,20 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamEntry* __restrict__ tab
 inline bool adam_stream(int64_t chunks) { return chunks >= ((int64_t)1 << 25) / kChunk; }
 
 // Chunks of a workgroup.  Short runs keep the waves' places in memory close
-// together: 0.94e9 values with FP32 moments 4.83 / 5.06 / 5.06 ms with 1 / 2 / 4
-// chunks each (persistent workgroups 5.4 and more); with E4M3 moments a chunk's
-// time no longer covers the search of the table: 4.19 / 3.28 / 3.12 (8: 3.15), and
-// 60e6 values in BF16 213 / 165 / 149 us (8: 160).
+// together, longer ones cover the search of the table: 0.94e9 values with FP32
+// moments 4.76 / 4.67 / 4.90 / 4.95 ms with 1 / 2 / 3 / 4 chunks each (persistent
+// workgroups 5.4 and more); with E4M3 moments 3.14 / 3.07 / 3.10 with 2 / 4 / 8, and
+// 60e6 values in BF16 190 / 174 / 190 us.
 inline int64_t adam_run(int state, int64_t chunks) {
-  return state == FP8BLK_ADAMW_F32 ? 1 : std::clamp<int64_t>(chunks / 4096, 1, 4);
+  return std::clamp<int64_t>(chunks / 4096, 1, state == FP8BLK_ADAMW_F32 ? 2 : 4);
 }
-// LDS that a workgroup of streamed FP32 moments asks for and does not use: five
-// of them to a compute unit instead of six took 4.55 ms, six 4.71, four 4.76.
-constexpr unsigned kAdamRoom = 32000;
+// LDS that a workgroup of a streamed table asks for and does not use, so that
+// five of them share a compute unit (four with BF16 moments), not seven: the fewer
+// places memory is worked on at once, the better.  FP32 moments 4.67 ms with five,
+// 4.76 with six, 4.78 with four; BF16 throughout 174.4 us with four, 174.9 with
+// five, 178 with seven; E4M3 3.07 / 3.09 / 3.15 ms with four / five / seven, but
+// without copies and FP32 gradients 730 / 698 / 702 us (0.27e9 values).
+inline unsigned adam_room(int state) { return state == FP8BLK_ADAMW_BF16 ? 40000 : 32000; }
 
 inline bool state_ok(int state) {
   return state == FP8BLK_ADAMW_F32 || state == FP8BLK_ADAMW_BF16 || state == FP8BLK_ADAMW_E4M3;
@@ -465,7 +526,7 @@ extern "C" fp8blk_status_t fp8blk_adamw_step(const void* table, int64_t n, int64
   const dim3 grid((unsigned)std::min<int64_t>(ceil_div(chunks, adam_run(state, chunks)), 0xFFFFFF)), block(256);
   const AdamEntry* tab = reinterpret_cast<const AdamEntry*>(table);
   const bool random = s->flags & FP8BLK_ADAMW_RANDOM, nt = adam_stream(chunks);
-  const unsigned room = nt && state == FP8BLK_ADAMW_F32 ? kAdamRoom : 0;
+  const unsigned room = nt ? adam_room(state) : 0;
 #define FP8BLK_ADAMW_LAUNCH(ST_)                                                                                    \
   hipLaunchKernelGGL((nt ? k_adamw<ST_, true> : k_adamw<ST_, false>), grid, block, room, as_stream(stream), tab, n, chunks, \
                      a, random)

@@ -254,6 +254,24 @@ def test_tiny_and_huge_moments():
     _check(s, before, [g], 1.0, False, 1, eps=1e-20)
 
 
+def test_roots_are_rounded_correctly():
+    """The root of every moment from the smallest subnormal on: p = -1 / sqrt(v) where m = 1, in FP32 bit for bit."""
+    g = torch.Generator().manual_seed(3)
+    n = 1 << 20
+    bits = torch.randint(1, 0x7F000000, (n,), generator=g, dtype=torch.int64)  # halves of finite values
+    bits[:64] = torch.arange(1, 65)
+    bits[64:4160] = 0x0D800000 - 2048 + torch.arange(4096)  # around 2^-100
+    x = bits.to(torch.int32).view(F32)
+    x[4160:4160 + 4096] = torch.arange(1, 4097).float() ** 2 * 2.0 ** -60  # exact roots, and their neighbours
+    x[9000:9000 + 4096] = torch.nextafter(x[4160:4160 + 4096], torch.tensor(3e38))
+    p = torch.zeros(n, device="cuda")
+    s = fb.AdamWState([p], [torch.full((n,), 2.0, device="cuda")], [(2 * x.double()).float().cuda()])
+    fb.adamw_step(fb.adamw_table(s, [torch.zeros(n, device="cuda")]), 1.0, 10000, beta1=0.5, beta2=0.5, eps=0.0)
+    assert torch.equal(s.vs[0].cpu(), x) and (s.ms[0] == 1).all()
+    want = -(np.float32(1) / np.sqrt(x.numpy()))
+    assert want.dtype == np.float32 and np.array_equal(p.cpu().numpy(), want)
+
+
 def test_refusals_on_the_gpu():
     p, g = torch.zeros(8, device="cuda"), torch.zeros(8, device="cuda")
     t = fb.adamw_table(fb.AdamWState([p]), [g])
