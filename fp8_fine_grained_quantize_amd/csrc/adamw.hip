@@ -158,7 +158,15 @@ struct Place {
   uint32_t mine;
   int count;  // of the lane's four elements, those that exist
   Lie lie;
+  int64_t row, col;  // of the first of them, unless DENSE
   __device__ __forceinline__ int64_t index() const { return base + mine; }
+  // Element j's offset, in rows of cols, ld apart.
+  __device__ __forceinline__ int64_t at(int j, int64_t cols, int64_t ld) const {
+    if (lie == DENSE) return index() + j;
+    int64_t r = row, c = col + j;
+    while (c >= cols) c -= cols, ++r;  // at most three times
+    return r * ld + c;
+  }
 };
 
 // The elements at a place of a tensor in rows of cols, ld apart (4 at once: one
@@ -166,12 +174,12 @@ struct Place {
 template <bool NT, typename T>
 __device__ __forceinline__ RawV<T, 4> load4(const T* t, const Place& w, int64_t cols, int64_t ld) {
   if (w.count == 4 && w.lie == DENSE) return load_raw<4, NT>(global(t + w.base) + w.mine);
-  if (w.count == 4 && w.lie == ROW) return load_raw<4, NT>(global(t + at(w.index(), cols, ld)));
+  if (w.count == 4 && w.lie == ROW) return load_raw<4, NT>(global(t + w.at(0, cols, ld)));
   RawV<T, 4> r{};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (j >= w.count) continue;
-    const T x = global(t)[w.lie == DENSE ? w.index() + j : at(w.index() + j, cols, ld)];
+    const T x = global(t)[w.at(j, cols, ld)];
     if constexpr (sizeof(T) == 4) r[j] = __float_as_uint(x);
     else r[j >> 1] |= (uint32_t)x << ((j & 1) * 16);
   }
@@ -180,10 +188,10 @@ __device__ __forceinline__ RawV<T, 4> load4(const T* t, const Place& w, int64_t 
 template <bool NT, typename T>
 __device__ __forceinline__ void store4(T* t, const float (&v)[4], const Place& w, int64_t cols, int64_t ld) {
   if (w.count == 4 && w.lie == DENSE) return store_v<4, NT>(global(t + w.base) + w.mine, v);
-  if (w.count == 4 && w.lie == ROW) return store_v<4, NT>(global(t + at(w.index(), cols, ld)), v);
+  if (w.count == 4 && w.lie == ROW) return store_v<4, NT>(global(t + w.at(0, cols, ld)), v);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (j < w.count) global(t)[w.lie == DENSE ? w.index() + j : at(w.index() + j, cols, ld)] = from_f32<T>(v[j]);
+    if (j < w.count) global(t)[w.at(j, cols, ld)] = from_f32<T>(v[j]);
 }
 
 // The moments' type as stored, and what a lane loads of them.
@@ -367,7 +375,11 @@ struct AdamRange {
     const Lie lie = !e.pitched ? DENSE : (e.cols & 3) == 0 ? ROW : ROWS;
     for (; base < hi; base += kChunk) {
       const int left = (int)max((int64_t)0, min((int64_t)4, hi - base - mine));
-      const Place w{base, mine, left, lie};
+      Place w{base, mine, left, lie};
+      if (lie != DENSE) {  // one division for every tensor and value
+        w.row = w.index() / e.cols;
+        w.col = w.index() - w.row * e.cols;
+      }
       finish(load(w), w);
     }
   }
