@@ -17,8 +17,8 @@
 // moments rounded at random 3.12 ms (5.5 TB/s); 60e6 values in BF16 throughout,
 // without copies, 172 us (4.9 TB/s counting 14 bytes a value); 1.2e6 values in 200
 // tensors 9 us, three dependent reads of the table and one of the data.  With E4M3
-// moments the vector instructions, some 100 a value, take nearly as long as the
-// bytes: a root by root_of, a scale's reciprocal by one Newton step, magnitudes
+// moments the vector instructions, 96 a value, take three quarters of the time (121
+// of them all of it): a root by root_of, a scale's reciprocal by one Newton step, magnitudes
 // without signs, and addresses in scalar registers took 0.27e9 values without
 // copies from 829 to 752 us (BF16 parameters, to nearest: 700 to 615).
 //
