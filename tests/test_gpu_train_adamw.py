@@ -344,6 +344,38 @@ def test_streams_and_graph():
         assert all(same), (k, same)
 
 
+@pytest.mark.parametrize("kind", [F32, BF, E4])
+@pytest.mark.parametrize("pt,gt", [(F32, BF), (BF, F32)])
+@pytest.mark.parametrize("large", [17_000_003, 36_000_131])
+def test_many_chunks_of_a_workgroup(kind, pt, gt, large):
+    """A table whose workgroups take several chunks, cached and streamed: the bits that its parts get in short tables."""
+    print(f"[train] adamw many chunks {kind} {pt} {gt} {large}", flush=True)
+    sizes = [large] + [1024 * k + d for k in range(7) for d in (1, 1023, 500)]
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    P = [torch.randn(n, generator=gen, device="cuda").to(pt) for n in sizes]
+    G = [(torch.randn(n, generator=gen, device="cuda") * 1e-2).to(gt) for n in sizes]
+    C = [torch.zeros(n, dtype=BF, device="cuda") for n in sizes]
+
+    def step(p, c, g):
+        s = fb.AdamWState(p, dtype=kind, decay=0.1, copies=c)
+        t = fb.adamw_table(s, g)
+        for k in (1, 2):
+            fb.adamw_step(t, LR, k, beta1=B1, beta2=B2, eps=EPS)
+        return [t for part in zip(*(x for x in (p, s.ms, s.vs, c, s.m_scales, s.v_scales) if x[0] is not None)) for t in part]
+
+    first, part = [p.clone() for p in P], 1024 * 4000
+    cuts = [list(torch.split(x[0], part)) for x in (first, C, G)]
+    got = step(P, C, G)
+    per = len(got) // len(sizes)
+    want = step(first[1:], [torch.zeros_like(c) for c in C[1:]], G[1:])
+    assert all(torch.equal(a, b) for a, b in zip(got[per:], want))
+    whole = got[:per]  # the large one's, against its pieces
+    for i, (p, c, g) in enumerate(zip(*cuts)):
+        for whole_t, t in zip(whole, step([p], [torch.zeros_like(c)], [g])):
+            lo = i * (part if whole_t.numel() == large else part // 128)
+            assert torch.equal(whole_t[lo:lo + t.numel()], t), (i, t.dtype)
+
+
 @pytest.mark.parametrize("kind", [BF, E4])
 def test_past_32_bits(kind):
     """The end of a tensor of more than 2^32 bytes equals the same values in a short one."""
