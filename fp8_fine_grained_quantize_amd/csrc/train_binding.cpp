@@ -75,6 +75,18 @@ void quantized(const Product& p, int64_t cols, const Tensor* oq, const Tensor* o
   s = os != nullptr ? *os : vec({cols / 128, p.M}, at::kFloat, *p.A);
 }
 
+// An output and u, another one or what the gradient reads: they share no memory (du may be u, element for element).
+void apart(const Tensor& t, int64_t ld, const Tensor& u, int64_t ldu, const char* what) {
+  if (!t.defined() || t.numel() == 0 || u.numel() == 0) return;
+  const auto span = [](const Tensor& x, int64_t pitch) {
+    const int64_t size = x.element_size();
+    return Span{static_cast<int64_t>(reinterpret_cast<uintptr_t>(addr(x))), x.size(1) * size, pitch * size, x.size(0)};
+  };
+  const Span a = span(t, ld), b = span(u, ldu);
+  if (t.scalar_type() == u.scalar_type() && a.base == b.base && a.width == b.width && a.pitch == b.pitch) return;
+  if (a.base < b.end() && b.base < a.end() && meet(a, b)) value_error(std::string(what) + " shares memory with u");
+}
+
 // The given workspace, or a new one of that size (none for 0 bytes).
 Tensor room(const Tensor* given, size_t bytes, const Tensor& like) {
   if (given != nullptr) return *given;
@@ -100,6 +112,10 @@ PyObject* gated_gemm(PyObject* const* a) {
   if (ou != nullptr || want_u) u = output(ou, p.M, 2 * H, at::kBFloat16, *p.A, "u", ldu);
   if (oh != nullptr || want_h || !quantize) h = output(oh, p.M, H, at::kBFloat16, *p.A, "h", ldh);
   if (quantize) quantized(p, H, oq, os, q, s, ldq);
+  if (u.defined()) {
+    apart(h, ldh, u, ldu, "h");
+    apart(q, ldq, u, ldu, "q");
+  }
   const uint32_t flags = pow2 ? FP8BLK_SCALE_POW2 : 0;
   auto* qp = q.defined() ? static_cast<uint8_t*>(addr(q)) : nullptr;
   auto* sp = s.defined() ? static_cast<float*>(addr(s)) : nullptr;
@@ -140,6 +156,9 @@ PyObject* gated_gemm_backward(PyObject* const* a) {
   if (od != nullptr || want_du || !quantize) du = output(od, p.M, 2 * H, at::kBFloat16, *p.A, "du", lddu);
   if (oh != nullptr || want_h) h = output(oh, p.M, H, at::kBFloat16, *p.A, "h", ldh);
   if (quantize) quantized(p, 2 * H, oq, os, q, s, ldq);
+  apart(du, lddu, u, ldu, "du");
+  apart(h, ldh, u, ldu, "h");
+  apart(q, ldq, u, ldu, "q");
   const uint32_t flags = pow2 ? FP8BLK_SCALE_POW2 : 0;
   auto* qp = q.defined() ? static_cast<uint8_t*>(addr(q)) : nullptr;
   auto* sp = s.defined() ? static_cast<float*>(addr(s)) : nullptr;

@@ -385,3 +385,35 @@ def test_refuses():
     for call in (lambda: f(x, sx, w, sw, u=shifted), lambda: b(x, sx, w[:, :256].contiguous(), sw[:, :2].contiguous(), shifted)):
         with pytest.raises(fb.Fp8BlkError):
             call()
+
+
+def test_refuses_outputs_in_u():
+    """du is u element for element or shares nothing with it; h and q share nothing with it."""
+    x, sx = fb.quantize_1x128(_bf16((8, 256), 1))
+    d, sd = _weights(256, 256, 2, False)
+    room = _bf16((17, 512), 3)
+    u = room[:8]
+    b = fb.gated_gemm_backward_fp8_blockscaled
+    want = b(x, sx, d, sd, u, opB=0)
+    for what, call in (("du", lambda: b(x, sx, d, sd, u, opB=0, du=room[1:9])),
+                       ("du", lambda: b(x, sx, d, sd, u, opB=0, du=room[:16:2])),
+                       ("h", lambda: b(x, sx, d, sd, u, opB=0, h=u[:, 256:])),
+                       ("q", lambda: b(x, sx, d, sd, u, opB=0, quantize=True, q=u.view(torch.uint8)[:, :512]))):
+        with pytest.raises(ValueError, match=f"^{what} shares memory with u"):
+            call()
+    w, sw = _weights(256, 512, 4, False)
+    with pytest.raises(ValueError, match="^h shares memory with u"):
+        fb.gated_gemm_fp8_blockscaled(x, sx, w, sw, u=u, h=u[:, :256])
+    off = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="^du shares memory with u"):
+        fb.grouped_gated_gemm_backward_fp8_blockscaled(off, x, sx, d[None], sd[None], u, opB=0, du=room[1:9])
+    spaced = room[1:17].view(8, 1024)[:, 512:]  # rows between u's, from a u whose rows lie apart
+    between = room[1:17].view(8, 1024)[:, :512]
+    between.copy_(u.clone())
+    kept = between.clone()
+    got = b(x, sx, d, sd, between, opB=0, du=spaced)
+    ref_ = b(x, sx, d, sd, kept, opB=0)
+    assert torch.equal(got.du, ref_.du) and torch.equal(got.h, ref_.h) and torch.equal(between, kept)
+    same = kept.clone()
+    assert torch.equal(b(x, sx, d, sd, same, opB=0, du=same).du, ref_.du) and torch.equal(same, ref_.du)
+    assert want.du.shape == (8, 512)
