@@ -29,6 +29,7 @@
 // nothing to cover its end (a quantizer of its own 19 and a launch), and 90 us for
 // the experts (148).
 #include <algorithm>
+#include <cmath>
 
 #include "../../include/libfp8blk_train.h"
 #include "gemm_tile.h"
@@ -700,10 +701,10 @@ struct GatedForm {
 inline GatedForm gated_form(int64_t M, int64_t N, int64_t K, bool gradient, bool may_split) {
   const int64_t n = ceil_div(N, 256), cus = device_cus(), G = K / 128;
   GatedForm best{256, 1};
-  int64_t least = INT64_MAX;
-  auto fused = [&](int rows, int64_t group) {
+  double least = INFINITY;
+  auto fused = [&](int rows, int group) {
     const int64_t rounds = ceil_div(std::min<int64_t>(ceil_div(M, rows), 1 << 20) * std::min<int64_t>(n, 1 << 20), cus);
-    const int64_t ns = (gradient ? 5200 : 3300) + group * G * rounds;
+    const double ns = (gradient ? 5200 : 3300) + (double)group * G * rounds;
     if (ns < least) least = ns, best = {rows, 1};
   };
   fused(256, 1330);
@@ -715,7 +716,7 @@ inline GatedForm gated_form(int64_t M, int64_t N, int64_t K, bool gradient, bool
     const int64_t tiles = ceil_div(M, rows) * n;
     for (int64_t s = 2; s <= 16 && s <= G; ++s) {
       const int64_t per = ceil_div(G, s), S = ceil_div(G, per);
-      const int64_t ns = 5200 + (rows == 64 ? 470 : 420) * per * ceil_div(tiles * S, cus) + S * M * N * 3 / 2000;
+      const double ns = 5200.0 + (rows == 64 ? 470 : 420) * per * ceil_div(tiles * S, cus) + S * M * N * 3 / 2000;
       if (ns < least) least = ns, best = {rows, S};
     }
   }
@@ -890,7 +891,8 @@ inline void launch_join(const float* partials, int64_t S, const GatedArgs& a, co
 }
 
 inline size_t gated_bytes(int64_t M, int64_t H, int64_t K, int64_t N) {
-  if (M <= 0 || H <= 0 || K <= 0 || H % 128 != 0 || K % 128 != 0 || M > kGatedMost || H > kGatedMost) return 0;
+  if (M <= 0 || H <= 0 || K <= 0 || H % 128 != 0 || K % 128 != 0) return 0;
+  if (M > kGatedMost || H > kGatedMost || K > kGatedMost) return 0;
   const int64_t S = gated_form(M, N, K, N == H, true).splits;
   return S > 1 ? (size_t)(S * M * N) * sizeof(float) : 0;
 }

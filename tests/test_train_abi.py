@@ -214,6 +214,8 @@ def test_gated_refuses():
     w = fb.lib().fp8blk_gated_gemm_workspace_bytes
     assert w(0, 256, 384) == 0 and w(16, 100, 384) == 0 and w(16, 256, 100) == 0 and w(-1, 256, 384) == 0
     assert w(8192, 2048, 7168) == 0 and w(2 ** 62, 2 ** 62 - 2 ** 62 % 128, 128) == 0
+    most = 2 ** 31  # sizes whose products pass 64 bits
+    assert w(most, most, most) == 0 and w(16, 256, 2 ** 62) == 0 and w(most + 1, 256, 128) == 0
     assert w(16, 256, 7168) >= 2 * 16 * 512 * 4 and w(16, 256, 7168) % (16 * 512 * 4) == 0  # two parts or more
 
 
