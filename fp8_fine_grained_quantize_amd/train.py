@@ -262,8 +262,12 @@ def _entries(state: AdamWState, grads):
         if p.numel() == 0:
             continue
         c = state.copies[i]
-        spans = [_rows(t, _order(p)) for t in (p, g, c) if t is not None]
-        same = _same_rows(spans) if None not in spans else None
+        if p.is_contiguous() and g.is_contiguous() and (c is None or c.is_contiguous()):
+            same = 1, p.numel(), (p.numel(),) * 3
+        else:
+            order = _order(p)
+            spans = [_rows(t, order) for t in (p, g, c) if t is not None]
+            same = _same_rows(spans) if None not in spans else None
         if same is None:
             raise ValueError(f"parameter {i}, its gradient and its copy must lie in memory in the same order, in rows")
         rows, cols, ld = same
@@ -296,8 +300,9 @@ class AdamWTable:
             raise TypeError("state must be an AdamWState")
         self.state, self.grads = state, _per_tensor(grads, len(state.params), "gradients")
         self.device = state.params[0].device if state.params else torch.device("cuda", torch.cuda.current_device())
+        here = not state.params or _stream(state.params[0]) is not None
         for t in (*state.params, *self.grads):
-            if t.device != self.device or _stream(t) is None:
+            if t.device != self.device or not here:
                 raise ValueError(f"expected tensors on the current GPU, got {t.device}")
         entries = _entries(state, self.grads)
         L = _fb.lib()
