@@ -183,6 +183,63 @@ PyObject* gated_gemm_backward(PyObject* const* a) {
 
 // --- AdamW -------------------------------------------------------------------
 
+// A list or tuple of n tensors (or None, where that may be).
+struct Tensors {
+  PyObject* fast;
+  const char* what;
+  Tensors(PyObject* o, const char* what_) : fast(PySequence_Fast(o, "a state's tensors must be lists")), what(what_) {
+    if (fast == nullptr) throw python_error();
+  }
+  Tensors(const Tensors&) = delete;
+  Tensors& operator=(const Tensors&) = delete;
+  ~Tensors() { Py_DECREF(fast); }
+  int64_t size() const { return PySequence_Fast_GET_SIZE(fast); }
+  const Tensor* at(int64_t i) const { return maybe(PySequence_Fast_GET_ITEM(fast, i), what); }
+};
+
+// That a state's tensors fit each other.  A table asks it anew: a parameter's
+// memory may be another one, of another size, type or device, since the state
+// was built (a module moved or sharded under its parameters), as may what its
+// lists hold, and the kernel takes every size from the parameter.
+PyObject* adamw_check(PyObject* const* a) {  // params, ms, vs, m_scales, v_scales, copies, state
+  const Tensors params(a[0], "parameters"), copies(a[5], "copies");
+  const Tensors moments[2] = {{a[1], "moments"}, {a[2], "moments"}}, scales[2] = {{a[3], "scales"}, {a[4], "scales"}};
+  const int64_t state = integer(a[6]), n = params.size();
+  for (const Tensors* t : {&moments[0], &moments[1], &scales[0], &scales[1], &copies})
+    if (t->size() != n)
+      value_error(std::to_string(n) + " parameters, " + std::to_string(t->size()) + " " + t->what);
+  const ScalarType kind = state == FP8BLK_ADAMW_F32 ? at::kFloat : state == FP8BLK_ADAMW_BF16 ? at::kBFloat16 : at::kByte;
+  const auto none = [](const char* what, const std::string& of) { type_error(std::string(what) + of + " must be tensors"); };
+  for (int64_t i = 0; i < n; ++i) {
+    const auto of = [&] { return " of parameter " + std::to_string(i); };
+    if (params.at(i) == nullptr) type_error("parameter " + std::to_string(i) + " must be a tensor");
+    const Tensor& p = *params.at(i);
+    is_f32(p, "parameters");
+    if (p.device() != params.at(0)->device())
+      value_error("parameter " + std::to_string(i) + " is on " + p.device().str() + ", the first one on " +
+                  params.at(0)->device().str());
+    const auto fits = [&](const Tensors& list, ScalarType dtype, int64_t count, const char* counted) {
+      const Tensor* t = list.at(i);
+      if (t == nullptr) none(list.what, of());
+      if (t->scalar_type() != dtype)
+        type_error(list.what + of() + " must be " + c10::toString(dtype) + ", got " + c10::toString(t->scalar_type()));
+      if (t->numel() != count || !t->is_contiguous() || t->device() != p.device())
+        value_error(list.what + of() + " must be contiguous, " + counted + " (" + std::to_string(count) + "), on " +
+                    p.device().str());
+    };
+    for (const Tensors& list : moments) fits(list, kind, p.numel(), "one for each element");
+    if (state == FP8BLK_ADAMW_E4M3)
+      for (const Tensors& list : scales) fits(list, at::kFloat, (p.numel() + 127) / 128, "one for 128 elements");
+    const Tensor* c = copies.at(i);
+    if (c == nullptr) continue;
+    if (c->scalar_type() != at::kBFloat16)
+      type_error("copy " + std::to_string(i) + " must be bfloat16, got " + c10::toString(c->scalar_type()));
+    if (c->sizes() != p.sizes() || c->device() != p.device())
+      value_error("copy " + std::to_string(i) + " must have the parameter's shape and device");
+  }
+  Py_RETURN_NONE;
+}
+
 // Two tensors of a list that a step must not take together: memory that one of
 // them writes is the other's too.  Returns None, or (entry, name, entry, name).
 PyObject* adamw_shared(PyObject* const* a) {  // address of the entries, their number, state
@@ -281,6 +338,7 @@ PyObject* adamw_step(PyObject* const* a) {
 
 PyMethodDef fp8blk_train_methods[] = {FP8BLK_METHOD(gated_gemm, 20),
                                       FP8BLK_METHOD(gated_gemm_backward, 21),
+                                      FP8BLK_METHOD(adamw_check, 7),
                                       FP8BLK_METHOD(adamw_shared, 3),
                                       FP8BLK_METHOD(adamw_step, 14),
                                       {nullptr, nullptr, 0, nullptr}};

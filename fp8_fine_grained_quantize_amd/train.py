@@ -235,25 +235,19 @@ class AdamWState:
             self.decay = [float(d) for d in decay]
         if len(self.decay) != n:
             raise ValueError(f"{n} parameters, {len(self.decay)} decays")
-        for i, p in enumerate(self.params):
-            for t in (self.ms[i], self.vs[i]):
-                if t.numel() != p.numel() or not t.is_contiguous() or t.device != p.device:
-                    raise ValueError(f"moments of parameter {i} must be contiguous, of {p.numel()} elements, on {p.device}")
-            for t in (self.m_scales[i], self.v_scales[i]) if codes else ():
-                if t.dtype != torch.float32:
-                    raise TypeError(f"scales of parameter {i} must be float32, got {t.dtype}")
-                if t.numel() != -(-p.numel() // 128) or not t.is_contiguous() or t.device != p.device:
-                    raise ValueError(f"scales of parameter {i} must be contiguous, one for 128 elements, on {p.device}")
-            c = self.copies[i]
-            if c is not None:
-                if c.dtype != torch.bfloat16:
-                    raise TypeError(f"copy {i} must be bfloat16, got {c.dtype}")
-                if c.shape != p.shape or c.device != p.device or _overlaps(c):
-                    raise ValueError(f"copy {i} must have the parameter's shape and device, and memory for every element")
+        self._check()
+        for i, c in enumerate(self.copies):
+            if c is not None and _overlaps(c):
+                raise ValueError(f"copy {i} must have memory for every element")
+
+    def _check(self):
+        """That the tensors still fit each other: sizes, types, devices (ValueError or TypeError)."""
+        _ext().adamw_check(self.params, self.ms, self.vs, self.m_scales, self.v_scales, self.copies, self.state)
 
 
 def _entries(state: AdamWState, grads):
     """The table entries of a state and its gradients; empty tensors have none."""
+    state._check()
     entries = []
     for i, (p, g) in enumerate(zip(state.params, grads)):
         if g.shape != p.shape:
@@ -293,7 +287,8 @@ class AdamWTable:
     one whose gradients are new tensors every step builds one a step.  A
     parameter's gradient and copy lie in memory in the order of its dimensions
     (any row pitch each); tensors that a step writes share no memory with any
-    other."""
+    other.  The state's tensors are checked anew for every table, since a
+    parameter's memory may have changed with its module."""
 
     def __init__(self, state: AdamWState, grads: Sequence[torch.Tensor]):
         if not isinstance(state, AdamWState):
