@@ -75,16 +75,68 @@ void quantized(const Product& p, int64_t cols, const Tensor* oq, const Tensor* o
   s = os != nullptr ? *os : vec({cols / 128, p.M}, at::kFloat, *p.A);
 }
 
-// An output and u, another one or what the gradient reads: they share no memory (du may be u, element for element).
-void apart(const Tensor& t, int64_t ld, const Tensor& u, int64_t ldu, const char* what) {
-  if (!t.defined() || t.numel() == 0 || u.numel() == 0) return;
-  const auto span = [](const Tensor& x, int64_t pitch) {
-    const int64_t size = x.element_size();
-    return Span{static_cast<int64_t>(reinterpret_cast<uintptr_t>(addr(x))), x.size(1) * size, pitch * size, x.size(0)};
-  };
-  const Span a = span(t, ld), b = span(u, ldu);
-  if (t.scalar_type() == u.scalar_type() && a.base == b.base && a.width == b.width && a.pitch == b.pitch) return;
-  if (a.base < b.end() && b.base < a.end() && meet(a, b)) value_error(std::string(what) + " shares memory with u");
+// A tensor of a call by its name, and the bytes it covers: `pieces` times rows, `apart` bytes from one to the next.
+struct Named {
+  const Tensor* t;
+  const char* name;
+};
+struct Bytes {
+  Span at;
+  int64_t pieces = 1, apart = 0;
+  int64_t end() const { return at.end() + (pieces - 1) * apart; }
+  explicit Bytes(const Tensor& t) {
+    const int64_t size = t.element_size(), d = t.dim();
+    at.base = static_cast<int64_t>(reinterpret_cast<uintptr_t>(addr(t)));
+    const auto reach = [&](int64_t i) { return (t.size(i) - 1) * t.stride(i) * size; };
+    at.width = size + (d > 0 ? reach(d - 1) : 0);
+    at.pitch = at.width;
+    at.rows = 1;
+    if (d > 1 && t.size(d - 2) > 1) {
+      at.pitch = t.stride(d - 2) * size;
+      at.rows = t.size(d - 2);
+    }
+    if (d > 2) {
+      pieces = t.size(d - 3);
+      apart = t.stride(d - 3) * size;
+    }
+    if (d <= 3 && at.pitch >= at.width) return;
+    at.width = size;  // of another kind, refused by its shape or strides: all that it reaches over
+    for (int64_t i = 0; i < d; ++i) at.width += reach(i);
+    at.pitch = at.width;
+    at.rows = pieces = 1;
+  }
+};
+bool meet(const Bytes& a, const Bytes& b) {
+  if (a.at.base >= b.end() || b.at.base >= a.end()) return false;
+  for (int64_t i = 0; i < a.pieces; ++i)
+    for (int64_t j = 0; j < b.pieces; ++j) {
+      Span p = a.at, q = b.at;
+      p.base += i * a.apart;
+      q.base += j * b.apart;
+      if (p.base < q.end() && q.base < p.end() && fp8blk_py::meet(p, q)) return true;
+    }
+  return false;
+}
+
+// What a call writes, among itself and with what it reads: workgroups run in
+// any order, so none of it may lie in another's memory.  `onto`: an output that
+// may be that input element for element (each lane reads its own before it writes).
+void apart(std::initializer_list<Named> outs, std::initializer_list<Named> ins, const Tensor* onto = nullptr) {
+  const auto real = [](const Named& n) { return n.t != nullptr && n.t->numel() != 0; };
+  for (const Named* o = outs.begin(); o != outs.end(); ++o) {
+    if (!real(*o)) continue;
+    const Bytes a(*o->t);
+    const auto check = [&](const Named& n, bool may_be_same) {
+      if (!real(n)) return;
+      const Bytes b(*n.t);
+      if (may_be_same && n.t == onto && o->t->scalar_type() == n.t->scalar_type() && a.at.base == b.at.base &&
+          a.at.width == b.at.width && a.at.pitch == b.at.pitch && a.at.rows == b.at.rows)
+        return;
+      if (meet(a, b)) value_error(std::string(o->name) + " shares memory with " + n.name);
+    };
+    for (const Named& n : ins) check(n, o == outs.begin());
+    for (const Named* n = outs.begin(); n != o; ++n) check(*n, false);
+  }
 }
 
 // The given workspace, or a new one of that size (none for 0 bytes).
@@ -103,19 +155,17 @@ PyObject* gated_gemm(PyObject* const* a) {
   if (p.N % 256 != 0) value_error("B must have the gate's columns and as many of the up projection, got " + sizes(*p.B));
   if (!quantize && (oq != nullptr || os != nullptr)) value_error("q and s need quantize");
   scratch(w);
+  own({w, ou, oh, oq, os});
+  apart({{ou, "u"}, {oh, "h"}, {oq, "q"}, {os, "s"}, {split ? w : nullptr, "workspace"}},
+        {{p.A, "A"}, {p.sA, "sA"}, {p.B, "B"}, {p.sB, "sB"}, {p.offsets, "offsets"}});
   void* stream = stream_of(a[10], *p.A, {p.offsets, p.sA, p.B, p.sB, w, ou, oh, oq, os});
   Unlocked unlocked;
-  own({w, ou, oh, oq, os});
   const int64_t H = p.N / 2;
   int64_t ldu = 0, ldh = 0, ldq = 0;
   Tensor u, h, q, s;
   if (ou != nullptr || want_u) u = output(ou, p.M, 2 * H, at::kBFloat16, *p.A, "u", ldu);
   if (oh != nullptr || want_h || !quantize) h = output(oh, p.M, H, at::kBFloat16, *p.A, "h", ldh);
   if (quantize) quantized(p, H, oq, os, q, s, ldq);
-  if (u.defined()) {
-    apart(h, ldh, u, ldu, "h");
-    apart(q, ldq, u, ldu, "q");
-  }
   const uint32_t flags = pow2 ? FP8BLK_SCALE_POW2 : 0;
   auto* qp = q.defined() ? static_cast<uint8_t*>(addr(q)) : nullptr;
   auto* sp = s.defined() ? static_cast<float*>(addr(s)) : nullptr;
@@ -148,17 +198,16 @@ PyObject* gated_gemm_backward(PyObject* const* a) {
   if (!quantize && (oq != nullptr || os != nullptr)) value_error("q and s need quantize");
   const int64_t H = p.N, ldu = pitch(u, at::kBFloat16, p.M, 2 * H, "u");
   scratch(w);
+  own({w, od, oh, oq, os});
+  apart({{od, "du"}, {oh, "h"}, {oq, "q"}, {os, "s"}, {split ? w : nullptr, "workspace"}},
+        {{&u, "u"}, {p.A, "A"}, {p.sA, "sA"}, {p.B, "B"}, {p.sB, "sB"}, {p.offsets, "offsets"}}, &u);
   void* stream = stream_of(a[11], *p.A, {p.offsets, p.sA, p.B, p.sB, &u, w, od, oh, oq, os});
   Unlocked unlocked;
-  own({w, od, oh, oq, os});
   int64_t lddu = 0, ldh = 0, ldq = 0;
   Tensor du, h, q, s;
   if (od != nullptr || want_du || !quantize) du = output(od, p.M, 2 * H, at::kBFloat16, *p.A, "du", lddu);
   if (oh != nullptr || want_h) h = output(oh, p.M, H, at::kBFloat16, *p.A, "h", ldh);
   if (quantize) quantized(p, 2 * H, oq, os, q, s, ldq);
-  apart(du, lddu, u, ldu, "du");
-  apart(h, ldh, u, ldu, "h");
-  apart(q, ldq, u, ldu, "q");
   const uint32_t flags = pow2 ? FP8BLK_SCALE_POW2 : 0;
   auto* qp = q.defined() ? static_cast<uint8_t*>(addr(q)) : nullptr;
   auto* sp = s.defined() ? static_cast<float*>(addr(s)) : nullptr;

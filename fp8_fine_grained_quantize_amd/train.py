@@ -86,7 +86,8 @@ def gated_gemm_fp8_blockscaled(A, sA, B, sB, act: str = "silu", opB: int = 0, po
     bf16 [M][2H] unless want_u is False, h bf16 [M][H], and with quantize (q uint8 [M][H], s float32
     [H/128][M]) = quantize_1x128(h, pow2); want_h=False then leaves h out.  H and K are multiples of 128.
     split_k: a product of few rows is split over the GPU, with a workspace allocated here unless given (which
-    no other work, a captured graph's neither, may use at the same time).  Outputs share no memory with inputs."""
+    no other work, a captured graph's neither, may use at the same time).  Outputs and the workspace share no memory
+    with each other or with inputs."""
     return GatedGemm(*_ext().gated_gemm(None, A, sA, B, sB, _act(act), opB, pow2_scales, None, quantize, pow2, want_h,
                                         want_u, split_k, workspace, u, h, q, s, _stream(A)))
 
@@ -110,9 +111,9 @@ def gated_gemm_backward_fp8_blockscaled(A, sA, B, sB, u, act: str = "silu", opB:
     """Gradient of h = act(u[:, :H]) * u[:, H:] and of the down projection that reads it, in one GEMM: dh = A B
     with A the codes of the gradient of the projection's output [M][K] and B its weights, [H][K] as the
     forward stored them (OP_T) or [K][H] (OP_N).  Returns du bf16 [M][2H] (du may be u itself, which it
-    replaces; outputs share no other memory with inputs), h bf16 [M][H] again for the weights' gradient unless
-    want_h is False, and with quantize (q uint8 [M][2H], s float32 [2H/128][M]) = quantize_1x128(du, pow2);
-    want_du=False then leaves du out."""
+    replaces; nothing else that is written shares memory with another argument), h bf16 [M][H] again for the
+    weights' gradient unless want_h is False, and with quantize (q uint8 [M][2H], s float32 [2H/128][M]) =
+    quantize_1x128(du, pow2); want_du=False then leaves du out."""
     return GatedGemmGrad(*_ext().gated_gemm_backward(None, A, sA, B, sB, _act(act), opB, pow2_scales, None, u, quantize, pow2,
                                                      want_h, want_du, split_k, workspace, du, h, q, s, _stream(A)))
 

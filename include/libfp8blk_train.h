@@ -49,6 +49,10 @@ int fp8blk_train_abi_version(void);
  * by other work during the call) has the bytes that the call's _workspace_bytes
  * gives; without it, one launch computes it all.  Either form gives the same
  * bits on every run.
+ *
+ * Outputs and the workspace overlap neither each other nor an input; only du
+ * may be u.  (The Python binding refuses such calls, this interface does not see
+ * the memory's owners.)
  * ------------------------------------------------------------------------ */
 enum { FP8BLK_ACT_SILU = 0, FP8BLK_ACT_GELU = 1 };
 

@@ -82,3 +82,119 @@ def test_state_unchanged():
         s.ms[0] = s.ms[0].clone()
         e, = train._entries(s, [torch.zeros(100)])
         assert e.param == p.data_ptr() and e.m == s.ms[0].data_ptr()
+
+
+# --- gated products: what they write shares no memory ---------------------------
+
+M, H, K = 8, 256, 384
+U8 = torch.uint8
+
+
+def _operands(N, G=None):
+    of = [] if G is None else [G]
+    return dict(A=torch.zeros(M, K, dtype=U8), sA=torch.zeros(K // 128, M), B=torch.zeros(*of, K, N, dtype=U8),
+                sB=torch.zeros(*of, K // 128, N // 128))
+
+
+def _outputs(**width):
+    """u, h, q, s or du, h, q, s of the given widths, a lent workspace too."""
+    d = {k: torch.zeros(M, n, dtype=U8 if k == "q" else BF) for k, n in width.items()}
+    return dict(d, s=torch.zeros(d["q"].shape[1] // 128, M), workspace=torch.zeros(4096))
+
+
+def _forward(offsets=None, **kw):
+    if offsets is None:
+        return fb.gated_gemm_fp8_blockscaled(quantize=True, **kw)
+    kw.pop("workspace")
+    return fb.grouped_gated_gemm_fp8_blockscaled(offsets, quantize=True, **kw)
+
+
+def _backward(offsets=None, **kw):
+    if offsets is None:
+        return fb.gated_gemm_backward_fp8_blockscaled(quantize=True, opB=0, **kw)
+    kw.pop("workspace")
+    return fb.grouped_gated_gemm_backward_fp8_blockscaled(offsets, quantize=True, opB=0, **kw)
+
+
+CALLS = [(_forward, 2 * H, dict(u=2 * H, h=H, q=H)), (_backward, H, dict(du=2 * H, h=H, q=2 * H))]
+
+
+def _call(f, N, widths, G):
+    kw = dict(_operands(N, G), **_outputs(**widths))
+    if f is _backward:
+        kw["u"] = torch.zeros(M, 2 * H, dtype=BF)
+    offsets = None if G is None else torch.zeros(G + 1, dtype=torch.int32)
+    return kw, offsets
+
+
+@pytest.mark.parametrize("f,N,widths", CALLS)
+@pytest.mark.parametrize("G", [None, 3])
+def test_outputs_share_memory(f, N, widths, G):
+    """Each output in each other one's, each operand's and the workspace's memory, at its first byte."""
+    kw, offsets = _call(f, N, widths, G)
+    with pytest.raises(ValueError, match="current GPU"):  # nothing shared: refused as CPU tensors only
+        f(offsets, **kw)
+    inputs = ["A", "sA", "B", "sB"] + (["u"] if f is _backward else []) + ([] if G is None else ["offsets"])
+    outputs = [*widths, "s"] + (["workspace"] if G is None else [])
+    for o in outputs:
+        for other in inputs + outputs:
+            if o == other or {o, other} == {"du", "u"}:
+                continue
+            kw, offsets = _call(f, N, widths, G)
+            room = torch.zeros(1 << 21, dtype=U8)
+            for k in (o, other):
+                t = offsets if k == "offsets" else kw[k]
+                t = room.view(t.dtype).as_strided(t.shape, t.stride())
+                if k == "offsets":
+                    offsets = t
+                else:
+                    kw[k] = t
+            with pytest.raises(ValueError, match=f"^({o} shares memory with {other}|{other} shares memory with {o})$"):
+                f(offsets, **kw)
+
+
+@pytest.mark.parametrize("f,N,widths", CALLS)
+def test_outputs_that_only_touch(f, N, widths):
+    """Rows between rows, one after another in one buffer, and the last byte."""
+    kw, _ = _call(f, N, widths, None)
+    first, wide = list(widths)[0], torch.zeros(M, 3 * H, dtype=BF)
+    kw[first], kw["h"] = wide[:, :2 * H], wide[:, 2 * H:]
+    with pytest.raises(ValueError, match="current GPU"):
+        f(**kw)
+    kw["h"] = wide[:, 2 * H - 1:3 * H - 1]
+    with pytest.raises(ValueError, match=f"^h shares memory with {first}$"):
+        f(**kw)
+    # experts' weights whose matrices lie apart, an output in the space between them, and one byte too far
+    kw, _ = _call(f, N, widths, 3)
+    room = torch.zeros(3, K * N + M * H * 2, dtype=U8)
+    kw["B"] = room[:, :K * N].as_strided((3, K, N), (room.stride(0), N, 1))
+    gap = room[1].view(BF)[K * N // 2:].view(M, H)
+    offsets = torch.zeros(4, dtype=torch.int32)
+    kw["h"] = gap
+    with pytest.raises(ValueError, match="current GPU"):
+        f(offsets, **kw)
+    kw["h"] = room.view(-1).view(BF)[(room.stride(0) + K * N) // 2 - 1:][:M * H].view(M, H)
+    with pytest.raises(ValueError, match="^h shares memory with B$"):
+        f(offsets, **kw)
+
+
+def test_gradient_in_place():
+    kw, _ = _call(*CALLS[1], None)
+    for du in (kw["u"], kw["u"].view(M, 2 * H)):  # u itself
+        with pytest.raises(ValueError, match="current GPU"):
+            _backward(**dict(kw, du=du))
+    room = torch.zeros(2 * M + 1, 2 * H, dtype=BF)
+    kw["u"] = room[:M]
+    for du in (room[1:M + 1], room[:2 * M:2], room[:M].view(torch.float16)):
+        with pytest.raises(ValueError, match="^du shares memory with u$"):
+            _backward(**dict(kw, du=du))
+    with pytest.raises(ValueError, match="^h shares memory with "):  # in place, and h there too
+        _backward(**dict(kw, du=kw["u"], h=kw["u"][:, :H]))
+
+
+def test_workspace_that_is_not_used():
+    """A call that is not split leaves its workspace alone."""
+    kw, _ = _call(*CALLS[0], None)
+    kw["workspace"] = kw["h"]
+    with pytest.raises(ValueError, match="current GPU"):
+        _forward(**kw, split_k=False)
