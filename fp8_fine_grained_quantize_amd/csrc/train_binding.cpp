@@ -3,6 +3,7 @@
 #include <ATen/ops/new_empty.h>
 
 #include <algorithm>
+#include <memory>
 #include <vector>
 
 #include "../../include/libfp8blk_train.h"
@@ -333,6 +334,73 @@ PyObject* adamw_shared(PyObject* const* a) {  // address of the entries, their n
   Py_RETURN_NONE;
 }
 
+// The memory that a table names, kept as long as the table: a step looks whether
+// the tensors still have it.  (One whose memory was replaced since would be left
+// as it is, and what it had be written behind its next owner's back.)
+struct Place {
+  c10::Storage memory;
+  const void* at;
+  int64_t entry;
+  const char* what;
+  bool written;
+};
+const void* place_of(const Tensor& t, bool written) {
+  return written ? t.mutable_data_ptr() : t.const_data_ptr();  // a copy-on-write clone that is written gets its own
+}
+std::vector<Place>& places_of(PyObject* held) {
+  if (!PyTuple_Check(held) || PyTuple_GET_SIZE(held) != 2) type_error("held must be what adamw_hold returned");
+  auto* p = static_cast<std::vector<Place>*>(PyCapsule_GetPointer(PyTuple_GET_ITEM(held, 1), "fp8blk.places"));
+  if (p == nullptr) throw python_error();
+  return *p;
+}
+
+// Returns (the tensors that a table names, their places).
+PyObject* adamw_hold(PyObject* const* a) {  // params, grads, ms, vs, m_scales, v_scales, copies
+  static const char* const names[] = {"parameter",      "gradient", "first moment", "second moment", "first moment's scales",
+                                      "second moment's scales", "copy"};
+  std::vector<PyObject*> tensors;
+  auto places = std::make_unique<std::vector<Place>>();
+  const Tensors params(a[0], names[0]);
+  for (int k = 0; k < 7; ++k) {
+    const Tensors list(a[k], names[k]);
+    for (int64_t i = 0; i < std::min(list.size(), params.size()); ++i) {
+      const Tensor* t = list.at(i);
+      if (t == nullptr || t->numel() == 0) continue;
+      const bool written = k != 1;
+      const void* at = place_of(*t, written);
+      tensors.push_back(PySequence_Fast_GET_ITEM(list.fast, i));
+      places->push_back({t->storage(), at, i, names[k], written});
+    }
+  }
+  PyObject* capsule = PyCapsule_New(places.get(), "fp8blk.places", [](PyObject* c) {
+    delete static_cast<std::vector<Place>*>(PyCapsule_GetPointer(c, "fp8blk.places"));
+  });
+  if (capsule == nullptr) throw python_error();
+  places.release();
+  PyObject* kept = PyTuple_New(static_cast<Py_ssize_t>(tensors.size()));
+  if (kept == nullptr) {
+    Py_DECREF(capsule);
+    throw python_error();
+  }
+  for (size_t i = 0; i < tensors.size(); ++i) {
+    Py_INCREF(tensors[i]);
+    PyTuple_SET_ITEM(kept, static_cast<Py_ssize_t>(i), tensors[i]);
+  }
+  return Py_BuildValue("NN", kept, capsule);
+}
+
+// Refuses a step whose tensors have other memory than when the table was built.
+void still_there(PyObject* held) {
+  const std::vector<Place>& places = places_of(held);
+  PyObject* kept = PyTuple_GET_ITEM(held, 0);
+  for (size_t i = 0; i < places.size(); ++i) {
+    const Place& p = places[i];
+    if (place_of(THPVariable_Unpack(PyTuple_GET_ITEM(kept, static_cast<Py_ssize_t>(i))), p.written) != p.at)
+      value_error(std::string(p.what) + " " + std::to_string(p.entry) +
+                  " has other memory than when the table was built: build it anew");
+  }
+}
+
 // One value on the device that a captured step reads anew at every replay, or NULL.
 const Tensor* device_value(PyObject* o, ScalarType dtype, const char* what) {
   if (!THPVariable_Check(o)) return nullptr;
@@ -342,7 +410,7 @@ const Tensor* device_value(PyObject* o, ScalarType dtype, const char* what) {
   return &t;
 }
 
-// table, n, chunks, state, lr, step, beta1, beta2, eps, norm, max_norm, clip_eps, seed, stream
+// table, n, chunks, state, lr, step, beta1, beta2, eps, norm, max_norm, clip_eps, seed, held, stream
 PyObject* adamw_step(PyObject* const* a) {
   const Tensor& table = given(a[0], "table");
   const int64_t n = integer(a[1]), chunks = integer(a[2]);
@@ -372,7 +440,8 @@ PyObject* adamw_step(PyObject* const* a) {
       s.seed = static_cast<uint32_t>(v);
     }
   }
-  void* stream = stream_of(a[13], table, {lr, step, norm, seed});
+  still_there(a[13]);
+  void* stream = stream_of(a[14], table, {lr, step, norm, seed});
   s.lr_at = static_cast<float*>(addr(lr));
   s.step_at = static_cast<int64_t*>(addr(step));
   s.seed_at = static_cast<int64_t*>(addr(seed));
@@ -388,6 +457,7 @@ PyObject* adamw_step(PyObject* const* a) {
 PyMethodDef fp8blk_train_methods[] = {FP8BLK_METHOD(gated_gemm, 20),
                                       FP8BLK_METHOD(gated_gemm_backward, 21),
                                       FP8BLK_METHOD(adamw_check, 7),
+                                      FP8BLK_METHOD(adamw_hold, 7),
                                       FP8BLK_METHOD(adamw_shared, 3),
-                                      FP8BLK_METHOD(adamw_step, 14),
+                                      FP8BLK_METHOD(adamw_step, 15),
                                       {nullptr, nullptr, 0, nullptr}};

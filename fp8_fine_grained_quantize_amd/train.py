@@ -281,12 +281,19 @@ def _shared(array, n: int, state: int):
     return f"the {a} of parameter {array[i].index} and the {b} of parameter {array[j].index}"
 
 
+def _hold(state: AdamWState, grads):
+    """The tensors of a table and the memory that it names, which it keeps."""
+    return _ext().adamw_hold(state.params, grads, state.ms, state.vs, state.m_scales, state.v_scales, state.copies)
+
+
 class AdamWTable:
     """An AdamWState and its gradients laid out on the device for adamw_step.
-    It names the tensors' memory and holds the tensors: a training loop that
-    keeps its gradient buffers builds it once (and before a graph is captured),
-    one whose gradients are new tensors every step builds one a step.  A
-    parameter's gradient and copy lie in memory in the order of its dimensions
+    It names the tensors' memory and holds the tensors and that memory: a
+    training loop that keeps its gradient buffers builds it once (and before a
+    graph is captured), one whose gradients are new tensors every step builds
+    one a step.  A step is refused once a tensor has other memory than the table
+    names (p.data replaced, a storage resized); a captured one does not look.
+    A parameter's gradient and copy lie in memory in the order of its dimensions
     (any row pitch each); tensors that a step writes share no memory with any
     other.  The state's tensors are checked anew for every table, since a
     parameter's memory may have changed with its module."""
@@ -301,6 +308,7 @@ class AdamWTable:
             if t.device != self.device or not here:
                 raise ValueError(f"expected tensors on the current GPU, got {t.device}")
         entries = _entries(state, self.grads)
+        self.held = _hold(state, self.grads)
         L = _fb.lib()
         self.n = len(entries)
         array = (_Tensor * max(self.n, 1))(*entries)
@@ -340,4 +348,4 @@ def adamw_step(table: AdamWTable, lr, step, beta1: float = 0.9, beta2: float = 0
     if stream is not None and stream != table._stream:  # the table's memory must outlive this stream's work too
         t.record_stream(torch.cuda.current_stream())
     _ext().adamw_step(t, table.n, table.chunks, table.state.state, lr, step, beta1, beta2, eps, norm, max_norm, clip_eps,
-                      seed, stream)
+                      seed, table.held, stream)

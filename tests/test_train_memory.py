@@ -198,3 +198,56 @@ def test_workspace_that_is_not_used():
     kw["workspace"] = kw["h"]
     with pytest.raises(ValueError, match="current GPU"):
         _forward(**kw, split_k=False)
+
+
+# --- a table whose tensors have other memory by now -----------------------------
+
+def _held(dtype=E4):
+    p, s = _state(dtype=dtype)
+    g = [torch.zeros(100)]
+    return p, s, g, train._hold(s, g)
+
+
+def _step(held):
+    """A step refused as one of CPU tensors, unless what it holds has moved."""
+    return train._ext().adamw_step(torch.zeros(64, dtype=torch.int64), 1, 1, 2, 1e-3, 1, 0.9, 0.95, 1e-8, None, None, 1e-6,
+                                   None, held, None)
+
+
+def test_step_after_memory_moved():
+    def set_data(t, n=100):
+        t.data = torch.zeros(n, dtype=t.dtype)
+
+    changes = {"parameter 0": lambda p, s, g: set_data(p), "gradient 0": lambda p, s, g: set_data(g[0]),
+               "first moment 0": lambda p, s, g: s.ms[0].untyped_storage().resize_(0),
+               "second moment 0": lambda p, s, g: s.vs[0].resize_(1 << 20),
+               "first moment's scales 0": lambda p, s, g: set_data(s.m_scales[0], 1),
+               "second moment's scales 0": lambda p, s, g: set_data(s.v_scales[0], 1),
+               "copy 0": lambda p, s, g: set_data(s.copies[0])}
+    for what, change in changes.items():
+        p, s, g, held = _held()
+        with pytest.raises(ValueError, match="current GPU"):
+            _step(held)
+        change(p, s, g)
+        with pytest.raises(ValueError, match=f"^{what} "):
+            _step(held)
+
+
+def test_table_keeps_its_memory():
+    """Lists that change after the table was built: it goes on with the tensors that it was built of."""
+    p, s, g, held = _held()
+    at, kept = s.ms[0].data_ptr(), [s.ms[0].data_ptr(), g[0].data_ptr()]
+    s.ms[0], g[0] = torch.ones(100, dtype=torch.uint8), torch.ones(100)
+    fresh = [torch.zeros(100, dtype=torch.uint8) for _ in range(64)] + [torch.zeros(100) for _ in range(64)]
+    assert not {t.data_ptr() for t in fresh} & set(kept) and at == kept[0]
+    with pytest.raises(ValueError, match="current GPU"):
+        _step(held)
+
+
+def test_written_clone_on_write():
+    """A tensor that shares its memory with a clone until either is written gets its own: the table is another one's."""
+    p, s, g, held = _held(torch.float32)
+    clone = torch._lazy_clone(s.ms[0])
+    with pytest.raises(ValueError, match="^first moment 0 "):
+        _step(held)
+    assert clone.numel() == 100
