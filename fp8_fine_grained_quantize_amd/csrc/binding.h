@@ -137,6 +137,17 @@ inline void own(std::initializer_list<const Tensor*> lent) {
     if (t != nullptr) t->mutable_data_ptr();
 }
 
+// A kernel wrote this tensor of the caller's: autograd refuses a graph that still
+// needs the old values, as after torch's own in-place operations.  (Tensors of
+// inference mode have no versions.)
+inline void wrote(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+inline void wrote(std::initializer_list<const Tensor*> lent) {
+  for (const Tensor* t : lent)
+    if (t != nullptr) wrote(*t);
+}
+
 inline Tensor vec(std::initializer_list<int64_t> shape, ScalarType dtype, const Tensor& like) {
   return at::empty(c10::IntArrayRef(shape), at::TensorOptions().dtype(dtype).device(like.device()));
 }

@@ -185,6 +185,7 @@ PyObject* gated_gemm(PyObject* const* a) {
        "gated_gemm_fp8_blockscaled");
   }
   unlocked.end();
+  wrote({ou, oh, oq, os});
   return tuple({&u, &h, &q, &s});
 }
 
@@ -228,6 +229,7 @@ PyObject* gated_gemm_backward(PyObject* const* a) {
        "gated_gemm_backward_fp8_blockscaled");
   }
   unlocked.end();
+  wrote({od, oh, oq, os});
   return tuple({&du, &h, &q, &s});
 }
 
@@ -401,6 +403,14 @@ void still_there(PyObject* held) {
   }
 }
 
+// A step has written what the table names, but for the gradients.
+void wrote_all(PyObject* held) {
+  const std::vector<Place>& places = places_of(held);
+  PyObject* kept = PyTuple_GET_ITEM(held, 0);
+  for (size_t i = 0; i < places.size(); ++i)
+    if (places[i].written) wrote(THPVariable_Unpack(PyTuple_GET_ITEM(kept, static_cast<Py_ssize_t>(i))));
+}
+
 // One value on the device that a captured step reads anew at every replay, or NULL.
 const Tensor* device_value(PyObject* o, ScalarType dtype, const char* what) {
   if (!THPVariable_Check(o)) return nullptr;
@@ -449,6 +459,7 @@ PyObject* adamw_step(PyObject* const* a) {
   Unlocked unlocked;
   ok(fp8blk_adamw_step(addr(table), n, chunks, state, &s, stream), "adamw_step");
   unlocked.end();
+  wrote_all(a[13]);
   Py_RETURN_NONE;
 }
 

@@ -86,8 +86,9 @@ def gated_gemm_fp8_blockscaled(A, sA, B, sB, act: str = "silu", opB: int = 0, po
     bf16 [M][2H] unless want_u is False, h bf16 [M][H], and with quantize (q uint8 [M][H], s float32
     [H/128][M]) = quantize_1x128(h, pow2); want_h=False then leaves h out.  H and K are multiples of 128.
     split_k: a product of few rows is split over the GPU, with a workspace allocated here unless given (which
-    no other work, a captured graph's neither, may use at the same time).  Outputs and the workspace share no memory
-    with each other or with inputs."""
+    no other work, a captured graph's neither, may use at the same time; one that is too small or not 16-byte
+    aligned leaves the call to one launch).  Outputs and the workspace share no memory with each other or with
+    inputs; a given output counts as modified in place."""
     return GatedGemm(*_ext().gated_gemm(None, A, sA, B, sB, _act(act), opB, pow2_scales, None, quantize, pow2, want_h,
                                         want_u, split_k, workspace, u, h, q, s, _stream(A)))
 
@@ -111,9 +112,9 @@ def gated_gemm_backward_fp8_blockscaled(A, sA, B, sB, u, act: str = "silu", opB:
     """Gradient of h = act(u[:, :H]) * u[:, H:] and of the down projection that reads it, in one GEMM: dh = A B
     with A the codes of the gradient of the projection's output [M][K] and B its weights, [H][K] as the
     forward stored them (OP_T) or [K][H] (OP_N).  Returns du bf16 [M][2H] (du may be u itself, which it
-    replaces; nothing else that is written shares memory with another argument), h bf16 [M][H] again for the
-    weights' gradient unless want_h is False, and with quantize (q uint8 [M][2H], s float32 [2H/128][M]) =
-    quantize_1x128(du, pow2); want_du=False then leaves du out."""
+    replaces; nothing else that is written shares memory with another argument; a given output counts as
+    modified in place), h bf16 [M][H] again for the weights' gradient unless want_h is False, and with quantize
+    (q uint8 [M][2H], s float32 [2H/128][M]) = quantize_1x128(du, pow2); want_du=False then leaves du out."""
     return GatedGemmGrad(*_ext().gated_gemm_backward(None, A, sA, B, sB, _act(act), opB, pow2_scales, None, u, quantize, pow2,
                                                      want_h, want_du, split_k, workspace, du, h, q, s, _stream(A)))
 
@@ -340,7 +341,9 @@ def adamw_step(table: AdamWTable, lr, step, beta1: float = 0.9, beta2: float = 0
     random by this integer, another one every step (None: to nearest).  lr, step
     and seed may be one-element tensors on the device (float32, int64, int64),
     which a captured step reads anew at every replay; the graph reads the table
-    too, which has to live as long as it is replayed."""
+    too, which has to live as long as it is replayed.  Parameters, copies and
+    moments count as modified in place: a graph that still needs the old values
+    refuses its backward (a replay does not count)."""
     if not isinstance(table, AdamWTable):
         raise TypeError("table must be an AdamWTable")
     t = table.device_table
