@@ -16,7 +16,8 @@ Forward, for the residual stream x:
 Backward, from the gradients of x' and n', the same in reverse; quantization
 passes gradients through.  Between the two, only u is kept of an expert's rows:
 the gradient of the down projection's input, the activation's gradient and h
-again are one call (grouped_gated_gemm_backward_fp8_blockscaled).
+from u are one call (grouped_gated_gemm_backward_fp8_blockscaled), which leaves
+the gradient in u's memory: a backward pass uses up what its forward kept.
 
 Update: AdamW with E4M3 moments on the FP32 norms and router and on the BF16
 expert weights (rounded at random), gradients clipped by their global norm as
@@ -124,7 +125,7 @@ def backward(b: Block, s: dict, dx_out: torch.Tensor, dn: torch.Tensor):
     g1 = fb.residual_norm_backward(r1.x, dx_out=dx_out, dn=dn, rstd_pre=r1.rstd_pre, w_pre=b.w_next, f=s["y"],
                                    rstd_post=r1.rstd_post, w_post=b.w_post, gate=b.gate, alpha=ALPHA)
     do, dweights = fb.moe_combine_backward(g1.df, s["o"], row_of, s["w"], drows_dtype=torch.bfloat16)
-    # down projection and activation: gradient of u (in its place) with its codes, and h again
+    # down projection and activation: gradient of u (in its place) with its codes, and h from u
     g = fb.grouped_gated_gemm_backward_fp8_blockscaled(off, *fb.quantize_1x128(do), b.q_down, b.s_down, s["u"],
                                                        quantize=True, du=s["u"])
     d_down = fb.grouped_wgrad_fp8_blockscaled(off, P, *fb.quantize_128x1_grouped(g.h, off),

@@ -50,8 +50,10 @@ __device__ __forceinline__ float act_slope(float g) {
   return GELU ? k * __builtin_fmaf(0.134145f * g, g, 1.0f) : 1.0f;
 }
 // 1 / (1 + e^-z) by the hardware's 2^x and reciprocal, one unit in the last place
-// each: with the products before them within (4 + 2 |z|) 2^-24 of itself (BF16
-// has 2^-8), and 0 where e^-z passes FP32's range, z < -88.
+// (2^-23) each.  e^-z is off by that and by 2^-24 |z| for each of the two
+// roundings before it, to which GELU's argument adds up to six; the sum and the
+// reciprocal add 3 x 2^-24: within ((1 - p) (8 |z| + 2) + 3) 2^-24 of itself in all
+// (BF16 has 2^-8), and 0 where e^-z passes FP32's range, z < -88.
 __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
@@ -694,7 +696,8 @@ struct GatedForm {
 // The form that takes least time by what the forms take per K group and round
 // over the compute units, in ns: fitted to 252 products (1 to 4096 rows, K 512
 // to 7168, H 512 to 2048, either direction) measured in every form on one box,
-// within 0.5 % of the best form on average.  Both sides, forward of K = 7168 and
+// within 0.5 % of the best form on average and 10 % at worst (as for 168 others, of
+// up to 30000 rows and H 4096).  Both sides, forward of K = 7168 and
 // H = 2048 in us: 16 rows 64 fused 50, 32 in 14 parts 11.5; 128 rows 64 fused
 // 51, 64 in 8 parts 16; 1024 rows 64 fused 57, 128 70, 64 in 2 parts 67; 2048
 // rows 128 fused 74, 256 100, 64 103; 4096 rows 256 fused 102, 128 139.
@@ -729,7 +732,11 @@ inline GatedForm gated_form(int64_t M, int64_t N, int64_t K, bool gradient, bool
 // 128 / 256 rows in us: mean 2 439 / - / 528 (gradient 240 / - / 298), 32 730 /
 // 724 / 809 (376 / 364 / 432), 96 977 / 902 / 942 (558 / 504 / 563), 192 1460 /
 // 1244 / 1204 (802 / 721 / 729), 256 1833 / 1528 / 1434 (1006 / 859 / 874), 384
-// 2569 / 2045 / 1879 (1397 / 1167 / 1090).
+// 2569 / 2045 / 1879 (1397 / 1167 / 1090).  The limits are those of that size.
+// 64 experts of 2048 x 2816 (2048 x 1408), 64 / 128 / 256 rows: mean 32 92 / 86 /
+// 100 (43 / 51 / 62), 96 121 / 109 / 120 (82 / 70 / 89), 128 140 / 133 / 145 (89 /
+// 97 / 109), 256 236 / 182 / 186 (151 / 136 / 162), 384 330 / 251 / 232 (211 / 190 /
+// 214): there the gradient's choice costs up to 13 % at means of 128 and 384.
 inline int expert_rows(int64_t G, int64_t M, bool gradient) {
   if (M <= (gradient ? 40 : 28) * G) return 64;
   return M <= (gradient ? 256 : 160) * G ? 128 : 256;

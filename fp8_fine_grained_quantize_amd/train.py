@@ -64,7 +64,7 @@ class GatedGemm(NamedTuple):
 
 
 class GatedGemmGrad(NamedTuple):
-    """du: gradient of u; (q, s): its 1x128 codes and scales; h: the forward's h again."""
+    """du: gradient of u; (q, s): its 1x128 codes and scales; h: act(gate) * up of the u given."""
     du: Optional[torch.Tensor]
     h: Optional[torch.Tensor]
     q: Optional[torch.Tensor]
@@ -113,7 +113,8 @@ def gated_gemm_backward_fp8_blockscaled(A, sA, B, sB, u, act: str = "silu", opB:
     with A the codes of the gradient of the projection's output [M][K] and B its weights, [H][K] as the
     forward stored them (OP_T) or [K][H] (OP_N).  Returns du bf16 [M][2H] (du may be u itself, which it
     replaces; nothing else that is written shares memory with another argument; a given output counts as
-    modified in place), h bf16 [M][H] again for the weights' gradient unless want_h is False, and with quantize
+    modified in place), h bf16 [M][H] for the weights' gradient unless want_h is False (from the u given, in BF16;
+    the forward's h is from FP32 products, so that the two lie apart by u's rounding), and with quantize
     (q uint8 [M][2H], s float32 [2H/128][M]) = quantize_1x128(du, pow2); want_du=False then leaves du out."""
     return GatedGemmGrad(*_ext().gated_gemm_backward(None, A, sA, B, sB, _act(act), opB, pow2_scales, None, u, quantize, pow2,
                                                      want_h, want_du, split_k, workspace, du, h, q, s, _stream(A)))

@@ -92,7 +92,9 @@ fp8blk_status_t fp8blk_grouped_gated_gemm_fp8_blockscaled(
  *      with FP8BLK_OP_N) or [K][H] (FP8BLK_OP_N), block scales.
  *   u  [M][2H] BF16 that the forward kept.
  *   du [M][2H] BF16, pitch lddu, or NULL; it may be u itself (same pitch).
- *   h  [M][H] BF16, h again for the down projection's weight gradient, or NULL.
+ *   h  [M][H] BF16, act(u_g) u_u for the down projection's weight gradient, or
+ *      NULL.  It is formed from u as given, the forward's h from the FP32
+ *      products: the two lie apart by what u's rounding to BF16 makes of h.
  *   q  [M][2H] codes of du, what the up projection's gradients read, with
  *      s [2H/128][M], or both NULL.  At least one of du and q is given.
  */
@@ -171,6 +173,7 @@ fp8blk_status_t fp8blk_adamw_table_build(const fp8blk_adamw_t* list, int64_t n, 
  *   i = place, k = (seed + index * 0x27D4EB2F) mod 2^32
  *   h = (i * 0x9E3779B1 xor i >> 32) + k;  h = (h xor h >> 16) * 0x85EBCA6B;
  *   h = (h xor h >> 13) * 0xC2B2AE35;  r = h xor h >> 16          (all mod 2^32)
+ * (the last two lines are the 32-bit finalizer of MurmurHash3, a published one).
  * m takes the low half of r, v the high half, a BF16 param the low half of
  * the r of k xor 0x5BD1E995: 16 bits, added below the kept ones (16 dropped
  * ones of BF16, 20 of E4M3, the upper 16 of those) before they are dropped.
