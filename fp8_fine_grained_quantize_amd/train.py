@@ -310,17 +310,18 @@ class AdamWTable:
             if t.device != self.device or not here:
                 raise ValueError(f"expected tensors on the current GPU, got {t.device}")
         entries = _entries(state, self.grads)
+        self.kind = state.state  # the table's layout, whatever becomes of the state
         self.held = _hold(state, self.grads)
         L = _fb.lib()
         self.n = len(entries)
         array = (_Tensor * max(self.n, 1))(*entries)
-        shared = _shared(array, self.n, state.state)
+        shared = _shared(array, self.n, self.kind)
         if shared is not None:
             raise ValueError(f"{shared} share memory that the step would write")
         nbytes = L.fp8blk_adamw_table_bytes(self.n)
         host = torch.empty(nbytes // 8, dtype=torch.int64)
         chunks = _i64(0)
-        _fb._check(L.fp8blk_adamw_table_build(ctypes.cast(array, _vp), self.n, state.state, host.data_ptr(), nbytes,
+        _fb._check(L.fp8blk_adamw_table_build(ctypes.cast(array, _vp), self.n, self.kind, host.data_ptr(), nbytes,
                                               ctypes.cast(ctypes.pointer(chunks), _vp)), "adamw_table")
         self.chunks = chunks.value
         self.device_table = host.to(self.device)
@@ -351,5 +352,5 @@ def adamw_step(table: AdamWTable, lr, step, beta1: float = 0.9, beta2: float = 0
     stream = _stream(t)
     if stream is not None and stream != table._stream:  # the table's memory must outlive this stream's work too
         t.record_stream(torch.cuda.current_stream())
-    _ext().adamw_step(t, table.n, table.chunks, table.state.state, lr, step, beta1, beta2, eps, norm, max_norm, clip_eps,
+    _ext().adamw_step(t, table.n, table.chunks, table.kind, lr, step, beta1, beta2, eps, norm, max_norm, clip_eps,
                       seed, table.held, stream)

@@ -145,3 +145,14 @@ def test_table_of_moved_memory():
     s.ms[0] = torch.zeros_like(kept)  # the table goes on with the tensors that it was built of
     fb.adamw_step(t, 0.5, 1)
     assert kept.any() and not s.ms[0].any()
+
+
+def test_table_of_a_state_that_holds_other_moments_now():
+    """A step goes by the moments that its table was built of."""
+    p, g = torch.zeros(300, device="cuda"), torch.ones(300, device="cuda")
+    s = fb.AdamWState([p])
+    t = fb.adamw_table(s, [g])
+    old = s.ms[0]
+    s.__init__([p], dtype=E4)
+    fb.adamw_step(t, 0.5, 1, eps=0.0)
+    assert (p == -0.5).all() and old.all() and not s.ms[0].any()
